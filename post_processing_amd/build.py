@@ -18,7 +18,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libws.so")
 SOURCES = ["ws_preprocess.hip", "ws_topk.hip", "ws_detect.hip", "ws_runtime.hip",
-           "ws_noalloc.hip"]
+           "ws_noalloc.hip", "ws_logits.hip"]
 ARCH = "gfx950"
 
 
@@ -65,11 +65,11 @@ def build_lib(verbose: bool = False, marks: bool = False) -> str:
     return lib
 
 
-def build_host_test(out: str, sanitize: bool = False) -> str:
-    """g++ build of the planning code's host-only test driver (no HIP);
+def build_host_test(out: str, sanitize: bool = False, driver: str = "ws_plan_test") -> str:
+    """g++ build of a host-only test driver of the planning code (no HIP);
     with `sanitize`, instrumented by AddressSanitizer and
     UndefinedBehaviorSanitizer, any report aborting the run."""
-    src = os.path.join(ROOT, "tests", "host", "ws_plan_test.cpp")
+    src = os.path.join(ROOT, "tests", "host", driver + ".cpp")
     cmd = ["g++", "-std=c++17", "-O1", "-Wall", "-Werror", "-I", INCLUDE, "-I", CSRC]
     if sanitize:
         cmd += ["-g", "-fno-omit-frame-pointer", "-fsanitize=address,undefined",

@@ -1,0 +1,152 @@
+// ws_logits_plan.h -- host-side checks and launch geometry of the operators
+// over rows of logits (ws_logits.h).
+//
+// Plain C++17 with no HIP dependency, so the same code the library runs can
+// be compiled and tested on a host without a GPU.
+#pragma once
+
+#include <cmath>
+#include <cstddef>
+#include <cstdint>
+
+#include "ws_logits.h"
+
+namespace ws {
+
+inline int64_t logit_bytes(int32_t dtype) { return dtype == WS_DTYPE_F32 ? 4 : 2; }
+
+inline bool aligned_to(const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+
+inline int validate_rows(const ws_rows* r) {
+    if (!r) return WS_E_INVALID_ARG;
+    if (r->device < 0) return WS_E_INVALID_ARG;
+    if (r->dtype != WS_DTYPE_F32 && r->dtype != WS_DTYPE_F16 && r->dtype != WS_DTYPE_BF16)
+        return WS_E_INVALID_ARG;
+    if (r->rows < 0 || r->rows > WS_MAX_ROWS) return WS_E_INVALID_ARG;
+    if (r->vocab < 1 || r->vocab > WS_MAX_SCORES) return WS_E_INVALID_ARG;
+    if (r->row_stride < r->vocab || r->row_stride > WS_MAX_ROW_STRIDE) return WS_E_INVALID_ARG;
+    if (!(r->temperature >= WS_MIN_TEMPERATURE && r->temperature <= WS_MAX_TEMPERATURE))
+        return WS_E_INVALID_ARG;
+    if (r->reserved != 0) return WS_E_INVALID_ARG;
+    return WS_OK;
+}
+
+// Bytes from the first to one past the last element of a matrix of rows.
+inline int64_t rows_extent(const ws_rows& r, int64_t stride) {
+    if (r.rows == 0) return 0;
+    return ((int64_t)(r.rows - 1) * stride + r.vocab) * logit_bytes(r.dtype);
+}
+
+// The gradient's matrix: the logits themselves, or apart from them.
+inline int validate_gradient(const ws_rows& r, const void* logits, const void* grad,
+                             int64_t stride) {
+    if (stride < r.vocab || stride > WS_MAX_ROW_STRIDE) return WS_E_INVALID_ARG;
+    if (r.rows == 0) return WS_OK;
+    if (!grad || !aligned_to(grad, (uintptr_t)logit_bytes(r.dtype))) return WS_E_INVALID_ARG;
+    if (grad == logits)
+        return stride == r.row_stride || r.rows == 1 ? WS_OK : WS_E_INVALID_ARG;
+    const uintptr_t a = (uintptr_t)logits, b = (uintptr_t)grad;
+    const uintptr_t an = (uintptr_t)rows_extent(r, r.row_stride);
+    const uintptr_t bn = (uintptr_t)rows_extent(r, stride);
+    if (a < b ? b - a < an : a - b < bn) return WS_E_INVALID_ARG;
+    return WS_OK;
+}
+
+inline bool logits_ok(const ws_rows& r, const void* logits) {
+    return logits && aligned_to(logits, (uintptr_t)logit_bytes(r.dtype));
+}
+
+// Two arrays that come together or not at all; where they come, both aligned.
+inline bool paired(const void* a, const void* b, uintptr_t align_a, uintptr_t align_b) {
+    return (a != nullptr) == (b != nullptr) && aligned_to(a, align_a) && aligned_to(b, align_b);
+}
+
+inline int validate_top_k(const ws_rows& r, int32_t top_k) {
+    const int32_t most = r.vocab < WS_MAX_K ? r.vocab : WS_MAX_K;
+    return top_k >= 0 && top_k <= most ? WS_OK : WS_E_INVALID_ARG;
+}
+
+inline int validate_logprobs(const ws_rows* r, const ws_logprobs_args* a) {
+    const int v = validate_rows(r);
+    if (v != WS_OK) return v;
+    if (!a || a->reserved != 0) return WS_E_INVALID_ARG;
+    if (validate_top_k(*r, a->top_k) != WS_OK) return WS_E_INVALID_ARG;
+    if (r->rows == 0) return WS_OK;
+    if (!logits_ok(*r, a->logits)) return WS_E_INVALID_ARG;
+    if (!paired(a->targets, a->logprob, 4, 4)) return WS_E_INVALID_ARG;
+    if ((a->top != nullptr) != (a->top_k > 0)) return WS_E_INVALID_ARG;
+    if (!aligned_to(a->entropy, 4) || !aligned_to(a->top, 8) || !aligned_to(a->stats, 8))
+        return WS_E_INVALID_ARG;
+    return WS_OK;
+}
+
+inline int validate_logprobs_grad(const ws_rows* r, const ws_logprobs_grad_args* a) {
+    const int v = validate_rows(r);
+    if (v != WS_OK) return v;
+    if (!a || a->reserved != 0) return WS_E_INVALID_ARG;
+    if (a->top_k < 0 || a->top_k > WS_MAX_K) return WS_E_INVALID_ARG;
+    if (r->rows > 0) {
+        if (!logits_ok(*r, a->logits)) return WS_E_INVALID_ARG;
+        if (!a->stats || !aligned_to(a->stats, 8)) return WS_E_INVALID_ARG;
+        if (!paired(a->targets, a->grad_logprob, 4, 4)) return WS_E_INVALID_ARG;
+        if (!paired(a->entropy, a->grad_entropy, 4, 4)) return WS_E_INVALID_ARG;
+        if (!paired(a->top, a->grad_top, 8, 4)) return WS_E_INVALID_ARG;
+        if ((a->top != nullptr) != (a->top_k > 0)) return WS_E_INVALID_ARG;
+    }
+    return validate_gradient(*r, a->logits, a->grad_logits, a->grad_stride);
+}
+
+inline int validate_teacher(int32_t teacher_k, int32_t mode) {
+    if (teacher_k < 1 || teacher_k > WS_DISTILL_MAX_K) return WS_E_INVALID_ARG;
+    return mode == WS_DISTILL_RENORM || mode == WS_DISTILL_TAIL ? WS_OK : WS_E_INVALID_ARG;
+}
+
+inline int validate_distill(const ws_rows* r, const ws_distill_args* a) {
+    const int v = validate_rows(r);
+    if (v != WS_OK) return v;
+    if (!a || a->reserved[0] != 0 || a->reserved[1] != 0) return WS_E_INVALID_ARG;
+    if (validate_teacher(a->teacher_k, a->mode) != WS_OK) return WS_E_INVALID_ARG;
+    if (a->tail && a->mode != WS_DISTILL_TAIL) return WS_E_INVALID_ARG;
+    if (r->rows == 0) return WS_OK;
+    if (!logits_ok(*r, a->logits)) return WS_E_INVALID_ARG;
+    if (!a->teacher || !aligned_to(a->teacher, 8)) return WS_E_INVALID_ARG;
+    if (!a->loss || !aligned_to(a->loss, 4)) return WS_E_INVALID_ARG;
+    if (!aligned_to(a->stats, 8) || !aligned_to(a->tail, 4)) return WS_E_INVALID_ARG;
+    if (!paired(a->grad_logits, a->grad_loss, 1, 4)) return WS_E_INVALID_ARG;
+    if (!a->grad_logits) return WS_OK;
+    return validate_gradient(*r, a->logits, a->grad_logits, a->grad_stride);
+}
+
+inline int validate_distill_grad(const ws_rows* r, const ws_distill_grad_args* a) {
+    const int v = validate_rows(r);
+    if (v != WS_OK) return v;
+    if (!a || validate_teacher(a->teacher_k, a->mode) != WS_OK) return WS_E_INVALID_ARG;
+    if (r->rows > 0) {
+        if (!logits_ok(*r, a->logits)) return WS_E_INVALID_ARG;
+        if (!a->teacher || !aligned_to(a->teacher, 8)) return WS_E_INVALID_ARG;
+        if (!a->stats || !aligned_to(a->stats, 8)) return WS_E_INVALID_ARG;
+        if ((a->tail != nullptr) != (a->mode == WS_DISTILL_TAIL)) return WS_E_INVALID_ARG;
+        if (!aligned_to(a->tail, 4)) return WS_E_INVALID_ARG;
+        if (!a->grad_loss || !aligned_to(a->grad_loss, 4)) return WS_E_INVALID_ARG;
+    }
+    return validate_gradient(*r, a->logits, a->grad_logits, a->grad_stride);
+}
+
+inline int validate_workspace(const void* workspace, size_t given, size_t needed) {
+    if (needed == 0) return WS_OK;
+    if (!workspace || !aligned_to(workspace, 16) || given < needed) return WS_E_INVALID_ARG;
+    return WS_OK;
+}
+
+// ---------------------------------------------------------------------------
+// Workspaces.
+
+// ws_distill with a gradient runs the loss kernel, then the gradient kernel
+// from the row statistics and tails it left here.
+inline size_t distill_workspace_bytes(const ws_rows& r, int32_t mode, bool gradient) {
+    if (!gradient) return 0;
+    (void)mode;
+    return (size_t)r.rows * (sizeof(ws_row_stats) + sizeof(float));
+}
+
+}  // namespace ws
