@@ -1,6 +1,5 @@
 // ws_logits.hip -- the operators over rows of logits (ws_logits.h), written
-// for gfx950 (CDNA4, wave64): one workgroup a row.
-#include <hip/hip_fp16.h>
+// for gfx950 (CDNA4, wave64).
 #include <hip/hip_runtime.h>
 
 #include <cfloat>
@@ -9,67 +8,20 @@
 #include "ws_lanes.h"
 #include "ws_logits.h"
 #include "ws_logits_plan.h"
+#include "ws_logits_rows.h"
 
 namespace ws {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr float kLog2e = 1.44269504088896340736f;
-// A finite stand-in below every difference z - max that matters: at the
-// highest temperature exp((z - max) / tau) is 0 from -1.04e5 on, and 0 times a
-// finite number is 0 where 0 times -inf would be NaN.
-constexpr float kFar = -1.0e6f;
 
-struct F32 {
-    using type = float;
-    static __device__ __forceinline__ float load(const void* p, int64_t i) {
-        return static_cast<const float*>(p)[i];
-    }
-    static __device__ __forceinline__ void store(void* p, int64_t i, float v) {
-        static_cast<float*>(p)[i] = v;
-    }
-};
-
-struct F16 {
-    using type = uint16_t;
-    static __device__ __forceinline__ float load(const void* p, int64_t i) {
-        return (float)static_cast<const _Float16*>(p)[i];
-    }
-    static __device__ __forceinline__ void store(void* p, int64_t i, float v) {
-        static_cast<_Float16*>(p)[i] = (_Float16)v;
-    }
-};
-
-// Round to nearest even; a NaN stays one.
-__device__ __forceinline__ uint16_t bf16_bits(float v) {
-    const uint32_t u = __float_as_uint(v);
-    if ((u & 0x7fffffffu) > 0x7f800000u) return (uint16_t)((u >> 16) | 0x40u);
-    return (uint16_t)((u + 0x7fffu + ((u >> 16) & 1u)) >> 16);
+template <typename L>
+__device__ __forceinline__ float lload(const void* p, int64_t i) {
+    return L::up(static_cast<const typename L::Elem*>(p)[i]);
 }
-
-struct BF16 {
-    using type = uint16_t;
-    static __device__ __forceinline__ float load(const void* p, int64_t i) {
-        return __uint_as_float((uint32_t) static_cast<const uint16_t*>(p)[i] << 16);
-    }
-    static __device__ __forceinline__ void store(void* p, int64_t i, float v) {
-        static_cast<uint16_t*>(p)[i] = bf16_bits(v);
-    }
-};
-
-// Order-preserving unsigned image of an FP32 value: NaN -> -inf and -0 -> +0
-// first, then larger values have larger images.
-__device__ __forceinline__ uint32_t order_image(float v) {
-    uint32_t b = __float_as_uint(v);
-    b = (b & 0x7fffffffu) > 0x7f800000u ? 0xff800000u : b;
-    b = b == 0x80000000u ? 0u : b;
-    return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
-}
-
-// (value descending, index ascending) as one integer, larger = better; 0 is
-// below every key.
-__device__ __forceinline__ uint64_t order_key(float v, uint32_t index) {
-    return ((uint64_t)order_image(v) << 32) | (uint32_t)~index;
+template <typename L>
+__device__ __forceinline__ void lstore(void* p, int64_t i, float v) {
+    static_cast<typename L::Elem*>(p)[i] = L::down(v);
 }
 
 template <typename T, typename Op>
@@ -112,9 +64,6 @@ struct AddF {
 struct MaxF {
     __device__ float operator()(float a, float b) const { return fmaxf(a, b); }
 };
-struct MaxKey {
-    __device__ uint64_t operator()(uint64_t a, uint64_t b) const { return umax64(a, b); }
-};
 
 __device__ __forceinline__ bool listed(const uint32_t* ids, int k, uint32_t j) {
     for (int i = 0; i < k; ++i)
@@ -122,24 +71,17 @@ __device__ __forceinline__ bool listed(const uint32_t* ids, int k, uint32_t j) {
     return false;
 }
 
-// Row sums with respect to the row's maximum m (-FLT_MAX or more, so that a
-// difference from it is never inf - inf in a row without +inf):
-//   s = sum e_j, u = sum e_j (z_j - m), e_j = 2^((z_j - m) c), c = log2(e) / tau.
-struct Sums {
-    float m, s, u;
-};
-
 template <typename L>
 __device__ Sums row_sums(const void* logits, int64_t at, int V, float c, const uint32_t* ids,
                          int k, float* scratch) {
     float m = -FLT_MAX;
     for (int j = threadIdx.x; j < V; j += kThreads)
-        if (!listed(ids, k, j)) m = fmaxf(m, L::load(logits, at + j));
+        if (!listed(ids, k, j)) m = fmaxf(m, lload<L>(logits, at + j));
     m = group_reduce(m, scratch, MaxF());
     float s = 0.0f, u = 0.0f;
     for (int j = threadIdx.x; j < V; j += kThreads) {
         if (listed(ids, k, j)) continue;
-        const float d = L::load(logits, at + j) - m;
+        const float d = lload<L>(logits, at + j) - m;
         const float e = __builtin_amdgcn_exp2f(d * c);
         s += e;
         u += e * fmaxf(d, kFar);
@@ -151,6 +93,157 @@ __device__ Sums row_sums(const void* logits, int64_t at, int V, float c, const u
     return r;
 }
 
+// ---------------------------------------------------------------------------
+// Forward: one pass over the row.
+//
+// Each thread keeps running sums of its own slots against its own running
+// maximum (raised once per batch of slots), joined across lanes, waves and, for
+// a row split over several workgroups, parts.
+//
+// Best K: a thread also keeps its best slot (largest slot maximum, the first
+// one) and the second largest slot maximum.  The K-th largest of the threads'
+// best values is a lower bound t on the row's K-th best: K threads reach it, so
+// every element of the best K lies at or above t in one of those threads' slots
+// - in its best slot, or, only if its second largest slot maximum reaches t as
+// well, in any of its slots.  So after the pass about K slots are read again
+// instead of a selection running inside the pass.
+
+// A row's best keys as they are collected, in LDS.
+template <typename L, int NT>
+struct Best {
+    static constexpr int kScan = NT < 128 ? NT : 128;   // threads that read slots again
+    static constexpr int kRoom = kScan * L::VEC + WS_MAX_K;
+    static constexpr int kListed = 64;
+    uint64_t keys[kRoom];
+    uint64_t sorted[WS_MAX_K];
+    uint32_t tops[NT / 64 * 32];   // each wave's 32 largest thread bests, descending
+    int single[kListed];           // slots to read again
+    int thread[kListed];           // threads all of whose slots are read again
+    int above, picked, singles, threads, count;
+};
+
+// K-th largest over the workgroup of one value a thread (K <= 32); every
+// thread gets it.  The caller has synchronised since `tops` was last read.
+template <int NT>
+__device__ __forceinline__ uint32_t group_kth_largest(uint32_t v, int k, uint32_t* tops) {
+    const int lane = threadIdx.x & 63;
+    v = wave_sort<true>(v, lane);
+    if constexpr (NT > 64) {
+        static_assert(NT == 256, "one or four waves");
+        const int wave = threadIdx.x >> 6;
+        if (lane < 32) tops[wave * 32 + lane] = v;
+        __syncthreads();
+        // Lists 0 and 2 in the lower half of the lanes, 1 and 3 in the upper:
+        // the larger of one list and the other reversed are the 32 largest of
+        // both, a bitonic sequence; sorted, the halves meet the same way.
+        const int half = lane & 32, i = lane & 31;
+        const uint32_t a = tops[half + i], b = tops[64 + half + 31 - i];
+        v = bitonic_stages<64, 16, true>(a > b ? a : b, lane);
+        const uint32_t w = (uint32_t)__builtin_amdgcn_ds_bpermute((lane ^ 63) * 4, (int)v);
+        v = bitonic_stages<64, 16, true>(v > w ? v : w, lane);
+    }
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, k - 1);
+}
+
+// Keeps the K best of the collected keys, in order, at the list's start.
+template <typename L, int NT>
+__device__ __forceinline__ int keep_best(Best<L, NT>& b, int k) {
+    const int n = b.count;
+    for (int i = threadIdx.x; i < n; i += NT) {
+        const uint64_t x = b.keys[i];
+        const int r = keys_above(b.keys, n, x);
+        if (r < k) b.sorted[r] = x;
+    }
+    __syncthreads();
+    const int kept = n < k ? n : k;
+    if ((int)threadIdx.x < kept) b.keys[threadIdx.x] = b.sorted[threadIdx.x];
+    if (threadIdx.x == 0) b.count = kept;
+    __syncthreads();
+    return kept;
+}
+
+// What a thread remembers of its slots for the best K.
+struct SlotTrack {
+    float best, second;   // largest and second largest slot maximum
+    int slot;             // first slot of the largest
+};
+
+// The K best keys of a part of a row into b.sorted; returns how many there are
+// (K, or the part's elements if fewer).  all: read every slot again (a row
+// with a NaN, which the running maxima skip).
+template <typename L, int NT>
+__device__ __forceinline__ int select_best(const Part<L>& part, SlotTrack t, bool all, int k,
+                                           Best<L, NT>& b) {
+    const int tid = threadIdx.x;
+    const bool has = tid < part.n;
+    const uint32_t best = has ? value_image(t.best) : 0;
+    const uint32_t second = value_image(t.second);
+    if (tid == 0) b.above = b.picked = b.singles = b.threads = b.count = 0;
+    uint32_t bound = group_kth_largest<NT>(best, k, b.tops);
+    __syncthreads();
+    // Threads at the bound may be more than K when their bests are equal.
+    if (has && best >= bound) {
+        atomicAdd(&b.picked, 1);
+        if (best > bound) atomicAdd(&b.above, 1);
+    }
+    __syncthreads();
+    int last = 0x7fffffff;   // of the threads at the bound, those whose slot is not beyond
+    if (b.picked > Best<L, NT>::kListed) {
+        const int above = b.above;
+        const uint32_t early =
+            group_kth_largest<NT>(has && best == bound ? ~(uint32_t)t.slot : 0u, k - above, b.tops);
+        last = (int)~early;
+        __syncthreads();
+    }
+    const int rounds_per_thread = (part.n + NT - 1) / NT;
+    if (has && !all && (best > bound || (best == bound && t.slot <= last))) {
+        // A second slot at the bound counts only if it is not beyond `last`; it
+        // comes at least NT slots after the first when both are at the bound.
+        const bool more = second > bound ||
+                          (second == bound && (best > bound || (int64_t)t.slot + NT <= last));
+        if (more) b.thread[atomicAdd(&b.threads, 1)] = tid;
+        else b.single[atomicAdd(&b.singles, 1)] = t.slot;
+    }
+    __syncthreads();
+    const uint32_t edge = last == 0x7fffffff ? 0xffffffffu
+                                             : (uint32_t)(part.e0 + last * L::VEC + L::VEC - 1);
+    uint64_t least = all ? 0 : ((uint64_t)bound << 32) | (uint32_t)~edge;
+    const int singles = b.singles;
+    const int items = all ? part.n : singles + b.threads * rounds_per_thread;
+    for (int from = 0;; from += Best<L, NT>::kScan) {
+        const int item = from + tid;
+        if (tid < Best<L, NT>::kScan && item < items) {
+            int slot = item;
+            if (!all) {
+                if (item < singles) {
+                    slot = b.single[item];
+                } else {
+                    const int j = item - singles;
+                    slot = b.thread[j / rounds_per_thread] + (j % rounds_per_thread) * NT;
+                }
+            }
+            if (slot < part.n) {
+                float v[L::VEC];
+                part.load_any(slot, v);
+#pragma unroll
+                for (int j = 0; j < L::VEC; ++j) {
+                    const int e = part.e0 + slot * L::VEC + j;
+                    const uint64_t key = value_key(v[j], (uint32_t)e);
+                    if (key >= least && e >= 0 && e < part.vocab)
+                        b.keys[atomicAdd(&b.count, 1)] = key;
+                }
+            }
+        }
+        __syncthreads();
+        const bool more = from + Best<L, NT>::kScan < items;
+        if (!more || b.count > WS_MAX_K) {
+            const int kept = keep_best(b, k);
+            if (!more) return kept;
+            if (kept == k) least = umax64(least, b.sorted[k - 1]);
+        }
+    }
+}
+
 struct LogprobsParams {
     const void* logits;
     int64_t stride;
@@ -159,49 +252,203 @@ struct LogprobsParams {
     float* entropy;
     ws_topk_entry* top;
     ws_row_stats* stats;
+    Sums* sums;         // [rows][parts], when a row has several parts
+    uint64_t* keys;     // [rows][parts][k]
     int32_t vocab;
     int32_t k;
-    float c;         // log2(e) / tau
+    int32_t chunk;      // slots of a part
+    int32_t parts;
+    float c;            // log2(e) / tau
     float inv_tau;
 };
 
+// Row outputs from its sums; `sorted` holds its best keys.  Called by every
+// thread of a workgroup.
 template <typename L>
-__global__ void __launch_bounds__(kThreads) logprobs_kernel(LogprobsParams p) {
-    __shared__ float scratch[kThreads / 64];
-    __shared__ uint64_t keys[kThreads / 64];
-    const int64_t row = blockIdx.x;
-    const int64_t at = row * p.stride;
-    const Sums r = row_sums<L>(p.logits, at, p.vocab, p.c, nullptr, 0, scratch);
-    const bool empty = r.s == 0.0f;
-    const float logsum = empty ? -INFINITY : logf(r.s);
+__device__ __forceinline__ void write_logprobs(const LogprobsParams& p, int64_t row, Sums t,
+                                               const uint64_t* sorted) {
+    const bool empty = t.s == 0.0f;
+    const float logsum = empty ? -INFINITY : logf(t.s);
     if (threadIdx.x == 0) {
-        if (p.stats) p.stats[row] = {empty ? -INFINITY : r.m, logsum};
-        if (p.entropy) p.entropy[row] = empty ? 0.0f : logsum - r.u * p.inv_tau / r.s;
+        if (p.stats) p.stats[row] = {empty ? -INFINITY : t.m, logsum};
+        if (p.entropy) p.entropy[row] = empty ? 0.0f : logsum - t.u * p.inv_tau / t.s;
         if (p.logprob) {
-            const int32_t t = p.targets[row];
+            const int32_t j = p.targets[row];
             float v = 0.0f;
-            if (t >= 0 && t < p.vocab)
-                v = empty ? -INFINITY : (L::load(p.logits, at + t) - r.m) * p.inv_tau - logsum;
-            else if (t != -1)
+            if (j >= 0 && j < p.vocab) {
+                const float z =
+                    L::up(static_cast<const typename L::Elem*>(p.logits)[row * p.stride + j]);
+                v = empty ? -INFINITY : (z - t.m) * p.inv_tau - logsum;
+            } else if (j != -1) {
                 v = NAN;
+            }
             p.logprob[row] = v;
         }
     }
-    uint64_t bound = ~0ull;
-    for (int i = 0; i < p.k; ++i) {
-        uint64_t best = 0;
-        for (int j = threadIdx.x; j < p.vocab; j += kThreads) {
-            const uint64_t key = order_key(L::load(p.logits, at + j), (uint32_t)j);
-            if (key < bound) best = umax64(best, key);
+    if ((int)threadIdx.x < p.k) {
+        const uint64_t key = sorted[threadIdx.x];
+        const float z = image_value((uint32_t)(key >> 32));
+        ws_topk_entry e;
+        e.score = empty ? -INFINITY : (z - t.m) * p.inv_tau - logsum;
+        e.index = (int32_t)~(uint32_t)key;
+        p.top[row * p.k + threadIdx.x] = e;
+    }
+}
+
+constexpr int kBatch = 4;   // slots a thread has in flight
+
+struct Nothing {
+    static constexpr uint64_t* sorted = nullptr;
+};
+template <bool ON, typename T>
+struct Select {
+    using Type = T;
+};
+template <typename T>
+struct Select<false, T> {
+    using Type = Nothing;
+};
+
+template <typename L, int NT, bool ENT, bool TOPK>
+__global__ void __launch_bounds__(NT) logprobs_kernel(LogprobsParams p) {
+    constexpr int VEC = L::VEC;
+    __shared__ Sums wave_sums[NT / 64];
+    __shared__ typename Select<TOPK, Best<L, NT>>::Type best;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int64_t row = blockIdx.x / (uint32_t)p.parts;
+    const int index = (int)(blockIdx.x % (uint32_t)p.parts);
+    Part<L> part;
+    part.init(p.logits, row * p.stride, p.vocab, p.chunk, p.parts, index);
+
+    Sums a;
+    a.init();
+    SlotTrack t{-INFINITY, -INFINITY, tid};
+    // The running sums over U slots of values, the first at `slot`, NT apart.
+    const auto take = [&](auto& v, int slot) {
+        constexpr int U = sizeof(v) / sizeof(v[0]);
+        float top = a.m;
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            float m = fmaxf(v[i][0], v[i][1]);
+#pragma unroll
+            for (int j = 2; j < VEC; ++j) m = fmaxf(m, v[i][j]);
+            top = fmaxf(top, m);
+            if constexpr (TOPK) {
+                t.second = __builtin_amdgcn_fmed3f(m, t.best, t.second);
+                t.slot = m > t.best ? slot + i * NT : t.slot;
+                t.best = fmaxf(t.best, m);
+            }
         }
-        bound = group_reduce(best, keys, MaxKey());
-        if (threadIdx.x == 0) {
-            const int32_t j = (int32_t)~(uint32_t)bound;
-            const float v =
-                empty ? -INFINITY : (L::load(p.logits, at + j) - r.m) * p.inv_tau - logsum;
-            p.top[row * p.k + i] = {v, j};
+        a.raise<ENT>(top, p.c);
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                const float d = v[i][j] - a.m;
+                const float e = __builtin_amdgcn_exp2f(d * p.c);
+                a.s += e;
+                if constexpr (ENT) a.u = fmaf(e, fmaxf(d, kFar), a.u);
+            }
+    };
+    int s = tid;
+    if (s < part.full_from) {   // the slot that sticks out in front
+        float v[1][VEC];
+        part.load_edge(s, v[0]);
+        take(v, s);
+        s += NT;
+    }
+    for (; s < part.full_to; s += kBatch * NT) {
+        float v[kBatch][VEC];
+        uint4 w[kBatch];
+        if (s + (kBatch - 1) * NT < part.full_to) {
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) w[i] = part.load(s + i * NT);
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) L::unpack(w[i], v[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+                if (s + i * NT < part.full_to) w[i] = part.load(s + i * NT);
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                if (s + i * NT < part.full_to) {
+                    L::unpack(w[i], v[i]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) v[i][j] = -INFINITY;
+                }
+            }
+        }
+        take(v, s);
+    }
+    // The slot that sticks out behind belongs to the thread next in turn.
+    const int tail = part.full_to > part.full_from ? part.full_to : part.full_from;
+    if (tail < part.n && tail % NT == tid) {
+        float v[1][VEC];
+        part.load_edge(tail, v[0]);
+        take(v, tail);
+    }
+
+    a = wave_join<ENT>(a, p.c, lane);
+    if constexpr (NT > 64) {
+        if (lane == 0) wave_sums[tid >> 6] = a;
+        __syncthreads();
+        a = join_in_order<ENT>(wave_sums, NT / 64, p.c);
+    }
+    int kept = 0;
+    if constexpr (TOPK) {
+        kept = select_best<L, NT>(part, t, a.s != a.s, p.k, best);
+    }
+    if (p.parts == 1) {
+        write_logprobs<L>(p, row, a, best.sorted);
+    } else {
+        if (tid == 0) p.sums[blockIdx.x] = a;
+        if constexpr (TOPK) {
+            if (tid < p.k)
+                p.keys[(int64_t)blockIdx.x * p.k + tid] = tid < kept ? best.sorted[tid] : 0;
         }
     }
+}
+
+// Joins the parts of a row (at most 64): one wave a row.
+
+
+template <typename L, bool ENT>
+__global__ void __launch_bounds__(64) logprobs_join_kernel(LogprobsParams p) {
+    __shared__ uint64_t keys[WS_MAX_K * WS_MAX_K + WS_MAX_K];
+    __shared__ uint64_t sorted[WS_MAX_K];
+    const int lane = threadIdx.x;
+    const int64_t row = blockIdx.x;
+    Sums a;
+    a.init();
+    if (lane < p.parts) a = p.sums[row * p.parts + lane];
+    if (p.k > 0) {
+        const uint64_t* in = p.keys + row * p.parts * p.k;
+        // The K-th largest of the lists' leading keys, as many from each as
+        // fill a wave, bounds the K-th best from below.
+        const int lead = 64 / p.parts < p.k ? 64 / p.parts : p.k;
+        uint64_t x = 0;
+        if (lane < p.parts * lead) x = in[lane / lead * p.k + lane % lead];
+        x = wave_sort<true>(x, lane);
+        const uint64_t least = umax64(readlane64(x, p.k - 1), 1);
+        int n = 0;
+        const int all = p.parts * p.k;
+        for (int i = 0; i < all; i += 64) {
+            const uint64_t key = i + lane < all ? in[i + lane] : 0;
+            const uint64_t hit = __ballot(key >= least);
+            if (key >= least) keys[n + lanes_below(hit)] = key;
+            n += __popcll(hit);
+        }
+        wave_lds_sync();
+        for (int i = lane; i < n; i += 64) {
+            const uint64_t key = keys[i];
+            const int r = keys_above(keys, n, key);
+            if (r < p.k) sorted[r] = key;
+        }
+        wave_lds_sync();
+    }
+    a = wave_join<ENT>(a, p.c, lane);
+    write_logprobs<L>(p, row, a, sorted);
 }
 
 struct GradParams {
@@ -300,11 +547,11 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(DistillParams p) {
     float m = r.m, s = r.s;
     if (tail_mode && !t.bad) {
         for (int i = 0; i < p.k; ++i)
-            if (t.ids[i] != 0xffffffffu) m = fmaxf(m, L::load(p.logits, at + t.ids[i]));
+            if (t.ids[i] != 0xffffffffu) m = fmaxf(m, lload<L>(p.logits, at + t.ids[i]));
         s = s == 0.0f ? 0.0f : s * __builtin_amdgcn_exp2f((r.m - m) * p.c);
         for (int i = 0; i < p.k; ++i)
             if (t.ids[i] != 0xffffffffu && !listed(t.ids, i, t.ids[i]))
-                s += __builtin_amdgcn_exp2f((L::load(p.logits, at + t.ids[i]) - m) * p.c);
+                s += __builtin_amdgcn_exp2f((lload<L>(p.logits, at + t.ids[i]) - m) * p.c);
     }
     const bool empty = s == 0.0f;
     const double logsum = empty ? -INFINITY : log((double)s);
@@ -315,7 +562,7 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(DistillParams p) {
         if (t.q[i] == 0.0) continue;
         const double logp =
             empty ? -(double)INFINITY
-                  : ((double)L::load(p.logits, at + t.ids[i]) - (double)m) * p.inv_tau - logsum;
+                  : ((double)lload<L>(p.logits, at + t.ids[i]) - (double)m) * p.inv_tau - logsum;
         loss += t.q[i] * (t.logq[i] - logp);
     }
     if (t.rest > 0.0) loss += t.rest * (log(t.rest) - tail);
@@ -333,7 +580,7 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(GradParams p) {
     const int64_t at = row * p.stride, to = row * p.grad_stride;
     const ws_row_stats st = p.stats[row];
     if (st.logsum == -INFINITY) {
-        for (int j = threadIdx.x; j < p.vocab; j += kThreads) L::store(p.grad, to + j, 0.0f);
+        for (int j = threadIdx.x; j < p.vocab; j += kThreads) lstore<L>(p.grad, to + j, 0.0f);
         return;
     }
     float a = 0.0f, b = 0.0f, scale = p.inv_tau;
@@ -379,7 +626,7 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(GradParams p) {
         }
     }
     for (int j = threadIdx.x; j < p.vocab; j += kThreads) {
-        const float d = L::load(p.logits, at + j) - st.max;
+        const float d = lload<L>(p.logits, at + j) - st.max;
         float v = a;
         if (b != 0.0f) v += b * fmaxf(d * p.inv_tau - st.logsum, kFar);
         float extra = 0.0f;
@@ -394,7 +641,7 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(GradParams p) {
             __builtin_amdgcn_exp2f(d * p.c - (DISTILL && named ? listed_base : base));
         if (!DISTILL && j == target) extra += gt;
         v = prob * v + extra;
-        L::store(p.grad, to + j, v * scale);
+        lstore<L>(p.grad, to + j, v * scale);
     }
 }
 
@@ -415,16 +662,43 @@ int device_ready(int32_t device) {
         else { CALL(BF16); }                            \
     } while (0)
 
-int launched() { return hipGetLastError() == hipSuccess ? WS_OK : WS_E_HIP; }
+// Enqueues one kernel; its parameters are one struct, copied by the call.
+template <typename P>
+int launch(void (*kernel)(P), int64_t groups, int threads, const P& params, hipStream_t s) {
+    P copy = params;
+    void* args[] = {&copy};
+    const hipError_t e =
+        hipLaunchKernel(reinterpret_cast<const void*>(kernel), dim3((uint32_t)groups),
+                        dim3((uint32_t)threads), args, 0, s);
+    return e == hipSuccess ? WS_OK : WS_E_HIP;
+}
+
+template <typename L>
+int run_logprobs(const ws_rows& r, const LogprobsPlan& plan, const LogprobsParams& p,
+                 hipStream_t s) {
+    const bool ent = p.entropy != nullptr, top = p.k > 0;
+    const auto wide = top ? (ent ? logprobs_kernel<L, 256, true, true>
+                                 : logprobs_kernel<L, 256, false, true>)
+                          : (ent ? logprobs_kernel<L, 256, true, false>
+                                 : logprobs_kernel<L, 256, false, false>);
+    const auto wave = top ? (ent ? logprobs_kernel<L, 64, true, true>
+                                 : logprobs_kernel<L, 64, false, true>)
+                          : (ent ? logprobs_kernel<L, 64, true, false>
+                                 : logprobs_kernel<L, 64, false, false>);
+    int v = launch(plan.threads == 64 ? wave : wide, (int64_t)r.rows * plan.parts, plan.threads, p,
+                   s);
+    if (v != WS_OK || plan.parts == 1) return v;
+    return launch(ent ? logprobs_join_kernel<L, true> : logprobs_join_kernel<L, false>, r.rows, 64,
+                  p, s);
+}
 
 float scale_c(const ws_rows& r) { return (float)(1.4426950408889634074 / (double)r.temperature); }
 float scale_inv(const ws_rows& r) { return (float)(1.0 / (double)r.temperature); }
 
 int run_distill_grad(const ws_rows& r, const GradParams& g, hipStream_t s) {
-#define CALL(L) grad_kernel<L, true><<<r.rows, kThreads, 0, s>>>(g)
+#define CALL(L) return launch(grad_kernel<L, true>, r.rows, kThreads, g, s)
     WS_BY_DTYPE(r.dtype, CALL);
 #undef CALL
-    return launched();
 }
 
 }  // namespace
@@ -434,25 +708,42 @@ extern "C" int ws_logprobs_workspace(const ws_rows* rows, int32_t top_k, size_t*
     const int v = ws::validate_rows(rows);
     if (v != WS_OK) return v;
     if (!bytes || ws::validate_top_k(*rows, top_k) != WS_OK) return WS_E_INVALID_ARG;
-    *bytes = 0;
+    *bytes = ws::plan_logprobs(*rows, top_k).workspace;
     return WS_OK;
 }
 
 extern "C" int ws_logprobs(const ws_rows* rows, const ws_logprobs_args* args, void* stream) {
     int v = ws::validate_logprobs(rows, args);
     if (v != WS_OK) return v;
-    if (rows->rows == 0) return WS_OK;
-    v = ws::device_ready(rows->device);
-    if (v != WS_OK) return v;
     const ws_rows& r = *rows;
-    ws::LogprobsParams p{args->logits, r.row_stride, args->targets, args->logprob, args->entropy,
-                         args->top, args->stats, r.vocab, args->top_k, ws::scale_c(r),
-                         ws::scale_inv(r)};
+    if (r.rows == 0) return WS_OK;
+    const ws::LogprobsPlan plan = ws::plan_logprobs(r, args->top_k);
+    v = ws::validate_workspace(args->workspace, args->workspace_bytes, plan.workspace);
+    if (v != WS_OK) return v;
+    v = ws::device_ready(r.device);
+    if (v != WS_OK) return v;
+    ws::LogprobsParams p{};
+    p.logits = args->logits;
+    p.stride = r.row_stride;
+    p.targets = args->targets;
+    p.logprob = args->logprob;
+    p.entropy = args->entropy;
+    p.top = args->top;
+    p.stats = args->stats;
+    p.vocab = r.vocab;
+    p.k = args->top_k;
+    p.chunk = plan.chunk;
+    p.parts = plan.parts;
+    p.c = ws::scale_c(r);
+    p.inv_tau = ws::scale_inv(r);
+    if (plan.parts > 1) {
+        p.keys = static_cast<uint64_t*>(args->workspace);
+        p.sums = reinterpret_cast<ws::Sums*>(p.keys + (int64_t)r.rows * plan.parts * p.k);
+    }
     const hipStream_t s = static_cast<hipStream_t>(stream);
-#define CALL(L) ws::logprobs_kernel<ws::L><<<r.rows, ws::kThreads, 0, s>>>(p)
+#define CALL(L) return ws::run_logprobs<ws::L>(r, plan, p, s)
     WS_BY_DTYPE(r.dtype, CALL);
 #undef CALL
-    return ws::launched();
 }
 
 extern "C" int ws_logprobs_grad(const ws_rows* rows, const ws_logprobs_grad_args* args,
@@ -480,10 +771,9 @@ extern "C" int ws_logprobs_grad(const ws_rows* rows, const ws_logprobs_grad_args
     g.c = ws::scale_c(r);
     g.inv_tau = ws::scale_inv(r);
     const hipStream_t s = static_cast<hipStream_t>(stream);
-#define CALL(L) ws::grad_kernel<ws::L, false><<<r.rows, ws::kThreads, 0, s>>>(g)
+#define CALL(L) return ws::launch(ws::grad_kernel<ws::L, false>, r.rows, ws::kThreads, g, s)
     WS_BY_DTYPE(r.dtype, CALL);
 #undef CALL
-    return ws::launched();
 }
 
 extern "C" int ws_distill_workspace(const ws_rows* rows, int32_t mode, int32_t gradient,
@@ -516,10 +806,9 @@ extern "C" int ws_distill(const ws_rows* rows, const ws_distill_args* args, void
         if (!p.tail)
             p.tail = reinterpret_cast<float*>(static_cast<ws_row_stats*>(args->workspace) + r.rows);
     }
-#define CALL(L) ws::distill_kernel<ws::L><<<r.rows, ws::kThreads, 0, s>>>(p)
+#define CALL(L) v = ws::launch(ws::distill_kernel<ws::L>, r.rows, ws::kThreads, p, s)
     WS_BY_DTYPE(r.dtype, CALL);
 #undef CALL
-    v = ws::launched();
     if (v != WS_OK || !gradient) return v;
     ws::GradParams g{};
     g.logits = args->logits;

@@ -139,7 +139,41 @@ inline int validate_workspace(const void* workspace, size_t given, size_t needed
 }
 
 // ---------------------------------------------------------------------------
-// Workspaces.
+// Launch geometry and workspaces.
+
+inline int64_t slots_of(const ws_rows& r) {
+    const int64_t vec = 16 / logit_bytes(r.dtype);
+    return (r.vocab + vec - 1) / vec;
+}
+
+// ws_logprobs: a row is split into `parts` of `chunk` 16-byte slots (the last
+// takes what is left, one slot more when the row's start is unaligned), one
+// workgroup each, joined by a second kernel.
+constexpr int kMaxRowParts = 64;
+
+struct LogprobsPlan {
+    int32_t threads = 256;
+    int32_t parts = 1;
+    int32_t chunk = 0;
+    size_t workspace = 0;
+};
+
+inline LogprobsPlan plan_logprobs(const ws_rows& r, int32_t top_k) {
+    LogprobsPlan p;
+    if (r.rows == 0) return p;
+    const int64_t slots = slots_of(r);
+    p.threads = slots <= 256 ? 64 : 256;
+    int64_t parts = (512 + r.rows - 1) / r.rows;
+    if (parts > slots / 256) parts = slots / 256;
+    if (parts > kMaxRowParts) parts = kMaxRowParts;
+    if (parts < 1) parts = 1;
+    p.chunk = (int32_t)((slots + parts - 1) / parts);
+    p.parts = (int32_t)((slots + p.chunk - 1) / p.chunk);
+    // Keys of the best K and the sums (three FP32) of every part.
+    if (p.parts > 1)
+        p.workspace = (size_t)r.rows * (size_t)p.parts * (8u * (size_t)top_k + 12u);
+    return p;
+}
 
 // ws_distill with a gradient runs the loss kernel, then the gradient kernel
 // from the row statistics and tails it left here.

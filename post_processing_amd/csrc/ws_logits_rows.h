@@ -1,0 +1,273 @@
+// ws_logits_rows.h -- device code shared by the kernels over rows of logits:
+// a row as 16-byte slots, running softmax sums, and reductions of a workgroup.
+// Internal to the library.
+//
+// A row may start at any element address.  It is read as 16-byte slots at
+// aligned addresses: slot s holds the VEC elements from s * VEC - off on,
+// where off is the row start's distance, in elements, from the aligned
+// address at or below it.  Slots that lie in the row whole are one 16-byte
+// load; the first and last, where they stick out, are read element by element.
+#pragma once
+
+#include <hip/hip_fp16.h>
+#include <hip/hip_runtime.h>
+
+#include <cfloat>
+#include <cstdint>
+
+#include "ws_lanes.h"
+#include "ws_logits.h"
+
+namespace ws {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+// A finite stand-in below every difference z - max that matters: at the
+// highest temperature exp((z - max) / tau) is 0 from -1.04e5 on, and 0 times a
+// finite number is 0 where 0 times -inf would be NaN.
+constexpr float kFar = -1.0e6f;
+
+// ---- element types ---------------------------------------------------------
+
+struct F32 {
+    using Elem = float;
+    static constexpr int VEC = 4;
+    static __device__ __forceinline__ float up(float v) { return v; }
+    static __device__ __forceinline__ float down(float v) { return v; }
+    static __device__ __forceinline__ void unpack(uint4 w, float (&v)[VEC]) {
+        v[0] = __uint_as_float(w.x);
+        v[1] = __uint_as_float(w.y);
+        v[2] = __uint_as_float(w.z);
+        v[3] = __uint_as_float(w.w);
+    }
+    static __device__ __forceinline__ uint4 pack(const float (&v)[VEC]) {
+        return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                          __float_as_uint(v[3]));
+    }
+};
+
+struct F16 {
+    using Elem = _Float16;
+    static constexpr int VEC = 8;
+    typedef _Float16 Pair __attribute__((ext_vector_type(2)));
+    static __device__ __forceinline__ float up(_Float16 v) { return (float)v; }
+    static __device__ __forceinline__ _Float16 down(float v) { return (_Float16)v; }
+    static __device__ __forceinline__ void unpack(uint4 w, float (&v)[VEC]) {
+        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const Pair p = __builtin_bit_cast(Pair, x[i]);
+            v[2 * i] = (float)p.x;
+            v[2 * i + 1] = (float)p.y;
+        }
+    }
+    static __device__ __forceinline__ uint4 pack(const float (&v)[VEC]) {
+        uint32_t x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            Pair p;
+            p.x = (_Float16)v[2 * i];
+            p.y = (_Float16)v[2 * i + 1];
+            x[i] = __builtin_bit_cast(uint32_t, p);
+        }
+        return make_uint4(x[0], x[1], x[2], x[3]);
+    }
+};
+
+struct BF16 {
+    using Elem = __bf16;
+    static constexpr int VEC = 8;
+    typedef __bf16 Pair __attribute__((ext_vector_type(2)));
+    static __device__ __forceinline__ float up(__bf16 v) {
+        return __uint_as_float((uint32_t)__builtin_bit_cast(uint16_t, v) << 16);
+    }
+    static __device__ __forceinline__ __bf16 down(float v) { return (__bf16)v; }   // nearest even
+    static __device__ __forceinline__ void unpack(uint4 w, float (&v)[VEC]) {
+        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(x[i] << 16);
+            v[2 * i + 1] = __uint_as_float(x[i] & 0xffff0000u);
+        }
+    }
+    static __device__ __forceinline__ uint4 pack(const float (&v)[VEC]) {
+        uint32_t x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            Pair p;
+            p.x = (__bf16)v[2 * i];
+            p.y = (__bf16)v[2 * i + 1];
+            x[i] = __builtin_bit_cast(uint32_t, p);
+        }
+        return make_uint4(x[0], x[1], x[2], x[3]);
+    }
+};
+
+// ---- a workgroup's part of a row ---------------------------------------------
+
+// Slots [first, first + n) of a row; slot numbers below are relative to first.
+template <typename L>
+struct Part {
+    static constexpr int VEC = L::VEC;
+    const typename L::Elem* row;   // element 0 of the row
+    const char* base;              // address of relative slot 0 (16-byte aligned)
+    int vocab;
+    int e0;                        // element at relative slot 0's start (may be < 0)
+    int n;                         // slots
+    int full_from, full_to;        // relative slots that lie in the row whole
+
+    // chunk: slots of a part; index: which of `parts`.  The last takes the rest.
+    __device__ __forceinline__ void init(const void* logits, int64_t at, int V, int chunk,
+                                         int parts, int index) {
+        row = static_cast<const typename L::Elem*>(logits) + at;
+        vocab = V;
+        const int off = (int)(((uintptr_t)row & 15u) / sizeof(typename L::Elem));
+        const int slots = (V + off + VEC - 1) / VEC;
+        const int first = index * chunk;
+        n = index == parts - 1 ? slots - first : chunk;
+        e0 = first * VEC - off;
+        base = reinterpret_cast<const char*>(row - off) + (int64_t)first * 16;
+        full_from = first == 0 && off != 0 ? 1 : 0;
+        const int whole = (V + off) / VEC - first;
+        full_to = whole < n ? whole : n;
+    }
+    __device__ __forceinline__ uint4 load(int s) const {
+        return *reinterpret_cast<const uint4*>(base + (uint32_t)s * 16u);
+    }
+    // Element by element; -inf outside the row.
+    __device__ __forceinline__ void load_edge(int s, float (&v)[VEC]) const {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            const int e = e0 + s * VEC + j;
+            v[j] = e >= 0 && e < vocab ? L::up(row[e]) : -INFINITY;
+        }
+    }
+    __device__ __forceinline__ bool whole(int s) const { return s >= full_from && s < full_to; }
+    __device__ __forceinline__ void load_any(int s, float (&v)[VEC]) const {
+        if (whole(s)) L::unpack(load(s), v);
+        else load_edge(s, v);
+    }
+    __device__ __forceinline__ float at(int e) const { return L::up(row[e]); }
+};
+
+// ---- running sums --------------------------------------------------------------
+
+// With respect to a running maximum m (-FLT_MAX or more, so that a difference
+// from it is never inf - inf in a row without +inf):
+//   s = sum e_j, u = sum e_j (z_j - m), e_j = 2^((z_j - m) c), c = log2(e) / tau.
+struct Sums {
+    float m, s, u;
+
+    __device__ __forceinline__ void init() {
+        m = -FLT_MAX;
+        s = 0.0f;
+        u = 0.0f;
+    }
+    // Moves to a maximum of at least m.
+    template <bool ENT>
+    __device__ __forceinline__ void raise(float to, float c) {
+        const float d = m - to;
+        const float a = __builtin_amdgcn_exp2f(d * c);
+        if constexpr (ENT) u = a * (u + fmaxf(d, kFar) * s);
+        s *= a;
+        m = to;
+    }
+};
+
+template <int J>
+__device__ __forceinline__ float xor_lane_f(float v, int lane) {
+    return __uint_as_float(xor_lane32<J>(__float_as_uint(v), lane));
+}
+
+__device__ __forceinline__ float wave_max(float v, int lane) {
+    v = fmaxf(v, xor_lane_f<32>(v, lane));
+    v = fmaxf(v, xor_lane_f<16>(v, lane));
+    v = fmaxf(v, xor_lane_f<8>(v, lane));
+    v = fmaxf(v, xor_lane_f<4>(v, lane));
+    v = fmaxf(v, xor_lane_f<2>(v, lane));
+    return fmaxf(v, xor_lane_f<1>(v, lane));
+}
+
+__device__ __forceinline__ float wave_sum(float v, int lane) {
+    v += xor_lane_f<32>(v, lane);
+    v += xor_lane_f<16>(v, lane);
+    v += xor_lane_f<8>(v, lane);
+    v += xor_lane_f<4>(v, lane);
+    v += xor_lane_f<2>(v, lane);
+    return v + xor_lane_f<1>(v, lane);
+}
+
+template <int J>
+__device__ __forceinline__ double xor_lane_d(double v, int lane) {
+    return __builtin_bit_cast(double, xor_lane64<J>(__builtin_bit_cast(uint64_t, v), lane));
+}
+
+__device__ __forceinline__ double wave_sum_d(double v, int lane) {
+    v += xor_lane_d<32>(v, lane);
+    v += xor_lane_d<16>(v, lane);
+    v += xor_lane_d<8>(v, lane);
+    v += xor_lane_d<4>(v, lane);
+    v += xor_lane_d<2>(v, lane);
+    return v + xor_lane_d<1>(v, lane);
+}
+
+// The sums of a wave's lanes, in every lane.
+template <bool ENT>
+__device__ __forceinline__ Sums wave_join(Sums a, float c, int lane) {
+    a.raise<ENT>(wave_max(a.m, lane), c);
+    a.s = wave_sum(a.s, lane);
+    if constexpr (ENT) a.u = wave_sum(a.u, lane);
+    return a;
+}
+
+// The sums of `count` partial sums in order, in every thread that calls.
+template <bool ENT>
+__device__ __forceinline__ Sums join_in_order(const Sums* p, int count, float c) {
+    Sums t = p[0];
+    for (int i = 1; i < count; ++i) t.m = fmaxf(t.m, p[i].m);
+    const float m = t.m;
+    t = p[0];
+    t.raise<ENT>(m, c);
+    for (int i = 1; i < count; ++i) {
+        Sums x = p[i];
+        x.raise<ENT>(m, c);
+        t.s += x.s;
+        if constexpr (ENT) t.u += x.u;
+    }
+    return t;
+}
+
+// ---- order keys ------------------------------------------------------------------
+
+// Order-preserving unsigned image of an FP32 value: NaN -> -inf and -0 -> +0
+// first, then larger values have larger images; 0 is below every image.
+__device__ __forceinline__ uint32_t value_image(float v) {
+    uint32_t b = __float_as_uint(v);
+    b = (b & 0x7fffffffu) > 0x7f800000u ? 0xff800000u : b;
+    b = b == 0x80000000u ? 0u : b;
+    return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+
+__device__ __forceinline__ float image_value(uint32_t i) {
+    return __uint_as_float(i & 0x80000000u ? i ^ 0x80000000u : ~i);
+}
+
+// (value descending, index ascending) as one integer, larger = better.
+__device__ __forceinline__ uint64_t value_key(float v, uint32_t index) {
+    return ((uint64_t)value_image(v) << 32) | (uint32_t)~index;
+}
+
+// Number of the n keys of v (LDS) greater than x.
+__device__ __forceinline__ int keys_above(const uint64_t* v, int n, uint64_t x) {
+    int r = 0, j = 0;
+    for (; j + 8 <= n; j += 8) {
+        uint64_t t[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t[i] = v[j + i];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r += t[i] > x ? 1 : 0;
+    }
+    for (; j < n; ++j) r += v[j] > x ? 1 : 0;
+    return r;
+}
+
+}  // namespace ws
