@@ -13,86 +13,6 @@
 namespace ws {
 namespace {
 
-constexpr int kThreads = 256;
-
-template <typename L>
-__device__ __forceinline__ float lload(const void* p, int64_t i) {
-    return L::up(static_cast<const typename L::Elem*>(p)[i]);
-}
-template <typename L>
-__device__ __forceinline__ void lstore(void* p, int64_t i, float v) {
-    static_cast<typename L::Elem*>(p)[i] = L::down(v);
-}
-
-template <typename T, typename Op>
-__device__ __forceinline__ T wave_reduce(T v, int lane, Op op) {
-    if constexpr (sizeof(T) == 8) {
-        v = op(v, xor_lane64<32>(v, lane));
-        v = op(v, xor_lane64<16>(v, lane));
-        v = op(v, xor_lane64<8>(v, lane));
-        v = op(v, xor_lane64<4>(v, lane));
-        v = op(v, xor_lane64<2>(v, lane));
-        v = op(v, xor_lane64<1>(v, lane));
-    } else {
-        v = op(v, __uint_as_float(xor_lane32<32>(__float_as_uint(v), lane)));
-        v = op(v, __uint_as_float(xor_lane32<16>(__float_as_uint(v), lane)));
-        v = op(v, __uint_as_float(xor_lane32<8>(__float_as_uint(v), lane)));
-        v = op(v, __uint_as_float(xor_lane32<4>(__float_as_uint(v), lane)));
-        v = op(v, __uint_as_float(xor_lane32<2>(__float_as_uint(v), lane)));
-        v = op(v, __uint_as_float(xor_lane32<1>(__float_as_uint(v), lane)));
-    }
-    return v;
-}
-
-// The same result in every thread of the workgroup; scratch holds one T per
-// wave and may be reused after the call.
-template <typename T, typename Op>
-__device__ __forceinline__ T group_reduce(T v, T* scratch, Op op) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    v = wave_reduce(v, lane, op);
-    if (lane == 0) scratch[wave] = v;
-    __syncthreads();
-    T r = scratch[0];
-    for (int w = 1; w < kThreads / 64; ++w) r = op(r, scratch[w]);
-    __syncthreads();
-    return r;
-}
-
-struct AddF {
-    __device__ float operator()(float a, float b) const { return a + b; }
-};
-struct MaxF {
-    __device__ float operator()(float a, float b) const { return fmaxf(a, b); }
-};
-
-__device__ __forceinline__ bool listed(const uint32_t* ids, int k, uint32_t j) {
-    for (int i = 0; i < k; ++i)
-        if (ids[i] == j) return true;
-    return false;
-}
-
-template <typename L>
-__device__ Sums row_sums(const void* logits, int64_t at, int V, float c, const uint32_t* ids,
-                         int k, float* scratch) {
-    float m = -FLT_MAX;
-    for (int j = threadIdx.x; j < V; j += kThreads)
-        if (!listed(ids, k, j)) m = fmaxf(m, lload<L>(logits, at + j));
-    m = group_reduce(m, scratch, MaxF());
-    float s = 0.0f, u = 0.0f;
-    for (int j = threadIdx.x; j < V; j += kThreads) {
-        if (listed(ids, k, j)) continue;
-        const float d = lload<L>(logits, at + j) - m;
-        const float e = __builtin_amdgcn_exp2f(d * c);
-        s += e;
-        u += e * fmaxf(d, kFar);
-    }
-    Sums r;
-    r.m = m;
-    r.s = group_reduce(s, scratch, AddF());
-    r.u = group_reduce(u, scratch, AddF());
-    return r;
-}
-
 // ---------------------------------------------------------------------------
 // Forward: one pass over the row.
 //
@@ -107,6 +27,124 @@ __device__ Sums row_sums(const void* logits, int64_t at, int V, float c, const u
 // - in its best slot, or, only if its second largest slot maximum reaches t as
 // well, in any of its slots.  So after the pass about K slots are read again
 // instead of a selection running inside the pass.
+
+constexpr int kBatch = kBatchSlots;   // slots a thread has in flight
+
+template <int VEC>
+__device__ __forceinline__ float slot_max(const float (&v)[VEC]) {
+    float m = fmaxf(v[0], v[1]);
+#pragma unroll
+    for (int j = 2; j < VEC; ++j) m = fmaxf(m, v[j]);
+    return m;
+}
+
+// Takes the tokens a slot's mark names out of its values.
+template <int VEC>
+__device__ __forceinline__ void hide_listed(uint32_t mark, float (&v)[VEC]) {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) v[j] = mark >> j & 1u ? -INFINITY : v[j];
+}
+
+// What a thread remembers of its slots for the best K.
+struct SlotTrack {
+    float best, second;   // largest and second largest slot maximum
+    int slot;             // first slot of the largest
+};
+
+// Takes U slots of values, the first at `slot` and NT apart, into a thread's
+// running sums.  ENT: the entropy's sum as well; TOPK: the slot maxima; MASK:
+// without the marked tokens.
+template <typename L, int NT, bool ENT, bool TOPK, bool MASK, int U>
+__device__ __forceinline__ void take_slots(float (&v)[U][L::VEC], int slot, float c,
+                                           const uint8_t* marks, Sums& a, SlotTrack& t) {
+    constexpr int VEC = L::VEC;
+    if constexpr (MASK) {
+#pragma unroll
+        for (int i = 0; i < U; ++i)   // rare
+            if (const uint32_t mark = marks[slot + i * NT]) hide_listed<VEC>(mark, v[i]);
+    }
+    float top = a.m;
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+        const float m = slot_max<VEC>(v[i]);
+        top = fmaxf(top, m);
+        if constexpr (TOPK) {
+            t.second = __builtin_amdgcn_fmed3f(m, t.best, t.second);
+            t.slot = m > t.best ? slot + i * NT : t.slot;
+            t.best = fmaxf(t.best, m);
+        }
+    }
+    a.raise<ENT>(top, c);
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            const float d = v[i][j] - a.m;
+            const float e = __builtin_amdgcn_exp2f(d * c);
+            a.s += e;
+            if constexpr (ENT) a.u = fmaf(e, fmaxf(d, kFar), a.u);
+        }
+}
+
+// A thread's running sums over its slots of a part.
+template <typename L, int NT, bool ENT, bool TOPK, bool MASK>
+__device__ __forceinline__ void stream_part(const Part<L>& part, float c, const uint8_t* marks,
+                                            Sums& a, SlotTrack& t) {
+    constexpr int VEC = L::VEC;
+    const int tid = threadIdx.x;
+    a.init();
+    t = {-INFINITY, -INFINITY, tid};
+    int s = tid;
+    if (s < part.full_from) {   // the slot that sticks out in front
+        float v[1][VEC];
+        part.load_edge(s, v[0]);
+        take_slots<L, NT, ENT, TOPK, MASK>(v, s, c, marks, a, t);
+        s += NT;
+    }
+    for (; s < part.full_to; s += kBatch * NT) {
+        float v[kBatch][VEC];
+        uint4 w[kBatch];
+        if (s + (kBatch - 1) * NT < part.full_to) {
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) w[i] = part.load(s + i * NT);
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) L::unpack(w[i], v[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+                if (s + i * NT < part.full_to) w[i] = part.load(s + i * NT);
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                if (s + i * NT < part.full_to) {
+                    L::unpack(w[i], v[i]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) v[i][j] = -INFINITY;
+                }
+            }
+        }
+        take_slots<L, NT, ENT, TOPK, MASK>(v, s, c, marks, a, t);
+    }
+    // The slot that sticks out behind belongs to the thread next in turn.
+    const int tail = part.full_to > part.full_from ? part.full_to : part.full_from;
+    if (tail < part.n && tail % NT == tid) {
+        float v[1][VEC];
+        part.load_edge(tail, v[0]);
+        take_slots<L, NT, ENT, TOPK, MASK>(v, tail, c, marks, a, t);
+    }
+}
+
+// The sums of a workgroup's threads, in every thread.
+template <int NT, bool ENT>
+__device__ __forceinline__ Sums group_join(Sums a, float c, Sums* wave_sums) {
+    a = wave_join<ENT>(a, c, threadIdx.x & 63);
+    if constexpr (NT > 64) {
+        if ((threadIdx.x & 63) == 0) wave_sums[threadIdx.x >> 6] = a;
+        __syncthreads();
+        a = join_in_order<ENT>(wave_sums, NT / 64, c);
+    }
+    return a;
+}
 
 // A row's best keys as they are collected, in LDS.
 template <typename L, int NT>
@@ -161,12 +199,6 @@ __device__ __forceinline__ int keep_best(Best<L, NT>& b, int k) {
     __syncthreads();
     return kept;
 }
-
-// What a thread remembers of its slots for the best K.
-struct SlotTrack {
-    float best, second;   // largest and second largest slot maximum
-    int slot;             // first slot of the largest
-};
 
 // The K best keys of a part of a row into b.sorted; returns how many there are
 // (K, or the part's elements if fewer).  all: read every slot again (a row
@@ -295,8 +327,6 @@ __device__ __forceinline__ void write_logprobs(const LogprobsParams& p, int64_t 
     }
 }
 
-constexpr int kBatch = 4;   // slots a thread has in flight
-
 struct Nothing {
     static constexpr uint64_t* sorted = nullptr;
 };
@@ -314,87 +344,16 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(LogprobsParams p) {
     constexpr int VEC = L::VEC;
     __shared__ Sums wave_sums[NT / 64];
     __shared__ typename Select<TOPK, Best<L, NT>>::Type best;
-    const int tid = threadIdx.x, lane = tid & 63;
+    const int tid = threadIdx.x;
     const int64_t row = blockIdx.x / (uint32_t)p.parts;
     const int index = (int)(blockIdx.x % (uint32_t)p.parts);
     Part<L> part;
     part.init(p.logits, row * p.stride, p.vocab, p.chunk, p.parts, index);
 
     Sums a;
-    a.init();
-    SlotTrack t{-INFINITY, -INFINITY, tid};
-    // The running sums over U slots of values, the first at `slot`, NT apart.
-    const auto take = [&](auto& v, int slot) {
-        constexpr int U = sizeof(v) / sizeof(v[0]);
-        float top = a.m;
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-            float m = fmaxf(v[i][0], v[i][1]);
-#pragma unroll
-            for (int j = 2; j < VEC; ++j) m = fmaxf(m, v[i][j]);
-            top = fmaxf(top, m);
-            if constexpr (TOPK) {
-                t.second = __builtin_amdgcn_fmed3f(m, t.best, t.second);
-                t.slot = m > t.best ? slot + i * NT : t.slot;
-                t.best = fmaxf(t.best, m);
-            }
-        }
-        a.raise<ENT>(top, p.c);
-#pragma unroll
-        for (int i = 0; i < U; ++i)
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                const float d = v[i][j] - a.m;
-                const float e = __builtin_amdgcn_exp2f(d * p.c);
-                a.s += e;
-                if constexpr (ENT) a.u = fmaf(e, fmaxf(d, kFar), a.u);
-            }
-    };
-    int s = tid;
-    if (s < part.full_from) {   // the slot that sticks out in front
-        float v[1][VEC];
-        part.load_edge(s, v[0]);
-        take(v, s);
-        s += NT;
-    }
-    for (; s < part.full_to; s += kBatch * NT) {
-        float v[kBatch][VEC];
-        uint4 w[kBatch];
-        if (s + (kBatch - 1) * NT < part.full_to) {
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) w[i] = part.load(s + i * NT);
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) L::unpack(w[i], v[i]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i)
-                if (s + i * NT < part.full_to) w[i] = part.load(s + i * NT);
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                if (s + i * NT < part.full_to) {
-                    L::unpack(w[i], v[i]);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) v[i][j] = -INFINITY;
-                }
-            }
-        }
-        take(v, s);
-    }
-    // The slot that sticks out behind belongs to the thread next in turn.
-    const int tail = part.full_to > part.full_from ? part.full_to : part.full_from;
-    if (tail < part.n && tail % NT == tid) {
-        float v[1][VEC];
-        part.load_edge(tail, v[0]);
-        take(v, tail);
-    }
-
-    a = wave_join<ENT>(a, p.c, lane);
-    if constexpr (NT > 64) {
-        if (lane == 0) wave_sums[tid >> 6] = a;
-        __syncthreads();
-        a = join_in_order<ENT>(wave_sums, NT / 64, p.c);
-    }
+    SlotTrack t;
+    stream_part<L, NT, ENT, TOPK, false>(part, p.c, nullptr, a, t);
+    a = group_join<NT, ENT>(a, p.c, wave_sums);
     int kept = 0;
     if constexpr (TOPK) {
         kept = select_best<L, NT>(part, t, a.s != a.s, p.k, best);
@@ -451,75 +410,150 @@ __global__ void __launch_bounds__(64) logprobs_join_kernel(LogprobsParams p) {
     write_logprobs<L>(p, row, a, sorted);
 }
 
-struct GradParams {
-    const void* logits;
-    void* grad;
-    int64_t stride, grad_stride;
-    const ws_row_stats* stats;
-    const ws_topk_entry* entries;   // alternatives, or the teacher's entries
-    const float* grad_entries;      // [rows][k] upstream of the alternatives
-    const int32_t* targets;
-    const float* grad_target;       // [rows]
-    const float* entropy;
-    const float* grad_entropy;
-    const float* tail;              // distillation
-    const float* grad_loss;
-    int32_t vocab;
-    int32_t k;
-    int32_t mode;
-    float c, inv_tau;
+// ---------------------------------------------------------------------------
+// Tokens a row names: teacher entries, alternatives, the target.
+//
+// Wave 0 of a workgroup holds them, entries lane and lane + 64.  They are few,
+// so what they need in FP64 (a teacher's probabilities, the small difference 1 -
+// sum q, the loss's near-cancelling terms) costs a wave a few hundred
+// instructions a row.
+
+constexpr uint32_t kAbsent = 0xffffffffu;
+
+struct Named {
+    uint32_t id[2];    // kAbsent: none
+    float z[2];        // its logit
+    float add[2];      // what a gradient adds for the token, all its entries together
+    bool first[2];     // the token's first entry
+    bool bad;          // some index lies outside the row (wave-uniform)
 };
 
-// A distillation row's teacher entries in LDS.
-struct Teacher {
-    uint32_t ids[WS_DISTILL_MAX_K];   // 0xffffffff: absent
-    double q[WS_DISTILL_MAX_K];
-    double logq[WS_DISTILL_MAX_K];
-    double rest;                      // q_t
-    double mass;                      // M
-    int distinct;
-    bool bad;                         // an index outside the row
-};
-
-__device__ void read_teacher(const ws_topk_entry* e, int k, int mode, int V, Teacher* t) {
-    for (int i = threadIdx.x; i < k; i += kThreads) {
-        t->ids[i] = (uint32_t)e[i].index;
-        t->logq[i] = (double)e[i].score;
+// The token's logits, and whether any index lies outside.  Read before any
+// thread writes a gradient over the logits.
+template <typename L>
+__device__ __forceinline__ void read_named(Named& n, const typename L::Elem* row, int V) {
+    bool bad = false;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        n.z[h] = -INFINITY;
+        if (n.id[h] < (uint32_t)V) n.z[h] = L::up(row[n.id[h]]);
+        else if (n.id[h] != kAbsent) bad = true;
     }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        t->bad = false;
-        t->distinct = 0;
-        double high = -INFINITY;
-        for (int i = 0; i < k; ++i) {
-            if (t->ids[i] == 0xffffffffu) continue;
-            if (t->ids[i] >= (uint32_t)V) t->bad = true;
-            if (!listed(t->ids, i, t->ids[i])) ++t->distinct;
-            if (!(t->logq[i] <= high)) high = t->logq[i];
-        }
-        double sum = 0.0;
-        const double shift = mode == WS_DISTILL_RENORM && high != -INFINITY ? high : 0.0;
-        for (int i = 0; i < k; ++i) {
-            t->q[i] = t->ids[i] == 0xffffffffu ? 0.0 : exp(t->logq[i] - shift);
-            sum += t->q[i];
-        }
-        t->rest = 0.0;
-        t->mass = sum;
-        if (mode == WS_DISTILL_RENORM) {
-            if (sum != 0.0) {
-                for (int i = 0; i < k; ++i) {
-                    t->q[i] /= sum;
-                    t->logq[i] -= shift + log(sum);
-                }
-                t->mass = sum / sum;
-            }
-        } else if (t->distinct < V) {
-            t->rest = sum < 1.0 ? 1.0 - sum : 0.0;
-            t->mass = sum + t->rest;
-        }
-    }
-    __syncthreads();
+    n.bad = __ballot(bad) != 0;
 }
+
+// Finds tokens named more than once among `count` entries and gathers what
+// their entries add at the first.  ids and adds: LDS scratch of wave 0.
+__device__ __forceinline__ void merge_named(Named& n, int count, uint32_t* ids, float* adds,
+                                            int lane) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        ids[lane + 64 * h] = n.id[h];
+        adds[lane + 64 * h] = n.add[h];
+    }
+    wave_lds_sync();
+    n.first[0] = n.id[0] != kAbsent;
+    n.first[1] = n.id[1] != kAbsent;
+    bool again = false;
+    const int padded = (count + 3) & ~3;   // entries past count are kAbsent
+    for (int j = 0; j < padded; j += 4) {
+        const uint4 x = *reinterpret_cast<const uint4*>(ids + j);
+        const uint32_t q[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            again |= q[i] == n.id[0] && j + i < lane;
+            again |= q[i] == n.id[1] && j + i < lane + 64;
+        }
+    }
+    if (__ballot(again && (n.first[0] || n.first[1])) == 0) return;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if (n.id[h] == kAbsent) continue;
+        float sum = 0.0f;
+        for (int j = 0; j < count; ++j) {
+            if (ids[j] != n.id[h]) continue;
+            if (j < lane + 64 * h) n.first[h] = false;
+            sum += adds[j];
+        }
+        n.add[h] = sum;
+    }
+}
+
+// A distillation row's teacher, in wave 0.
+struct Teacher {
+    double q[2], logq[2];
+    double mass;   // sum of q, q_t included
+    double rest;   // q_t
+};
+
+// The entries' indices alone.
+__device__ __forceinline__ void read_ids(Named& n, const ws_topk_entry* entries, int k, int lane) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        n.id[h] = lane + 64 * h < k ? (uint32_t)entries[lane + 64 * h].index : kAbsent;
+}
+
+__device__ __forceinline__ Teacher read_teacher(Named& n, const ws_topk_entry* entries, int k,
+                                                int mode, int lane) {
+    Teacher t;
+    float score[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int i = lane + 64 * h;
+        n.id[h] = kAbsent;
+        score[h] = -INFINITY;
+        if (i < k) {
+            const ws_topk_entry e = entries[i];
+            n.id[h] = (uint32_t)e.index;
+            if (n.id[h] != kAbsent) score[h] = e.score;
+        }
+    }
+    double shift = 0.0;
+    if (mode == WS_DISTILL_RENORM) {
+        const float high = wave_max(fmaxf(score[0], score[1]), lane);
+        if (high != -INFINITY) shift = (double)high;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        t.logq[h] = (double)score[h] - shift;
+        t.q[h] = h == 0 || k > 64 ? exp(t.logq[h]) : 0.0;
+    }
+    const double sum = wave_sum_d(t.q[0] + t.q[1], lane);
+    t.mass = sum;
+    t.rest = 0.0;
+    if (mode == WS_DISTILL_RENORM) {
+        if (sum != 0.0) {
+            const double logsum = log(sum);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                t.q[h] /= sum;
+                t.logq[h] -= logsum;
+            }
+            t.mass = sum / sum;   // 1, or NaN
+        }
+    } else {
+        t.rest = sum < 1.0 ? 1.0 - sum : 0.0;
+    }
+    n.add[0] = -(float)t.q[0];
+    n.add[1] = -(float)t.q[1];
+    return t;
+}
+
+// With WS_DISTILL_TAIL, once merge_named has run: a list that names every
+// token leaves no rest.
+__device__ __forceinline__ void settle_rest(Teacher& t, const Named& n, int k, int V) {
+    if (V <= k && __popcll(__ballot(n.first[0])) + __popcll(__ballot(n.first[1])) >= V)
+        t.rest = 0.0;
+    t.mass += t.rest;
+}
+
+// ---------------------------------------------------------------------------
+// Distillation: the loss.
+//
+// With WS_DISTILL_TAIL the pass sums the unlisted tokens only (a byte a slot in
+// LDS marks the listed ones), and the few listed ones are added at the end: a
+// tail far below the listed tokens keeps its own maximum and its full
+// precision, which the difference of two sums near 1 would not.
 
 struct DistillParams {
     const void* logits;
@@ -528,121 +562,427 @@ struct DistillParams {
     float* loss;
     ws_row_stats* stats;
     float* tail;
+    Sums* sums;          // [rows][parts], when a row has several parts
+    const float* grad_loss;
+    void* grad;
+    int64_t grad_stride;
     int32_t vocab, k, mode;
+    int32_t chunk, parts;
+    int32_t mark_words;   // LDS words of marks
     float c, inv_tau;
 };
 
-template <typename L>
-__global__ void __launch_bounds__(kThreads) distill_kernel(DistillParams p) {
-    __shared__ float scratch[kThreads / 64];
-    __shared__ Teacher t;
-    const int64_t row = blockIdx.x;
-    const int64_t at = row * p.stride;
-    read_teacher(p.teacher + row * p.k, p.k, p.mode, p.vocab, &t);
-    const bool tail_mode = p.mode == WS_DISTILL_TAIL;
-    // The unlisted tokens' sums apart from the listed ones', so that a small
-    // tail is summed, never the difference of two sums near 1.
-    const Sums r = row_sums<L>(p.logits, at, p.vocab, p.c, t.ids, tail_mode ? p.k : 0, scratch);
-    if (threadIdx.x != 0) return;
-    float m = r.m, s = r.s;
-    if (tail_mode && !t.bad) {
-        for (int i = 0; i < p.k; ++i)
-            if (t.ids[i] != 0xffffffffu) m = fmaxf(m, lload<L>(p.logits, at + t.ids[i]));
-        s = s == 0.0f ? 0.0f : s * __builtin_amdgcn_exp2f((r.m - m) * p.c);
-        for (int i = 0; i < p.k; ++i)
-            if (t.ids[i] != 0xffffffffu && !listed(t.ids, i, t.ids[i]))
-                s += __builtin_amdgcn_exp2f((lload<L>(p.logits, at + t.ids[i]) - m) * p.c);
+// What the gradient of a row is made of: dz_j = scale 2^((z_j - max) c - base)
+// a, and for the listed tokens scale (2^((z_j - max) c - base_listed) a_listed +
+// add).  An unlisted token of a row with a tail is measured against the unlisted
+// tokens' own sum, so that a tail too small for FP32 still divides:
+//   p_j (M - q_t / p_t) = (p_j / p_t) (M p_t - q_t).
+struct Slope {
+    float max, base, base_listed;
+    float a, a_listed;
+    float b;       // entropy: a + b log2 p_j in a's place
+    float scale;
+    int zero;      // a row without a distribution: no gradient
+};
+
+__device__ __forceinline__ Slope distill_slope(const Teacher& t, bool bad, float max,
+                                               double logsum, double tail, float scale) {
+    constexpr double kLog2e64 = 1.4426950408889634074;
+    Slope s;
+    s.max = max;
+    s.base = s.base_listed = (float)(logsum * kLog2e64);
+    s.a = s.a_listed = bad ? NAN : (float)t.mass;
+    s.b = 0.0f;
+    if (t.rest > 0.0 && !bad) {
+        s.a = 0.0f;
+        if (tail != -(double)INFINITY) {
+            s.a = (float)(t.mass * exp(tail) - t.rest);
+            s.base = (float)((logsum + tail) * kLog2e64);
+        }
     }
-    const bool empty = s == 0.0f;
-    const double logsum = empty ? -INFINITY : log((double)s);
-    const double tail = r.s == 0.0f ? -(double)INFINITY
-                                    : ((double)r.m - (double)m) * p.inv_tau + log((double)r.s) - logsum;
-    double loss = 0.0;
-    for (int i = 0; i < p.k && !t.bad; ++i) {
-        if (t.q[i] == 0.0) continue;
-        const double logp =
-            empty ? -(double)INFINITY
-                  : ((double)lload<L>(p.logits, at + t.ids[i]) - (double)m) * p.inv_tau - logsum;
-        loss += t.q[i] * (t.logq[i] - logp);
-    }
-    if (t.rest > 0.0) loss += t.rest * (log(t.rest) - tail);
-    p.loss[row] = t.bad ? NAN : (float)loss;
-    if (p.stats) p.stats[row] = {empty ? -INFINITY : m, t.bad ? NAN : (float)logsum};
-    if (p.tail) p.tail[row] = (float)tail;
+    s.scale = scale;
+    s.zero = logsum == -(double)INFINITY;
+    return s;
 }
 
-// dz_j = p_j (a + b log p_j) for most tokens of a row; the few that a target,
-// an alternative or a teacher entry names get their own term on top.
-template <typename L, bool DISTILL>
-__global__ void __launch_bounds__(kThreads) grad_kernel(GradParams p) {
-    __shared__ Teacher t;
+// Row outputs from its sums, by wave 0; the slope for a gradient that follows.
+__device__ __forceinline__ Slope finish_distill(const DistillParams& p, int64_t row, Sums sums,
+                                                const Named& n, const Teacher& t, int lane) {
+    float m = sums.m, s = sums.s;
+    if (p.mode == WS_DISTILL_TAIL) {
+        m = fmaxf(m, wave_max(fmaxf(n.z[0], n.z[1]), lane));
+        float e = 0.0f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            if (n.first[h]) e += __builtin_amdgcn_exp2f((n.z[h] - m) * p.c);
+        s = (s == 0.0f ? 0.0f : s * __builtin_amdgcn_exp2f((sums.m - m) * p.c)) + wave_sum(e, lane);
+    }
+    const bool empty = s == 0.0f;
+    const double logsum = empty ? -(double)INFINITY : log((double)s);
+    double tail = -(double)INFINITY;
+    if (p.mode == WS_DISTILL_TAIL && sums.s != 0.0f)
+        tail = ((double)sums.m - (double)m) * p.inv_tau + log((double)sums.s) - logsum;
+    double loss = 0.0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if (t.q[h] == 0.0) continue;
+        const double logp = empty ? -(double)INFINITY
+                                  : ((double)n.z[h] - (double)m) * p.inv_tau - logsum;
+        loss += t.q[h] * (t.logq[h] - logp);
+    }
+    loss = wave_sum_d(loss, lane);
+    if (t.rest > 0.0) loss += t.rest * (log(t.rest) - tail);
+    if (lane == 0) {
+        p.loss[row] = n.bad ? NAN : (float)loss;
+        if (p.stats) p.stats[row] = {empty ? -INFINITY : m, (float)logsum};
+        if (p.tail) p.tail[row] = (float)tail;
+    }
+    return distill_slope(t, n.bad, m, logsum, tail,
+                         p.grad_loss ? p.grad_loss[row] * p.inv_tau : 0.0f);
+}
+
+// Marks the listed tokens of a part, one bit an element, one byte a slot;
+// `words` words of marks, which reach past the part's slots as far as a batch
+// of the pass does.
+template <typename L, int NT>
+__device__ __forceinline__ void mark_listed(const Part<L>& part, const Named& n, uint32_t* mask,
+                                            int words) {
+    for (int i = threadIdx.x; i < words; i += NT) mask[i] = 0;
+    __syncthreads();
+    if (threadIdx.x < 64) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (n.id[h] >= (uint32_t)part.vocab) continue;
+            const int e = (int)n.id[h] - part.e0;
+            if (e < 0 || e >= part.n * L::VEC) continue;
+            const int slot = e / L::VEC;
+            atomicOr(&mask[slot >> 2], 1u << ((slot & 3) * 8 + e % L::VEC));
+        }
+    }
+    __syncthreads();
+}
+
+// Dynamic LDS of a part with `slots` slots: its marks.
+extern __shared__ __align__(16) uint32_t listed_marks[];
+
+template <typename L, int NT, bool TAIL>
+__global__ void __launch_bounds__(NT) distill_kernel(DistillParams p) {
+    __shared__ Sums wave_sums[NT / 64];
+    __shared__ __align__(16) uint32_t ids[WS_DISTILL_MAX_K];
+    __shared__ float adds[WS_DISTILL_MAX_K];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int64_t row = blockIdx.x / (uint32_t)p.parts;
+    Part<L> part;
+    part.init(p.logits, row * p.stride, p.vocab, p.chunk, p.parts,
+              (int)(blockIdx.x % (uint32_t)p.parts));
+    Named n;
+    Teacher t;
+    if (tid < 64) {
+        if (p.parts == 1) {
+            t = read_teacher(n, p.teacher + row * p.k, p.k, p.mode, lane);
+            read_named<L>(n, part.row, p.vocab);
+        } else if constexpr (TAIL) {
+            read_ids(n, p.teacher + row * p.k, p.k, lane);
+        }
+    }
+    if constexpr (TAIL) mark_listed<L, NT>(part, n, listed_marks, p.mark_words);
+    Sums a;
+    SlotTrack unused;
+    stream_part<L, NT, false, false, TAIL>(part, p.c, reinterpret_cast<const uint8_t*>(listed_marks),
+                                           a, unused);
+    a = group_join<NT, false>(a, p.c, wave_sums);
+    if (p.parts > 1) {
+        if (tid == 0) p.sums[blockIdx.x] = a;
+    } else if (tid < 64) {
+        if constexpr (TAIL) {
+            merge_named(n, p.k, ids, adds, lane);
+            settle_rest(t, n, p.k, p.vocab);
+        }
+        finish_distill(p, row, a, n, t, lane);
+    }
+}
+
+template <typename L>
+__global__ void __launch_bounds__(64) distill_join_kernel(DistillParams p) {
+    __shared__ __align__(16) uint32_t ids[WS_DISTILL_MAX_K];
+    __shared__ float adds[WS_DISTILL_MAX_K];
+    const int lane = threadIdx.x;
     const int64_t row = blockIdx.x;
-    const int64_t at = row * p.stride, to = row * p.grad_stride;
+    Sums a;
+    a.init();
+    if (lane < p.parts) a = p.sums[row * p.parts + lane];
+    Named n;
+    Teacher t = read_teacher(n, p.teacher + row * p.k, p.k, p.mode, lane);
+    read_named<L>(n, static_cast<const typename L::Elem*>(p.logits) + row * p.stride, p.vocab);
+    if (p.mode == WS_DISTILL_TAIL) {
+        merge_named(n, p.k, ids, adds, lane);
+        settle_rest(t, n, p.k, p.vocab);
+    }
+    finish_distill(p, row, wave_join<false>(a, p.c, lane), n, t, lane);
+}
+
+// ---------------------------------------------------------------------------
+// Gradients.
+
+// Where a part's gradient goes: slots at the same place as the logits' slots
+// when both rows start alike relative to 16 bytes, else element by element.
+template <typename L>
+struct PartOut {
+    typename L::Elem* row;
+    char* base;
+    bool slots;
+
+    __device__ __forceinline__ void init(const Part<L>& part, void* grad, int64_t at) {
+        row = static_cast<typename L::Elem*>(grad) + at;
+        slots = (((uintptr_t)row ^ (uintptr_t)part.row) & 15u) == 0;
+        base = reinterpret_cast<char*>(row + part.e0);
+    }
+    __device__ __forceinline__ void store(const Part<L>& part, int s,
+                                          const float (&v)[L::VEC]) const {
+        if (slots && part.whole(s)) {
+            *reinterpret_cast<uint4*>(base + (uint32_t)s * 16u) = L::pack(v);
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < L::VEC; ++j) {
+            const int e = part.e0 + s * L::VEC + j;
+            if (e >= 0 && e < part.vocab) row[e] = L::down(v[j]);
+        }
+    }
+};
+
+template <typename L, bool ENT>
+__device__ __forceinline__ void slope_values(const Slope& g, float c, float (&v)[L::VEC]) {
+    const float a = g.a * g.scale, b = g.b * g.scale;
+#pragma unroll
+    for (int j = 0; j < L::VEC; ++j) {
+        const float t = fmaf(v[j] - g.max, c, -g.base);
+        const float prob = __builtin_amdgcn_exp2f(t);
+        if constexpr (ENT) v[j] = prob * fmaf(b, fmaxf(t, kFar), a);
+        else v[j] = prob * a;
+        if (g.zero) v[j] = 0.0f;
+    }
+}
+
+// The named tokens' values, written over what the pass left for them.
+template <typename L, bool ENT, bool DISTILL>
+__device__ __forceinline__ void store_named(const Slope& g, const Named& n, float c, int from,
+                                            int to, typename L::Elem* row) {
+    if (g.zero) return;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if (!n.first[h] || n.id[h] < (uint32_t)from || n.id[h] >= (uint32_t)to) continue;
+        const float t = fmaf(n.z[h] - g.max, c, -(DISTILL ? g.base_listed : g.base));
+        float a = DISTILL ? g.a_listed : g.a;
+        if constexpr (ENT) a = fmaf(g.b, fmaxf(t, kFar), a);
+        row[n.id[h]] = L::down((__builtin_amdgcn_exp2f(t) * a + n.add[h]) * g.scale);
+    }
+}
+
+struct GradParams {
+    const void* logits;
+    void* grad;
+    int64_t stride, grad_stride;
+    const ws_row_stats* stats;
+    const ws_topk_entry* entries;   // alternatives, or the teacher's entries
+    const float* grad_entries;      // [rows][k], upstream of the alternatives
+    const int32_t* targets;
+    const float* grad_target;
+    const float* entropy;
+    const float* grad_entropy;
+    const float* tail;              // distillation
+    const float* grad_loss;
+    int32_t vocab, k, mode;
+    int32_t chunk, parts;
+    float c, inv_tau;
+};
+
+// The row's slope and named tokens, by wave 0.
+template <typename L, bool DISTILL>
+__device__ __forceinline__ Slope grad_slope(const GradParams& p, int64_t row,
+                                            const typename L::Elem* z, Named& n, uint32_t* ids,
+                                            float* adds, int lane) {
     const ws_row_stats st = p.stats[row];
-    if (st.logsum == -INFINITY) {
-        for (int j = threadIdx.x; j < p.vocab; j += kThreads) lstore<L>(p.grad, to + j, 0.0f);
-        return;
-    }
-    float a = 0.0f, b = 0.0f, scale = p.inv_tau;
-    int target = -1;
-    float gt = 0.0f;
-    // log2 of the sum that p's exponent is measured against.  An unlisted token
-    // of a row with a tail uses the unlisted tokens' own, so that a tail too
-    // small for FP32 still divides: p_j (M - q_t / p_t) = p_j / p_t (M p_t - q_t).
-    float base = st.logsum * kLog2e;
-    const float listed_base = base;
-    float a_listed = 0.0f;
     if constexpr (DISTILL) {
-        read_teacher(p.entries + row * p.k, p.k, p.mode, p.vocab, &t);
-        a = a_listed = (float)t.mass;
-        if (p.mode == WS_DISTILL_TAIL && t.rest > 0.0) {
-            const double tail = (double)p.tail[row];
-            a = tail == -INFINITY ? 0.0f : (float)(t.mass * exp(tail) - t.rest);
-            if (tail != -INFINITY) base = (float)(((double)st.logsum + tail) * 1.4426950408889634074);
+        Teacher t = read_teacher(n, p.entries + row * p.k, p.k, p.mode, lane);
+        read_named<L>(n, z, p.vocab);
+        merge_named(n, p.k, ids, adds, lane);
+        double tail = 0.0;
+        if (p.mode == WS_DISTILL_TAIL) {
+            settle_rest(t, n, p.k, p.vocab);
+            tail = (double)p.tail[row];
         }
-        scale *= p.grad_loss[row];
-        if (t.bad) a = NAN;
+        return distill_slope(t, n.bad, st.max, (double)st.logsum, tail,
+                             p.grad_loss[row] * p.inv_tau);
     } else {
-        for (int i = threadIdx.x; i < p.k; i += kThreads)
-            t.ids[i] = (uint32_t)p.entries[row * p.k + i].index;
-        __syncthreads();
-        for (int i = 0; i < p.k; ++i) {
-            if (t.ids[i] == 0xffffffffu) continue;
-            a -= p.grad_entries[row * p.k + i];
-            if (t.ids[i] >= (uint32_t)p.vocab) a = NAN;
+        n.id[0] = n.id[1] = kAbsent;
+        n.add[0] = n.add[1] = 0.0f;
+        if (lane < p.k) {
+            n.id[0] = (uint32_t)p.entries[row * p.k + lane].index;
+            if (n.id[0] != kAbsent) n.add[0] = p.grad_entries[row * p.k + lane];
+        } else if (lane == p.k && p.targets) {
+            n.id[0] = (uint32_t)p.targets[row];
+            if (n.id[0] != kAbsent) n.add[0] = p.grad_target[row];
         }
-        if (p.targets) {
-            target = p.targets[row];
-            if (target != -1) {
-                gt = p.grad_target[row];
-                a -= gt;
-                if (target < 0 || target >= p.vocab) a = NAN;
-            }
-        }
+        read_named<L>(n, z, p.vocab);
+        Slope s;
+        s.max = st.max;
+        s.base = s.base_listed = st.logsum * kLog2e;
+        s.a = -wave_sum(n.add[0], lane);
+        s.b = 0.0f;
         if (p.entropy) {
+            // log p_j = log2 p_j log 2
             const float gh = p.grad_entropy[row];
-            b = -gh;
-            a -= gh * p.entropy[row];
+            s.b = -gh * 0.69314718055994530942f;
+            s.a -= gh * p.entropy[row];
+        }
+        if (n.bad) s.a = NAN;
+        s.a_listed = s.a;
+        s.scale = p.inv_tau;
+        s.zero = st.logsum == -INFINITY;
+        merge_named(n, p.k + 1, ids, adds, lane);
+        return s;
+    }
+}
+
+template <typename L, bool ENT, bool DISTILL>
+__global__ void __launch_bounds__(256) grad_kernel(GradParams p) {
+    constexpr int NT = 256, VEC = L::VEC;
+    __shared__ __align__(16) uint32_t ids[WS_DISTILL_MAX_K];
+    __shared__ float adds[WS_DISTILL_MAX_K];
+    __shared__ Slope slope;
+    const int tid = threadIdx.x;
+    const int64_t row = blockIdx.x / (uint32_t)p.parts;
+    Part<L> part;
+    part.init(p.logits, row * p.stride, p.vocab, p.chunk, p.parts,
+              (int)(blockIdx.x % (uint32_t)p.parts));
+    PartOut<L> out;
+    out.init(part, p.grad, row * p.grad_stride);
+    Named n;
+    if (tid < 64) {
+        const Slope s = grad_slope<L, DISTILL>(p, row, part.row, n, ids, adds, tid);
+        if (tid == 0) slope = s;
+    }
+    __syncthreads();   // every named logit is read before any is overwritten
+    const Slope g = slope;
+    for (int s = tid; s < part.n; s += kBatch * NT) {
+        float v[kBatch][VEC];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            if (s + i * NT < part.n) part.load_any(s + i * NT, v[i]);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            if (s + i * NT >= part.n) break;
+            slope_values<L, ENT>(g, p.c, v[i]);
+            out.store(part, s + i * NT, v[i]);
         }
     }
-    for (int j = threadIdx.x; j < p.vocab; j += kThreads) {
-        const float d = lload<L>(p.logits, at + j) - st.max;
-        float v = a;
-        if (b != 0.0f) v += b * fmaxf(d * p.inv_tau - st.logsum, kFar);
-        float extra = 0.0f;
-        bool named = false;
-        for (int i = 0; i < p.k; ++i)
-            if (t.ids[i] == (uint32_t)j) {
-                named = true;
-                extra += DISTILL ? -(float)t.q[i] : p.grad_entries[row * p.k + i];
-            }
-        if (DISTILL && named) v = a_listed;
-        const float prob =
-            __builtin_amdgcn_exp2f(d * p.c - (DISTILL && named ? listed_base : base));
-        if (!DISTILL && j == target) extra += gt;
-        v = prob * v + extra;
-        lstore<L>(p.grad, to + j, v * scale);
+    __syncthreads();
+    if (tid < 64) {
+        const int from = part.e0 < 0 ? 0 : part.e0;
+        const int to = part.e0 + part.n * VEC;
+        store_named<L, ENT, DISTILL>(g, n, p.c, from, to, out.row);
     }
+}
+
+// Loss and gradient of a row in one pass: the row stays in the registers of
+// its workgroup (R slots a thread), so it is read once.
+constexpr int kHeld = kHeldSlots;
+
+// Has the compiler work a value out again where it is used again, rather than
+// hold what it derived the first time (a slot's elements, sixteen lane masks).
+__device__ __forceinline__ void forget(uint4& w) {
+    asm volatile("" : "+v"(w.x), "+v"(w.y), "+v"(w.z), "+v"(w.w));
+}
+__device__ __forceinline__ int forget(int v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
+template <typename L, int NT, bool TAIL>
+__global__ void __launch_bounds__(NT) distill_step_kernel(DistillParams p) {
+    constexpr int VEC = L::VEC, R = kHeld, B = 2;
+    __shared__ Sums wave_sums[NT / 64];
+    __shared__ __align__(16) uint32_t ids[WS_DISTILL_MAX_K];
+    __shared__ float adds[WS_DISTILL_MAX_K];
+    __shared__ Slope slope;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int64_t row = blockIdx.x;
+    Part<L> part;
+    part.init(p.logits, row * p.stride, p.vocab, p.chunk, 1, 0);
+    PartOut<L> out;
+    out.init(part, p.grad, row * p.grad_stride);
+    // Slots that lie in the row whole; those that stick out, and -inf beyond.
+    uint4 w[R];
+    float v[VEC];
+    part.load_edge(part.n, v);
+    const uint4 none = L::pack(v);
+    part.load_edge(0, v);
+    const uint4 front = L::pack(v);
+    part.load_edge(part.n - 1, v);
+    const uint4 rear = L::pack(v);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int s = tid + i * NT;
+        w[i] = s == part.n - 1 ? rear : none;
+        if (i == 0 && s == 0) w[i] = front;
+        if (part.whole(s)) w[i] = part.load(s);
+    }
+    Named n;
+    if constexpr (TAIL) {
+        if (tid < 64) read_ids(n, p.teacher + row * p.k, p.k, lane);
+        mark_listed<L, NT>(part, n, listed_marks, R * NT / 4);
+        // Listed tokens leave the held row for good: store_named writes theirs.
+        const uint8_t* marks = reinterpret_cast<const uint8_t*>(listed_marks);
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const uint32_t mark = marks[forget(tid) + i * NT];
+            if (__ballot(mark != 0) != 0) {
+                L::unpack(w[i], v);
+                hide_listed<VEC>(mark, v);
+                w[i] = L::pack(v);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+    Sums a;
+    SlotTrack unused;
+    a.init();
+#pragma unroll
+    for (int i = 0; i < R; i += B) {
+        float x[B][VEC];
+#pragma unroll
+        for (int j = 0; j < B; ++j) {
+            forget(w[i + j]);
+            L::unpack(w[i + j], x[j]);
+        }
+        take_slots<L, NT, false, false, false>(x, 0, p.c, nullptr, a, unused);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    a = group_join<NT, false>(a, p.c, wave_sums);
+    if (tid < 64) {
+        Teacher t = read_teacher(n, p.teacher + row * p.k, p.k, p.mode, lane);
+        read_named<L>(n, part.row, p.vocab);
+        merge_named(n, p.k, ids, adds, lane);
+        if constexpr (TAIL) settle_rest(t, n, p.k, p.vocab);
+        const Slope s = finish_distill(p, row, a, n, t, lane);
+        if (lane == 0) slope = s;
+    }
+    __syncthreads();   // every named logit is read before any is overwritten
+    const Slope g = slope;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int s = forget(tid) + i * NT;
+        forget(w[i]);
+        if (s < part.n) {
+            L::unpack(w[i], v);
+            slope_values<L, false>(g, p.c, v);
+            out.store(part, s, v);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    __syncthreads();
+    if (tid < 64) store_named<L, false, true>(g, n, p.c, 0, p.vocab, out.row);
 }
 
 // ---------------------------------------------------------------------------
@@ -664,12 +1004,13 @@ int device_ready(int32_t device) {
 
 // Enqueues one kernel; its parameters are one struct, copied by the call.
 template <typename P>
-int launch(void (*kernel)(P), int64_t groups, int threads, const P& params, hipStream_t s) {
+int launch(void (*kernel)(P), int64_t groups, int threads, const P& params, hipStream_t s,
+           size_t lds = 0) {
     P copy = params;
     void* args[] = {&copy};
     const hipError_t e =
         hipLaunchKernel(reinterpret_cast<const void*>(kernel), dim3((uint32_t)groups),
-                        dim3((uint32_t)threads), args, 0, s);
+                        dim3((uint32_t)threads), args, lds, s);
     return e == hipSuccess ? WS_OK : WS_E_HIP;
 }
 
@@ -695,8 +1036,49 @@ int run_logprobs(const ws_rows& r, const LogprobsPlan& plan, const LogprobsParam
 float scale_c(const ws_rows& r) { return (float)(1.4426950408889634074 / (double)r.temperature); }
 float scale_inv(const ws_rows& r) { return (float)(1.0 / (double)r.temperature); }
 
-int run_distill_grad(const ws_rows& r, const GradParams& g, hipStream_t s) {
-#define CALL(L) return launch(grad_kernel<L, true>, r.rows, kThreads, g, s)
+template <typename L>
+int run_grad(const ws_rows& r, GradParams g, bool distill, hipStream_t s) {
+    const GradPlan plan = plan_grad(r);
+    g.chunk = plan.chunk;
+    g.parts = plan.parts;
+    const auto kernel = distill ? grad_kernel<L, false, true>
+                                : (g.entropy ? grad_kernel<L, true, false>
+                                             : grad_kernel<L, false, false>);
+    return launch(kernel, (int64_t)r.rows * plan.parts, 256, g, s);
+}
+
+template <typename L, bool TAIL>
+int run_distill(const ws_rows& r, const DistillPlan& plan, const DistillParams& p, hipStream_t s) {
+    const size_t lds = TAIL ? (size_t)plan.mark_bytes : 0;
+    if (plan.held > 0) {
+        const auto kernel = plan.threads == 256   ? distill_step_kernel<L, 256, TAIL>
+                            : plan.threads == 512 ? distill_step_kernel<L, 512, TAIL>
+                                                  : distill_step_kernel<L, 1024, TAIL>;
+        return launch(kernel, r.rows, plan.threads, p, s, lds);
+    }
+    const int v = launch(plan.threads == 64 ? distill_kernel<L, 64, TAIL>
+                                            : distill_kernel<L, 256, TAIL>,
+                         (int64_t)r.rows * plan.parts, plan.threads, p, s, lds);
+    if (v != WS_OK || plan.parts == 1) return v;
+    return launch(distill_join_kernel<L>, r.rows, 64, p, s);
+}
+
+int enqueue_distill_grad(const ws_rows& r, const ws_distill_grad_args& a, hipStream_t s) {
+    GradParams g{};
+    g.logits = a.logits;
+    g.grad = a.grad_logits;
+    g.stride = r.row_stride;
+    g.grad_stride = a.grad_stride;
+    g.stats = a.stats;
+    g.entries = a.teacher;
+    g.tail = a.tail;
+    g.grad_loss = a.grad_loss;
+    g.vocab = r.vocab;
+    g.k = a.teacher_k;
+    g.mode = a.mode;
+    g.c = scale_c(r);
+    g.inv_tau = scale_inv(r);
+#define CALL(L) return run_grad<L>(r, g, true, s)
     WS_BY_DTYPE(r.dtype, CALL);
 #undef CALL
 }
@@ -771,7 +1153,7 @@ extern "C" int ws_logprobs_grad(const ws_rows* rows, const ws_logprobs_grad_args
     g.c = ws::scale_c(r);
     g.inv_tau = ws::scale_inv(r);
     const hipStream_t s = static_cast<hipStream_t>(stream);
-#define CALL(L) return ws::launch(ws::grad_kernel<ws::L, false>, r.rows, ws::kThreads, g, s)
+#define CALL(L) return ws::run_grad<ws::L>(r, g, false, s)
     WS_BY_DTYPE(r.dtype, CALL);
 #undef CALL
 }
@@ -782,7 +1164,7 @@ extern "C" int ws_distill_workspace(const ws_rows* rows, int32_t mode, int32_t g
     if (v != WS_OK) return v;
     if (!bytes || ws::validate_teacher(1, mode) != WS_OK || (gradient != 0 && gradient != 1))
         return WS_E_INVALID_ARG;
-    *bytes = ws::distill_workspace_bytes(*rows, mode, gradient == 1);
+    *bytes = ws::plan_distill(*rows, mode, gradient == 1, false).workspace;
     return WS_OK;
 }
 
@@ -792,39 +1174,56 @@ extern "C" int ws_distill(const ws_rows* rows, const ws_distill_args* args, void
     const ws_rows& r = *rows;
     if (r.rows == 0) return WS_OK;
     const bool gradient = args->grad_logits != nullptr;
-    v = ws::validate_workspace(args->workspace, args->workspace_bytes,
-                               ws::distill_workspace_bytes(r, args->mode, gradient));
+    const ws::DistillPlan plan =
+        ws::plan_distill(r, args->mode, gradient, ws::rows_aligned(r, args->logits));
+    v = ws::validate_workspace(args->workspace, args->workspace_bytes, plan.workspace);
     if (v != WS_OK) return v;
     v = ws::device_ready(r.device);
     if (v != WS_OK) return v;
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    ws::DistillParams p{args->logits, r.row_stride, args->teacher, args->loss, args->stats,
-                        args->tail, r.vocab, args->teacher_k, args->mode, ws::scale_c(r),
-                        ws::scale_inv(r)};
-    if (gradient) {
-        if (!p.stats) p.stats = static_cast<ws_row_stats*>(args->workspace);
-        if (!p.tail)
-            p.tail = reinterpret_cast<float*>(static_cast<ws_row_stats*>(args->workspace) + r.rows);
+    ws::DistillParams p{};
+    p.logits = args->logits;
+    p.stride = r.row_stride;
+    p.teacher = args->teacher;
+    p.loss = args->loss;
+    p.stats = args->stats;
+    p.tail = args->tail;
+    p.vocab = r.vocab;
+    p.k = args->teacher_k;
+    p.mode = args->mode;
+    p.chunk = plan.chunk;
+    p.parts = plan.parts;
+    p.mark_words = plan.mark_bytes / 4;
+    p.c = ws::scale_c(r);
+    p.inv_tau = ws::scale_inv(r);
+    char* space = static_cast<char*>(args->workspace);
+    if (plan.parts > 1) p.sums = reinterpret_cast<ws::Sums*>(space + plan.sums_at);
+    if (plan.held > 0) {
+        p.grad_loss = args->grad_loss;
+        p.grad = args->grad_logits;
+        p.grad_stride = args->grad_stride;
+    } else if (gradient) {
+        // The loss first, then its gradient from the statistics it leaves.
+        if (!p.stats) p.stats = reinterpret_cast<ws_row_stats*>(space);
+        if (!p.tail) p.tail = reinterpret_cast<float*>(space + plan.tail_at);
     }
-#define CALL(L) v = ws::launch(ws::distill_kernel<ws::L>, r.rows, ws::kThreads, p, s)
+#define CALL(L)                                                                       \
+    v = args->mode == WS_DISTILL_TAIL ? ws::run_distill<ws::L, true>(r, plan, p, s)   \
+                                      : ws::run_distill<ws::L, false>(r, plan, p, s)
     WS_BY_DTYPE(r.dtype, CALL);
 #undef CALL
-    if (v != WS_OK || !gradient) return v;
-    ws::GradParams g{};
+    if (v != WS_OK || !gradient || plan.held > 0) return v;
+    ws_distill_grad_args g{};
     g.logits = args->logits;
-    g.grad = args->grad_logits;
-    g.stride = r.row_stride;
-    g.grad_stride = args->grad_stride;
+    g.teacher = args->teacher;
     g.stats = p.stats;
-    g.entries = args->teacher;
     g.tail = p.tail;
     g.grad_loss = args->grad_loss;
-    g.vocab = r.vocab;
-    g.k = args->teacher_k;
+    g.grad_logits = args->grad_logits;
+    g.grad_stride = args->grad_stride;
+    g.teacher_k = args->teacher_k;
     g.mode = args->mode;
-    g.c = p.c;
-    g.inv_tau = p.inv_tau;
-    return ws::run_distill_grad(r, g, s);
+    return ws::enqueue_distill_grad(r, g, s);
 }
 
 extern "C" int ws_distill_grad(const ws_rows* rows, const ws_distill_grad_args* args,
@@ -834,20 +1233,5 @@ extern "C" int ws_distill_grad(const ws_rows* rows, const ws_distill_grad_args* 
     if (rows->rows == 0) return WS_OK;
     v = ws::device_ready(rows->device);
     if (v != WS_OK) return v;
-    const ws_rows& r = *rows;
-    ws::GradParams g{};
-    g.logits = args->logits;
-    g.grad = args->grad_logits;
-    g.stride = r.row_stride;
-    g.grad_stride = args->grad_stride;
-    g.stats = args->stats;
-    g.entries = args->teacher;
-    g.tail = args->tail;
-    g.grad_loss = args->grad_loss;
-    g.vocab = r.vocab;
-    g.k = args->teacher_k;
-    g.mode = args->mode;
-    g.c = ws::scale_c(r);
-    g.inv_tau = ws::scale_inv(r);
-    return ws::run_distill_grad(r, g, static_cast<hipStream_t>(stream));
+    return ws::enqueue_distill_grad(*rows, *args, static_cast<hipStream_t>(stream));
 }

@@ -175,12 +175,86 @@ inline LogprobsPlan plan_logprobs(const ws_rows& r, int32_t top_k) {
     return p;
 }
 
-// ws_distill with a gradient runs the loss kernel, then the gradient kernel
-// from the row statistics and tails it left here.
-inline size_t distill_workspace_bytes(const ws_rows& r, int32_t mode, bool gradient) {
-    if (!gradient) return 0;
-    (void)mode;
-    return (size_t)r.rows * (sizeof(ws_row_stats) + sizeof(float));
+// Gradients: parts of a row as above, each workgroup reading the row's named
+// tokens for itself.
+constexpr int kGradChunk = 4096;
+
+struct GradPlan {
+    int32_t parts = 1;
+    int32_t chunk = 0;
+};
+
+inline GradPlan plan_grad(const ws_rows& r) {
+    GradPlan p;
+    const int64_t slots = slots_of(r);
+    int64_t parts = (slots + kGradChunk - 1) / kGradChunk;
+    int64_t want = (2048 + r.rows - 1) / r.rows;
+    if (want > slots / 256) want = slots / 256;
+    if (parts < want) parts = want;
+    p.chunk = (int32_t)((slots + parts - 1) / parts);
+    p.parts = (int32_t)((slots + p.chunk - 1) / p.chunk);
+    return p;
+}
+
+// ws_distill: the loss as ws_logprobs splits its rows, with a limit to a part
+// from the marks of the listed tokens in LDS (a byte a slot); with a gradient,
+// rows that fit the registers of one workgroup (`held` slots a thread) are done
+// in one kernel, others by the loss and then the gradient.
+constexpr int kBatchSlots = 4;      // slots a thread has in flight in a pass
+constexpr int kHeldSlots = 16;
+constexpr int kMaxMarkedSlots = 32768;
+
+struct DistillPlan {
+    int32_t threads = 256;
+    int32_t held = 0;
+    int32_t parts = 1;
+    int32_t chunk = 0;
+    int32_t mark_bytes = 0;
+    size_t tail_at = 0, sums_at = 0;   // offsets in the workspace
+    size_t workspace = 0;
+};
+
+// Whether every row starts on 16 bytes.
+inline bool rows_aligned(const ws_rows& r, const void* logits) {
+    return aligned_to(logits, 16) &&
+           (r.rows == 1 || (r.row_stride * logit_bytes(r.dtype)) % 16 == 0);
+}
+
+// aligned: as rows_aligned says; without it a row may take one slot more, and
+// the workspace (which is asked for before the rows' address is known) is at
+// least that of aligned rows.
+inline DistillPlan plan_distill(const ws_rows& r, int32_t mode, bool gradient, bool aligned) {
+    DistillPlan p;
+    if (r.rows == 0) return p;
+    const int64_t slots = slots_of(r);
+    const int64_t most = slots + (aligned ? 0 : 1);
+    if (gradient && most <= kHeldSlots * 1024 && r.rows >= 128) {
+        p.held = kHeldSlots;
+        p.threads = most <= kHeldSlots * 256 ? 256 : most <= kHeldSlots * 512 ? 512 : 1024;
+        p.chunk = (int32_t)slots;
+    } else {
+        p.threads = slots <= 256 ? 64 : 256;
+        int64_t parts = (512 + r.rows - 1) / r.rows;
+        if (parts > slots / 256) parts = slots / 256;
+        if (parts > kMaxRowParts) parts = kMaxRowParts;
+        if (parts < 1) parts = 1;
+        if (mode == WS_DISTILL_TAIL && parts * (kMaxMarkedSlots - 1) < slots)
+            parts = (slots + kMaxMarkedSlots - 2) / (kMaxMarkedSlots - 1);
+        p.chunk = (int32_t)((slots + parts - 1) / parts);
+        p.parts = (int32_t)((slots + p.chunk - 1) / p.chunk);
+        if (gradient) {
+            p.tail_at = (size_t)r.rows * sizeof(ws_row_stats);
+            p.sums_at = p.tail_at + (size_t)r.rows * sizeof(float);
+        }
+        p.workspace = p.sums_at;
+        if (p.parts > 1) p.workspace += (size_t)r.rows * (size_t)p.parts * 12u;
+    }
+    // A byte a slot: the part's, and past them what a batch of kBatchSlots
+    // slots a thread reaches.
+    if (mode == WS_DISTILL_TAIL)
+        p.mark_bytes = p.held > 0 ? p.held * p.threads
+                                  : (p.chunk + 1 + kBatchSlots * p.threads + 15) / 16 * 16;
+    return p;
 }
 
 }  // namespace ws

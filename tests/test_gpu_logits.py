@@ -68,7 +68,7 @@ class Matrix:
         self.dtype = dtype
         self.view = torch.as_strided(self.flat, (rows, V), (self.stride, 1), shift)
         if z.size:
-            self.view.copy_(torch.from_numpy(np.ascontiguousarray(z)).to(_dev()))
+            self.view.copy_(torch.from_numpy(np.array(z, order="C")).to(_dev()))
         self.z = self.view.double().cpu().numpy()
 
     def rows(self, tau=1.0):
@@ -632,6 +632,56 @@ def test_distill_special_rows(gpu_lib, mode, dtype, V):
     mat = Matrix(z, dtype)
     check_distill(mat, 1.0, ids, scores, mode, rng.random(len(z)))
     check_distill(Matrix(z, dtype), 1.0, ids, scores, mode, rng.random(len(z)), separate=True)
+
+
+@pytest.mark.parametrize("mode", [ol.RENORM, ol.TAIL])
+@pytest.mark.parametrize("dtype,V", [("f32", 900), ("f32", 20003), ("f32", 50001), ("f16", 5),
+                                     ("bf16", 9001), ("bf16", 40001), ("bf16", 70001),
+                                     ("bf16", 131072), ("bf16", 131073)])
+def test_distill_many_rows(gpu_lib, mode, dtype, V):
+    """Enough rows for a workgroup to hold a whole row, of each size of
+    workgroup, up to and past what it holds."""
+    import torch
+    rng = np.random.default_rng(V)
+    rows, few = 130, 5
+    z = np.broadcast_to(_logits(rng, few, V)[np.arange(rows) % few], (rows, V))
+    mat = Matrix(z, dtype, 1 if V == 9001 else 0, 3 if V == 9001 else 0)
+    k = min(V, 40)
+    ids, scores = make_teacher(rng, mat.z[:few], k, mode)
+    ids, scores = ids[np.arange(rows) % few].copy(), scores[np.arange(rows) % few]
+    ids[3, 0] = -1
+    ids[4, 0] = V - 1
+    ids[4, 1:] = np.where(ids[4, 1:] == V - 1, -1, ids[4, 1:])
+    g = np.arange(rows) + 1.0
+    loss, grad, _, _ = run_distill(mat, 1.2, ids, scores, mode, g)
+    # The first rows against the oracle, the others against the same row among them.
+    small = Matrix(z[:few], dtype)
+    check_distill(small, 1.2, ids[:few], scores[:few], mode, g[:few])
+    check_distill(mat, 1.2, ids, scores, mode, g, in_place=True) if V < 10000 else None
+    sub, subgrad, _, _ = run_distill(small, 1.2, ids[:few], scores[:few], mode, g[:few])
+    half = HALF[dtype]
+    np.testing.assert_allclose(loss[:few], sub, rtol=2 * _sum_tol(V), atol=2 * _sum_tol(V) * 20)
+    for r in range(few):
+        peak = np.abs(subgrad[r]).max()
+        # Two sums of one row in different orders, then two roundings.
+        np.testing.assert_allclose(grad[r], subgrad[r], rtol=2.1 * half + 4 * _sum_tol(V),
+                                   atol=8 * _sum_tol(V) * peak + 2 * SMALLEST[dtype])
+    for r in (few + 1, rows - 1):
+        np.testing.assert_allclose(loss[r], loss[r % few] if r % few not in (3, 4) else loss[r],
+                                   rtol=1e-6)
+
+
+@pytest.mark.parametrize("mode", [ol.RENORM, ol.TAIL])
+@pytest.mark.parametrize("dtype,V", [("f32", 300), ("f16", 2500), ("bf16", 9001), ("bf16", 40000)])
+def test_distill_many_special_rows(gpu_lib, mode, dtype, V):
+    """The special rows among enough others for a workgroup to hold a row."""
+    rng = np.random.default_rng(V + 1)
+    special = special_rows(V, dtype)
+    z = np.concatenate([special] + [_logits(rng, 130 - len(special), V)])
+    ids, scores = make_teacher(rng, z[:20], 4, mode)
+    ids, scores = np.tile(ids, (7, 1))[:130], np.tile(scores, (7, 1))[:130]
+    mat = Matrix(z, dtype)
+    check_distill(mat, 1.0, ids, scores, mode, rng.random(130))
 
 
 @pytest.mark.parametrize("mode", [ol.RENORM, ol.TAIL])
