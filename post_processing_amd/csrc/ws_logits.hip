@@ -104,24 +104,16 @@ __device__ __forceinline__ void stream_part(const Part<L>& part, float c, const 
     for (; s < part.full_to; s += kBatch * NT) {
         float v[kBatch][VEC];
         uint4 w[kBatch];
-        if (s + (kBatch - 1) * NT < part.full_to) {
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) w[i] = part.load(s + i * NT);
+        for (int i = 0; i < kBatch; ++i) w[i] = part.load_near(s + i * NT);
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) L::unpack(w[i], v[i]);
-        } else {
+        for (int i = 0; i < kBatch; ++i) L::unpack(w[i], v[i]);
+        if (s + (kBatch - 1) * NT >= part.full_to) {
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i)
-                if (s + i * NT < part.full_to) w[i] = part.load(s + i * NT);
+            for (int i = 1; i < kBatch; ++i)
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                if (s + i * NT < part.full_to) {
-                    L::unpack(w[i], v[i]);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) v[i][j] = -INFINITY;
-                }
-            }
+                for (int j = 0; j < VEC; ++j)
+                    v[i][j] = s + i * NT < part.full_to ? v[i][j] : -INFINITY;
         }
         take_slots<L, NT, ENT, TOPK, MASK>(v, s, c, marks, a, t);
     }
@@ -425,6 +417,7 @@ struct Named {
     float z[2];        // its logit
     float add[2];      // what a gradient adds for the token, all its entries together
     bool first[2];     // the token's first entry
+    float score[2];    // a teacher's
     bool bad;          // some index lies outside the row (wave-uniform)
 };
 
@@ -486,36 +479,30 @@ struct Teacher {
     double rest;   // q_t
 };
 
-// The entries' indices alone.
-__device__ __forceinline__ void read_ids(Named& n, const ws_topk_entry* entries, int k, int lane) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-        n.id[h] = lane + 64 * h < k ? (uint32_t)entries[lane + 64 * h].index : kAbsent;
-}
-
-__device__ __forceinline__ Teacher read_teacher(Named& n, const ws_topk_entry* entries, int k,
-                                                int mode, int lane) {
-    Teacher t;
-    float score[2];
+__device__ __forceinline__ void read_entries(Named& n, const ws_topk_entry* entries, int k,
+                                             int lane) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const int i = lane + 64 * h;
         n.id[h] = kAbsent;
-        score[h] = -INFINITY;
-        if (i < k) {
-            const ws_topk_entry e = entries[i];
+        n.score[h] = -INFINITY;
+        if (lane + 64 * h < k) {
+            const ws_topk_entry e = entries[lane + 64 * h];
             n.id[h] = (uint32_t)e.index;
-            if (n.id[h] != kAbsent) score[h] = e.score;
+            if (n.id[h] != kAbsent) n.score[h] = e.score;
         }
     }
+}
+
+__device__ __forceinline__ Teacher weigh_teacher(Named& n, int k, int mode, int lane) {
+    Teacher t;
     double shift = 0.0;
     if (mode == WS_DISTILL_RENORM) {
-        const float high = wave_max(fmaxf(score[0], score[1]), lane);
+        const float high = wave_max(fmaxf(n.score[0], n.score[1]), lane);
         if (high != -INFINITY) shift = (double)high;
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        t.logq[h] = (double)score[h] - shift;
+        t.logq[h] = (double)n.score[h] - shift;
         t.q[h] = h == 0 || k > 64 ? exp(t.logq[h]) : 0.0;
     }
     const double sum = wave_sum_d(t.q[0] + t.q[1], lane);
@@ -538,6 +525,51 @@ __device__ __forceinline__ Teacher read_teacher(Named& n, const ws_topk_entry* e
     n.add[1] = -(float)t.q[1];
     return t;
 }
+
+// Wave 0's teacher and named tokens put aside in LDS while it streams its
+// share of the row.
+struct Aside {
+    double q[WS_DISTILL_MAX_K], logq[WS_DISTILL_MAX_K];
+    float z[WS_DISTILL_MAX_K], add[WS_DISTILL_MAX_K];
+    uint32_t id[WS_DISTILL_MAX_K];
+    uint32_t first[WS_DISTILL_MAX_K];
+    double mass, rest;
+    uint32_t bad;
+
+    __device__ __forceinline__ void put(const Named& n, const Teacher& t, int lane) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int i = lane + 64 * h;
+            q[i] = t.q[h];
+            logq[i] = t.logq[h];
+            z[i] = n.z[h];
+            add[i] = n.add[h];
+            id[i] = n.id[h];
+            first[i] = n.first[h];
+        }
+        if (lane == 0) {
+            mass = t.mass;
+            rest = t.rest;
+            bad = n.bad;
+        }
+        wave_lds_sync();
+    }
+    __device__ __forceinline__ void get(Named& n, Teacher& t, int lane) const {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int i = lane + 64 * h;
+            t.q[h] = q[i];
+            t.logq[h] = logq[i];
+            n.z[h] = z[i];
+            n.add[h] = add[i];
+            n.id[h] = id[i];
+            n.first[h] = first[i] != 0;
+        }
+        t.mass = mass;
+        t.rest = rest;
+        n.bad = bad != 0;
+    }
+};
 
 // With WS_DISTILL_TAIL, once merge_named has run: a list that names every
 // token leaves no rest.
@@ -678,11 +710,10 @@ __global__ void __launch_bounds__(NT) distill_kernel(DistillParams p) {
     Named n;
     Teacher t;
     if (tid < 64) {
+        read_entries(n, p.teacher + row * p.k, p.k, lane);
         if (p.parts == 1) {
-            t = read_teacher(n, p.teacher + row * p.k, p.k, p.mode, lane);
             read_named<L>(n, part.row, p.vocab);
-        } else if constexpr (TAIL) {
-            read_ids(n, p.teacher + row * p.k, p.k, lane);
+            t = weigh_teacher(n, p.k, p.mode, lane);
         }
     }
     if constexpr (TAIL) mark_listed<L, NT>(part, n, listed_marks, p.mark_words);
@@ -712,7 +743,8 @@ __global__ void __launch_bounds__(64) distill_join_kernel(DistillParams p) {
     a.init();
     if (lane < p.parts) a = p.sums[row * p.parts + lane];
     Named n;
-    Teacher t = read_teacher(n, p.teacher + row * p.k, p.k, p.mode, lane);
+    read_entries(n, p.teacher + row * p.k, p.k, lane);
+    Teacher t = weigh_teacher(n, p.k, p.mode, lane);
     read_named<L>(n, static_cast<const typename L::Elem*>(p.logits) + row * p.stride, p.vocab);
     if (p.mode == WS_DISTILL_TAIL) {
         merge_named(n, p.k, ids, adds, lane);
@@ -737,12 +769,19 @@ struct PartOut {
         slots = (((uintptr_t)row ^ (uintptr_t)part.row) & 15u) == 0;
         base = reinterpret_cast<char*>(row + part.e0);
     }
+    // A slot that lies in the row whole.
     __device__ __forceinline__ void store(const Part<L>& part, int s,
                                           const float (&v)[L::VEC]) const {
-        if (slots && part.whole(s)) {
+        if (slots) {
             *reinterpret_cast<uint4*>(base + (uint32_t)s * 16u) = L::pack(v);
             return;
         }
+        typename L::Elem* to = row + (part.e0 + s * L::VEC);
+#pragma unroll
+        for (int j = 0; j < L::VEC; ++j) to[j] = L::down(v[j]);
+    }
+    __device__ __forceinline__ void store_edge(const Part<L>& part, int s,
+                                               const float (&v)[L::VEC]) const {
 #pragma unroll
         for (int j = 0; j < L::VEC; ++j) {
             const int e = part.e0 + s * L::VEC + j;
@@ -804,8 +843,9 @@ __device__ __forceinline__ Slope grad_slope(const GradParams& p, int64_t row,
                                             float* adds, int lane) {
     const ws_row_stats st = p.stats[row];
     if constexpr (DISTILL) {
-        Teacher t = read_teacher(n, p.entries + row * p.k, p.k, p.mode, lane);
+        read_entries(n, p.entries + row * p.k, p.k, lane);
         read_named<L>(n, z, p.vocab);
+        Teacher t = weigh_teacher(n, p.k, p.mode, lane);
         merge_named(n, p.k, ids, adds, lane);
         double tail = 0.0;
         if (p.mode == WS_DISTILL_TAIL) {
@@ -865,16 +905,28 @@ __global__ void __launch_bounds__(256) grad_kernel(GradParams p) {
     }
     __syncthreads();   // every named logit is read before any is overwritten
     const Slope g = slope;
-    for (int s = tid; s < part.n; s += kBatch * NT) {
-        float v[kBatch][VEC];
+    const int whole_to = part.full_from < part.full_to ? part.full_to : 0;
+    for (int s = tid; s < whole_to; s += kBatch * NT) {
+        uint4 w[kBatch];
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i)
-            if (s + i * NT < part.n) part.load_any(s + i * NT, v[i]);
+        for (int i = 0; i < kBatch; ++i) w[i] = part.load_near(s + i * NT);
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
-            if (s + i * NT >= part.n) break;
-            slope_values<L, ENT>(g, p.c, v[i]);
-            out.store(part, s + i * NT, v[i]);
+            if (!part.whole(s + i * NT)) continue;
+            float v[VEC];
+            L::unpack(w[i], v);
+            slope_values<L, ENT>(g, p.c, v);
+            out.store(part, s + i * NT, v);
+        }
+    }
+    // The slots that stick out of the row.
+    if (tid < 2) {
+        const int s = tid == 0 ? 0 : part.n - 1;
+        if (!part.whole(s) && (tid == 0 || s > 0)) {
+            float v[VEC];
+            part.load_edge(s, v);
+            slope_values<L, ENT>(g, p.c, v);
+            out.store_edge(part, s, v);
         }
     }
     __syncthreads();
@@ -906,44 +958,39 @@ __global__ void __launch_bounds__(NT) distill_step_kernel(DistillParams p) {
     __shared__ __align__(16) uint32_t ids[WS_DISTILL_MAX_K];
     __shared__ float adds[WS_DISTILL_MAX_K];
     __shared__ Slope slope;
+    __shared__ Aside aside;
     const int tid = threadIdx.x, lane = tid & 63;
     const int64_t row = blockIdx.x;
     Part<L> part;
     part.init(p.logits, row * p.stride, p.vocab, p.chunk, 1, 0);
     PartOut<L> out;
     out.init(part, p.grad, row * p.grad_stride);
-    // Slots that lie in the row whole; those that stick out, and -inf beyond.
-    uint4 w[R];
-    float v[VEC];
-    part.load_edge(part.n, v);
-    const uint4 none = L::pack(v);
-    part.load_edge(0, v);
-    const uint4 front = L::pack(v);
-    part.load_edge(part.n - 1, v);
-    const uint4 rear = L::pack(v);
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-        const int s = tid + i * NT;
-        w[i] = s == part.n - 1 ? rear : none;
-        if (i == 0 && s == 0) w[i] = front;
-        if (part.whole(s)) w[i] = part.load(s);
-    }
+    // The teacher's entries before the row, as loads return in order.
     Named n;
-    if constexpr (TAIL) {
-        if (tid < 64) read_ids(n, p.teacher + row * p.k, p.k, lane);
-        mark_listed<L, NT>(part, n, listed_marks, R * NT / 4);
-        // Listed tokens leave the held row for good: store_named writes theirs.
-        const uint8_t* marks = reinterpret_cast<const uint8_t*>(listed_marks);
+    Teacher t;
+    if (tid < 64) {
+        read_entries(n, p.teacher + row * p.k, p.k, lane);
+        read_named<L>(n, part.row, p.vocab);
+    }
+    float v[VEC];
+    uint4 front, rear;   // slots that stick out of the row
+    if (part.full_from > 0) {
+        part.load_edge(0, v);
+        front = L::pack(v);
+    }
+    if (part.full_to < part.n) {
+        part.load_edge(part.n - 1, v);
+        rear = L::pack(v);
+    }
+    uint4 w[R];
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const uint32_t mark = marks[forget(tid) + i * NT];
-            if (__ballot(mark != 0) != 0) {
-                L::unpack(w[i], v);
-                hide_listed<VEC>(mark, v);
-                w[i] = L::pack(v);
-            }
-            __builtin_amdgcn_sched_barrier(0);
-        }
+    for (int i = 0; i < R; ++i) w[i] = part.load_near(tid + i * NT);
+    if constexpr (TAIL) mark_listed<L, NT>(part, n, listed_marks, R * NT / 4);
+    if (tid < 64) {   // while the row is on its way
+        t = weigh_teacher(n, p.k, p.mode, lane);
+        merge_named(n, p.k, ids, adds, lane);
+        if constexpr (TAIL) settle_rest(t, n, p.k, p.vocab);
+        aside.put(n, t, lane);
     }
     Sums a;
     SlotTrack unused;
@@ -953,6 +1000,25 @@ __global__ void __launch_bounds__(NT) distill_step_kernel(DistillParams p) {
         float x[B][VEC];
 #pragma unroll
         for (int j = 0; j < B; ++j) {
+            const int slot = forget(tid) + (i + j) * NT;
+            if (__ballot(!part.whole(slot)) != 0) {
+                const uint4 none = L::none();
+                uint4 x = slot < part.n ? w[i + j] : none;
+                if (slot < part.full_from) x = front;
+                if (slot >= part.full_to && slot < part.n) x = rear;
+                w[i + j] = x;
+            }
+            if constexpr (TAIL) {
+                // Listed tokens leave the held row for good: store_named
+                // writes theirs.
+                const uint8_t* marks = reinterpret_cast<const uint8_t*>(listed_marks);
+                const uint32_t mark = marks[slot];
+                if (__ballot(mark != 0) != 0) {
+                    L::unpack(w[i + j], v);
+                    hide_listed<VEC>(mark, v);
+                    w[i + j] = L::pack(v);
+                }
+            }
             forget(w[i + j]);
             L::unpack(w[i + j], x[j]);
         }
@@ -961,10 +1027,7 @@ __global__ void __launch_bounds__(NT) distill_step_kernel(DistillParams p) {
     }
     a = group_join<NT, false>(a, p.c, wave_sums);
     if (tid < 64) {
-        Teacher t = read_teacher(n, p.teacher + row * p.k, p.k, p.mode, lane);
-        read_named<L>(n, part.row, p.vocab);
-        merge_named(n, p.k, ids, adds, lane);
-        if constexpr (TAIL) settle_rest(t, n, p.k, p.vocab);
+        aside.get(n, t, lane);
         const Slope s = finish_distill(p, row, a, n, t, lane);
         if (lane == 0) slope = s;
     }
@@ -977,7 +1040,8 @@ __global__ void __launch_bounds__(NT) distill_step_kernel(DistillParams p) {
         if (s < part.n) {
             L::unpack(w[i], v);
             slope_values<L, false>(g, p.c, v);
-            out.store(part, s, v);
+            if (part.whole(s)) out.store(part, s, v);
+            else out.store_edge(part, s, v);
         }
         __builtin_amdgcn_sched_barrier(0);
     }

@@ -202,6 +202,7 @@ inline GradPlan plan_grad(const ws_rows& r) {
 // in one kernel, others by the loss and then the gradient.
 constexpr int kBatchSlots = 4;      // slots a thread has in flight in a pass
 constexpr int kHeldSlots = 16;
+constexpr int kHeldLeast = 16;      // from here a row has a slot that lies in it whole
 constexpr int kMaxMarkedSlots = 32768;
 
 struct DistillPlan {
@@ -228,7 +229,7 @@ inline DistillPlan plan_distill(const ws_rows& r, int32_t mode, bool gradient, b
     if (r.rows == 0) return p;
     const int64_t slots = slots_of(r);
     const int64_t most = slots + (aligned ? 0 : 1);
-    if (gradient && most <= kHeldSlots * 1024 && r.rows >= 128) {
+    if (gradient && most <= kHeldSlots * 1024 && r.rows >= 128 && r.vocab >= kHeldLeast) {
         p.held = kHeldSlots;
         p.threads = most <= kHeldSlots * 256 ? 256 : most <= kHeldSlots * 512 ? 512 : 1024;
         p.chunk = (int32_t)slots;

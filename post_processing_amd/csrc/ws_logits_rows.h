@@ -31,6 +31,9 @@ constexpr float kFar = -1.0e6f;
 struct F32 {
     using Elem = float;
     static constexpr int VEC = 4;
+    static __device__ __forceinline__ uint4 none() {   // -inf
+        return make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u);
+    }
     static __device__ __forceinline__ float up(float v) { return v; }
     static __device__ __forceinline__ float down(float v) { return v; }
     static __device__ __forceinline__ void unpack(uint4 w, float (&v)[VEC]) {
@@ -49,6 +52,9 @@ struct F16 {
     using Elem = _Float16;
     static constexpr int VEC = 8;
     typedef _Float16 Pair __attribute__((ext_vector_type(2)));
+    static __device__ __forceinline__ uint4 none() {   // -inf
+        return make_uint4(0xfc00fc00u, 0xfc00fc00u, 0xfc00fc00u, 0xfc00fc00u);
+    }
     static __device__ __forceinline__ float up(_Float16 v) { return (float)v; }
     static __device__ __forceinline__ _Float16 down(float v) { return (_Float16)v; }
     static __device__ __forceinline__ void unpack(uint4 w, float (&v)[VEC]) {
@@ -77,6 +83,9 @@ struct BF16 {
     using Elem = __bf16;
     static constexpr int VEC = 8;
     typedef __bf16 Pair __attribute__((ext_vector_type(2)));
+    static __device__ __forceinline__ uint4 none() {   // -inf
+        return make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
+    }
     static __device__ __forceinline__ float up(__bf16 v) {
         return __uint_as_float((uint32_t)__builtin_bit_cast(uint16_t, v) << 16);
     }
@@ -133,12 +142,24 @@ struct Part {
     __device__ __forceinline__ uint4 load(int s) const {
         return *reinterpret_cast<const uint4*>(base + (uint32_t)s * 16u);
     }
+    // The nearest whole slot's content (there is one), whatever s: a load under
+    // a condition would be waited for before the next is issued.
+    __device__ __forceinline__ uint4 load_near(int s) const {
+        const int last = full_to - 1;
+        return load(s < full_from ? full_from : s < last ? s : last);
+    }
     // Element by element; -inf outside the row.
     __device__ __forceinline__ void load_edge(int s, float (&v)[VEC]) const {
+        typename L::Elem x[VEC];
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
             const int e = e0 + s * VEC + j;
-            v[j] = e >= 0 && e < vocab ? L::up(row[e]) : -INFINITY;
+            x[j] = row[e < 0 ? 0 : e < vocab ? e : vocab - 1];
+        }
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            const int e = e0 + s * VEC + j;
+            v[j] = e >= 0 && e < vocab ? L::up(x[j]) : -INFINITY;
         }
     }
     __device__ __forceinline__ bool whole(int s) const { return s >= full_from && s < full_to; }
