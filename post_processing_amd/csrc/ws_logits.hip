@@ -126,14 +126,20 @@ __device__ __forceinline__ void stream_part(const Part<L>& part, float c, const 
     }
 }
 
-// The sums of a workgroup's threads, in every thread.
-template <int NT, bool ENT>
+// The sums of a workgroup's threads, in every thread of wave 0 (EVERY: of the
+// workgroup).  The waves' sums are joined across lanes again.
+template <int NT, bool ENT, bool EVERY>
 __device__ __forceinline__ Sums group_join(Sums a, float c, Sums* wave_sums) {
-    a = wave_join<ENT>(a, c, threadIdx.x & 63);
+    const int lane = threadIdx.x & 63;
+    a = wave_join<ENT>(a, c, lane);
     if constexpr (NT > 64) {
-        if ((threadIdx.x & 63) == 0) wave_sums[threadIdx.x >> 6] = a;
+        if (lane == 0) wave_sums[threadIdx.x >> 6] = a;
         __syncthreads();
-        a = join_in_order<ENT>(wave_sums, NT / 64, c);
+        if (EVERY || threadIdx.x < 64) {
+            a.init();
+            if (lane < NT / 64) a = wave_sums[lane];
+            a = wave_join<ENT>(a, c, lane);
+        }
     }
     return a;
 }
@@ -345,7 +351,7 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(LogprobsParams p) {
     Sums a;
     SlotTrack t;
     stream_part<L, NT, ENT, TOPK, false>(part, p.c, nullptr, a, t);
-    a = group_join<NT, ENT>(a, p.c, wave_sums);
+    a = group_join<NT, ENT, true>(a, p.c, wave_sums);
     int kept = 0;
     if constexpr (TOPK) {
         kept = select_best<L, NT>(part, t, a.s != a.s, p.k, best);
@@ -503,14 +509,14 @@ __device__ __forceinline__ Teacher weigh_teacher(Named& n, int k, int mode, int 
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         t.logq[h] = (double)n.score[h] - shift;
-        t.q[h] = h == 0 || k > 64 ? exp(t.logq[h]) : 0.0;
+        t.q[h] = h == 0 || k > 64 ? small_exp(t.logq[h]) : 0.0;
     }
     const double sum = wave_sum_d(t.q[0] + t.q[1], lane);
     t.mass = sum;
     t.rest = 0.0;
     if (mode == WS_DISTILL_RENORM) {
         if (sum != 0.0) {
-            const double logsum = log(sum);
+            const double logsum = small_log(sum);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 t.q[h] /= sum;
@@ -526,11 +532,11 @@ __device__ __forceinline__ Teacher weigh_teacher(Named& n, int k, int mode, int 
     return t;
 }
 
-// Wave 0's teacher and named tokens put aside in LDS while it streams its
-// share of the row.
+// Wave 0's teacher and named tokens (but for their logits) put aside in LDS
+// while it streams its share of the row.
 struct Aside {
     double q[WS_DISTILL_MAX_K], logq[WS_DISTILL_MAX_K];
-    float z[WS_DISTILL_MAX_K], add[WS_DISTILL_MAX_K];
+    float add[WS_DISTILL_MAX_K];
     uint32_t id[WS_DISTILL_MAX_K];
     uint32_t first[WS_DISTILL_MAX_K];
     double mass, rest;
@@ -542,7 +548,6 @@ struct Aside {
             const int i = lane + 64 * h;
             q[i] = t.q[h];
             logq[i] = t.logq[h];
-            z[i] = n.z[h];
             add[i] = n.add[h];
             id[i] = n.id[h];
             first[i] = n.first[h];
@@ -560,7 +565,6 @@ struct Aside {
             const int i = lane + 64 * h;
             t.q[h] = q[i];
             t.logq[h] = logq[i];
-            n.z[h] = z[i];
             n.add[h] = add[i];
             n.id[h] = id[i];
             n.first[h] = first[i] != 0;
@@ -599,7 +603,7 @@ struct DistillParams {
     void* grad;
     int64_t grad_stride;
     int32_t vocab, k, mode;
-    int32_t chunk, parts;
+    int32_t rows, chunk, parts;
     int32_t mark_words;   // LDS words of marks
     float c, inv_tau;
 };
@@ -614,13 +618,21 @@ struct Slope {
     float a, a_listed;
     float b;       // entropy: a + b log2 p_j in a's place
     float scale;
-    int zero;      // a row without a distribution: no gradient
+    bool none;     // a row without a distribution: no gradient
+
+    // Its logits are all -inf, so every power of two comes out 0.
+    __device__ __forceinline__ void clear() {
+        max = a = a_listed = b = 0.0f;
+        base = base_listed = INFINITY;
+        none = true;
+    }
 };
 
 __device__ __forceinline__ Slope distill_slope(const Teacher& t, bool bad, float max,
                                                double logsum, double tail, float scale) {
     constexpr double kLog2e64 = 1.4426950408889634074;
     Slope s;
+    s.none = false;
     s.max = max;
     s.base = s.base_listed = (float)(logsum * kLog2e64);
     s.a = s.a_listed = bad ? NAN : (float)t.mass;
@@ -628,12 +640,12 @@ __device__ __forceinline__ Slope distill_slope(const Teacher& t, bool bad, float
     if (t.rest > 0.0 && !bad) {
         s.a = 0.0f;
         if (tail != -(double)INFINITY) {
-            s.a = (float)(t.mass * exp(tail) - t.rest);
+            s.a = (float)(t.mass * small_exp(tail) - t.rest);
             s.base = (float)((logsum + tail) * kLog2e64);
         }
     }
     s.scale = scale;
-    s.zero = logsum == -(double)INFINITY;
+    if (logsum == -(double)INFINITY) s.clear();
     return s;
 }
 
@@ -650,10 +662,12 @@ __device__ __forceinline__ Slope finish_distill(const DistillParams& p, int64_t 
         s = (s == 0.0f ? 0.0f : s * __builtin_amdgcn_exp2f((sums.m - m) * p.c)) + wave_sum(e, lane);
     }
     const bool empty = s == 0.0f;
-    const double logsum = empty ? -(double)INFINITY : log((double)s);
+    // The three logarithms a row needs, in three lanes at once.
+    const double logs = small_log(lane == 0 ? (double)s : lane == 1 ? (double)sums.s : t.rest);
+    const double logsum = empty ? -(double)INFINITY : lane_d(logs, 0);
     double tail = -(double)INFINITY;
     if (p.mode == WS_DISTILL_TAIL && sums.s != 0.0f)
-        tail = ((double)sums.m - (double)m) * p.inv_tau + log((double)sums.s) - logsum;
+        tail = ((double)sums.m - (double)m) * p.inv_tau + lane_d(logs, 1) - logsum;
     double loss = 0.0;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -663,7 +677,7 @@ __device__ __forceinline__ Slope finish_distill(const DistillParams& p, int64_t 
         loss += t.q[h] * (t.logq[h] - logp);
     }
     loss = wave_sum_d(loss, lane);
-    if (t.rest > 0.0) loss += t.rest * (log(t.rest) - tail);
+    if (t.rest > 0.0) loss += t.rest * (lane_d(logs, 2) - tail);
     if (lane == 0) {
         p.loss[row] = n.bad ? NAN : (float)loss;
         if (p.stats) p.stats[row] = {empty ? -INFINITY : m, (float)logsum};
@@ -673,10 +687,11 @@ __device__ __forceinline__ Slope finish_distill(const DistillParams& p, int64_t 
                          p.grad_loss ? p.grad_loss[row] * p.inv_tau : 0.0f);
 }
 
-// Marks the listed tokens of a part, one bit an element, one byte a slot;
-// `words` words of marks, which reach past the part's slots as far as a batch
-// of the pass does.
-template <typename L, int NT>
+// Marks the listed tokens of a part, one bit an element, one byte a slot, in
+// `words` words of LDS.  EACH = 1: slot s at byte s; the marks reach past the
+// part's slots as far as a batch of the pass does.  Otherwise a thread's EACH
+// slots (s, s + NT, ...) lie side by side, to be read at once.
+template <typename L, int NT, int EACH>
 __device__ __forceinline__ void mark_listed(const Part<L>& part, const Named& n, uint32_t* mask,
                                             int words) {
     for (int i = threadIdx.x; i < words; i += NT) mask[i] = 0;
@@ -688,7 +703,8 @@ __device__ __forceinline__ void mark_listed(const Part<L>& part, const Named& n,
             const int e = (int)n.id[h] - part.e0;
             if (e < 0 || e >= part.n * L::VEC) continue;
             const int slot = e / L::VEC;
-            atomicOr(&mask[slot >> 2], 1u << ((slot & 3) * 8 + e % L::VEC));
+            const int at = EACH == 1 ? slot : slot % NT * EACH + slot / NT;
+            atomicOr(&mask[at >> 2], 1u << ((at & 3) * 8 + e % L::VEC));
         }
     }
     __syncthreads();
@@ -716,12 +732,12 @@ __global__ void __launch_bounds__(NT) distill_kernel(DistillParams p) {
             t = weigh_teacher(n, p.k, p.mode, lane);
         }
     }
-    if constexpr (TAIL) mark_listed<L, NT>(part, n, listed_marks, p.mark_words);
+    if constexpr (TAIL) mark_listed<L, NT, 1>(part, n, listed_marks, p.mark_words);
     Sums a;
     SlotTrack unused;
     stream_part<L, NT, false, false, TAIL>(part, p.c, reinterpret_cast<const uint8_t*>(listed_marks),
                                            a, unused);
-    a = group_join<NT, false>(a, p.c, wave_sums);
+    a = group_join<NT, false, false>(a, p.c, wave_sums);
     if (p.parts > 1) {
         if (tid == 0) p.sums[blockIdx.x] = a;
     } else if (tid < 64) {
@@ -799,7 +815,6 @@ __device__ __forceinline__ void slope_values(const Slope& g, float c, float (&v)
         const float prob = __builtin_amdgcn_exp2f(t);
         if constexpr (ENT) v[j] = prob * fmaf(b, fmaxf(t, kFar), a);
         else v[j] = prob * a;
-        if (g.zero) v[j] = 0.0f;
     }
 }
 
@@ -807,7 +822,7 @@ __device__ __forceinline__ void slope_values(const Slope& g, float c, float (&v)
 template <typename L, bool ENT, bool DISTILL>
 __device__ __forceinline__ void store_named(const Slope& g, const Named& n, float c, int from,
                                             int to, typename L::Elem* row) {
-    if (g.zero) return;
+    if (g.none) return;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         if (!n.first[h] || n.id[h] < (uint32_t)from || n.id[h] >= (uint32_t)to) continue;
@@ -866,6 +881,7 @@ __device__ __forceinline__ Slope grad_slope(const GradParams& p, int64_t row,
         }
         read_named<L>(n, z, p.vocab);
         Slope s;
+        s.none = false;
         s.max = st.max;
         s.base = s.base_listed = st.logsum * kLog2e;
         s.a = -wave_sum(n.add[0], lane);
@@ -879,7 +895,7 @@ __device__ __forceinline__ Slope grad_slope(const GradParams& p, int64_t row,
         if (n.bad) s.a = NAN;
         s.a_listed = s.a;
         s.scale = p.inv_tau;
-        s.zero = st.logsum == -INFINITY;
+        if (st.logsum == -INFINITY) s.clear();
         merge_named(n, p.k + 1, ids, adds, lane);
         return s;
     }
@@ -952,7 +968,7 @@ __device__ __forceinline__ int forget(int v) {
 }
 
 template <typename L, int NT, bool TAIL>
-__global__ void __launch_bounds__(NT) distill_step_kernel(DistillParams p) {
+__global__ void __launch_bounds__(NT, 4) distill_step_kernel(DistillParams p) {
     constexpr int VEC = L::VEC, R = kHeld, B = 2;
     __shared__ Sums wave_sums[NT / 64];
     __shared__ __align__(16) uint32_t ids[WS_DISTILL_MAX_K];
@@ -963,35 +979,25 @@ __global__ void __launch_bounds__(NT) distill_step_kernel(DistillParams p) {
     const int64_t row = blockIdx.x;
     Part<L> part;
     part.init(p.logits, row * p.stride, p.vocab, p.chunk, 1, 0);
-    PartOut<L> out;
-    out.init(part, p.grad, row * p.grad_stride);
+    float v[VEC];
     // The teacher's entries before the row, as loads return in order.
     Named n;
     Teacher t;
-    if (tid < 64) {
-        read_entries(n, p.teacher + row * p.k, p.k, lane);
-        read_named<L>(n, part.row, p.vocab);
-    }
-    float v[VEC];
-    uint4 front, rear;   // slots that stick out of the row
-    if (part.full_from > 0) {
-        part.load_edge(0, v);
-        front = L::pack(v);
-    }
-    if (part.full_to < part.n) {
-        part.load_edge(part.n - 1, v);
-        rear = L::pack(v);
-    }
+    if (tid < 64) read_entries(n, p.teacher + row * p.k, p.k, lane);
     uint4 w[R];
 #pragma unroll
     for (int i = 0; i < R; ++i) w[i] = part.load_near(tid + i * NT);
-    if constexpr (TAIL) mark_listed<L, NT>(part, n, listed_marks, R * NT / 4);
+    if constexpr (TAIL) mark_listed<L, NT, R>(part, n, listed_marks, R * NT / 4);
     if (tid < 64) {   // while the row is on its way
+        read_named<L>(n, part.row, p.vocab);
         t = weigh_teacher(n, p.k, p.mode, lane);
         merge_named(n, p.k, ids, adds, lane);
         if constexpr (TAIL) settle_rest(t, n, p.k, p.vocab);
         aside.put(n, t, lane);
     }
+    uint4 marks = make_uint4(0, 0, 0, 0);   // this thread's, a byte a slot
+    static_assert(R == sizeof(marks), "sixteen slots a thread");
+    if constexpr (TAIL) marks = *reinterpret_cast<const uint4*>(listed_marks + tid * (R / 4));
     Sums a;
     SlotTrack unused;
     a.init();
@@ -1002,17 +1008,18 @@ __global__ void __launch_bounds__(NT) distill_step_kernel(DistillParams p) {
         for (int j = 0; j < B; ++j) {
             const int slot = forget(tid) + (i + j) * NT;
             if (__ballot(!part.whole(slot)) != 0) {
-                const uint4 none = L::none();
-                uint4 x = slot < part.n ? w[i + j] : none;
-                if (slot < part.full_from) x = front;
-                if (slot >= part.full_to && slot < part.n) x = rear;
-                w[i + j] = x;
+                if (!part.whole(slot)) w[i + j] = L::none();   // beyond the row
+                if (!part.whole(slot) && slot < part.n) {      // sticks out of it
+                    part.load_edge(slot, v);
+                    w[i + j] = L::pack(v);
+                }
             }
             if constexpr (TAIL) {
                 // Listed tokens leave the held row for good: store_named
                 // writes theirs.
-                const uint8_t* marks = reinterpret_cast<const uint8_t*>(listed_marks);
-                const uint32_t mark = marks[slot];
+                const uint32_t word = i + j < 4 ? marks.x : i + j < 8 ? marks.y
+                                    : i + j < 12 ? marks.z : marks.w;
+                const uint32_t mark = word >> (i + j) % 4 * 8 & 0xffu;
                 if (__ballot(mark != 0) != 0) {
                     L::unpack(w[i + j], v);
                     hide_listed<VEC>(mark, v);
@@ -1025,7 +1032,7 @@ __global__ void __launch_bounds__(NT) distill_step_kernel(DistillParams p) {
         take_slots<L, NT, false, false, false>(x, 0, p.c, nullptr, a, unused);
         __builtin_amdgcn_sched_barrier(0);
     }
-    a = group_join<NT, false>(a, p.c, wave_sums);
+    a = group_join<NT, false, false>(a, p.c, wave_sums);
     if (tid < 64) {
         aside.get(n, t, lane);
         const Slope s = finish_distill(p, row, a, n, t, lane);
@@ -1033,6 +1040,8 @@ __global__ void __launch_bounds__(NT) distill_step_kernel(DistillParams p) {
     }
     __syncthreads();   // every named logit is read before any is overwritten
     const Slope g = slope;
+    PartOut<L> out;
+    out.init(part, p.grad, row * p.grad_stride);
 #pragma unroll
     for (int i = 0; i < R; ++i) {
         const int s = forget(tid) + i * NT;
@@ -1252,6 +1261,7 @@ extern "C" int ws_distill(const ws_rows* rows, const ws_distill_args* args, void
     p.loss = args->loss;
     p.stats = args->stats;
     p.tail = args->tail;
+    p.rows = r.rows;
     p.vocab = r.vocab;
     p.k = args->teacher_k;
     p.mode = args->mode;

@@ -222,6 +222,10 @@ __device__ __forceinline__ double xor_lane_d(double v, int lane) {
     return __builtin_bit_cast(double, xor_lane64<J>(__builtin_bit_cast(uint64_t, v), lane));
 }
 
+__device__ __forceinline__ double lane_d(double v, int lane) {
+    return __builtin_bit_cast(double, readlane64(__builtin_bit_cast(uint64_t, v), lane));
+}
+
 __device__ __forceinline__ double wave_sum_d(double v, int lane) {
     v += xor_lane_d<32>(v, lane);
     v += xor_lane_d<16>(v, lane);
@@ -231,6 +235,33 @@ __device__ __forceinline__ double wave_sum_d(double v, int lane) {
     return v + xor_lane_d<1>(v, lane);
 }
 
+// e^x in FP64 for x <= 88, to about 1e-15 (1 + x^2) relative; 0 below -200.
+// (sum of (x / 1024)^n / n! up to n = 7) squared ten times: a few constants,
+// where a library routine's would crowd the registers of a held row.
+__device__ __forceinline__ double small_exp(double x) {
+    if (x < -200.0) return 0.0;
+    const double y = x * 0.0009765625;
+    double e = 1.0 / 5040.0;
+    e = fma(e, y, 1.0 / 720.0);
+    e = fma(e, y, 1.0 / 120.0);
+    e = fma(e, y, 1.0 / 24.0);
+    e = fma(e, y, 1.0 / 6.0);
+    e = fma(e, y, 0.5);
+    e = fma(e, y, 1.0);
+    e = fma(e, y, 1.0);
+#pragma unroll
+    for (int i = 0; i < 10; ++i) e *= e;
+    return e;
+}
+
+// log x in FP64 for x between 1e-30 and 1e30: the FP32 logarithm L, and what
+// x e^-L leaves of 1.
+__device__ __forceinline__ double small_log(double x) {
+    const double l = (double)__logf((float)x);
+    const double r = fma(x, small_exp(-l), -1.0);
+    return l + r * fma(r, fma(r, 1.0 / 3.0, -0.5), 1.0);
+}
+
 // The sums of a wave's lanes, in every lane.
 template <bool ENT>
 __device__ __forceinline__ Sums wave_join(Sums a, float c, int lane) {
@@ -238,23 +269,6 @@ __device__ __forceinline__ Sums wave_join(Sums a, float c, int lane) {
     a.s = wave_sum(a.s, lane);
     if constexpr (ENT) a.u = wave_sum(a.u, lane);
     return a;
-}
-
-// The sums of `count` partial sums in order, in every thread that calls.
-template <bool ENT>
-__device__ __forceinline__ Sums join_in_order(const Sums* p, int count, float c) {
-    Sums t = p[0];
-    for (int i = 1; i < count; ++i) t.m = fmaxf(t.m, p[i].m);
-    const float m = t.m;
-    t = p[0];
-    t.raise<ENT>(m, c);
-    for (int i = 1; i < count; ++i) {
-        Sums x = p[i];
-        x.raise<ENT>(m, c);
-        t.s += x.s;
-        if constexpr (ENT) t.u += x.u;
-    }
-    return t;
 }
 
 // ---- order keys ------------------------------------------------------------------
