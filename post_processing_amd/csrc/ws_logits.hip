@@ -126,16 +126,11 @@ __device__ __forceinline__ void stream_part(const Part<L>& part, float c, const 
     }
 }
 
-// The sums of a workgroup's threads, in every thread of wave 0 (EVERY: of the
-// workgroup).  The waves' sums are joined across lanes again.
-template <int NT, bool ENT, bool EVERY>
-__device__ __forceinline__ Sums group_join(Sums a, float c, Sums* wave_sums) {
-    const int lane = threadIdx.x & 63;
-    a = wave_join<ENT>(a, c, lane);
+template <int NT, bool ENT>
+__device__ __forceinline__ Sums join_waves(Sums a, float c, const Sums* wave_sums) {
     if constexpr (NT > 64) {
-        if (lane == 0) wave_sums[threadIdx.x >> 6] = a;
-        __syncthreads();
-        if (EVERY || threadIdx.x < 64) {
+        const int lane = threadIdx.x & 63;
+        if (threadIdx.x < 64) {
             a.init();
             if (lane < NT / 64) a = wave_sums[lane];
             a = wave_join<ENT>(a, c, lane);
@@ -144,46 +139,42 @@ __device__ __forceinline__ Sums group_join(Sums a, float c, Sums* wave_sums) {
     return a;
 }
 
-// A row's best keys as they are collected, in LDS.
-template <typename L, int NT>
-struct Best {
-    static constexpr int kScan = NT < 128 ? NT : 128;   // threads that read slots again
-    static constexpr int kRoom = kScan * L::VEC + WS_MAX_K;
-    static constexpr int kListed = 64;
-    uint64_t keys[kRoom];
-    uint64_t sorted[WS_MAX_K];
-    uint32_t tops[NT / 64 * 32];   // each wave's 32 largest thread bests, descending
-    int single[kListed];           // slots to read again
-    int thread[kListed];           // threads all of whose slots are read again
-    int above, picked, singles, threads, count;
-};
-
-// K-th largest over the workgroup of one value a thread (K <= 32); every
-// thread gets it.  The caller has synchronised since `tops` was last read.
-template <int NT>
-__device__ __forceinline__ uint32_t group_kth_largest(uint32_t v, int k, uint32_t* tops) {
+// The sums of a workgroup's threads, in wave 0: each wave's across its lanes,
+// then the waves' the same way.  FENCE: with the barrier between the two.
+template <int NT, bool ENT, bool FENCE = true>
+__device__ __forceinline__ Sums group_join(Sums a, float c, Sums* wave_sums) {
     const int lane = threadIdx.x & 63;
-    v = wave_sort<true>(v, lane);
+    a = wave_join<ENT>(a, c, lane);
     if constexpr (NT > 64) {
-        static_assert(NT == 256, "one or four waves");
-        const int wave = threadIdx.x >> 6;
-        if (lane < 32) tops[wave * 32 + lane] = v;
-        __syncthreads();
-        // Lists 0 and 2 in the lower half of the lanes, 1 and 3 in the upper:
-        // the larger of one list and the other reversed are the 32 largest of
-        // both, a bitonic sequence; sorted, the halves meet the same way.
-        const int half = lane & 32, i = lane & 31;
-        const uint32_t a = tops[half + i], b = tops[64 + half + 31 - i];
-        v = bitonic_stages<64, 16, true>(a > b ? a : b, lane);
-        const uint32_t w = (uint32_t)__builtin_amdgcn_ds_bpermute((lane ^ 63) * 4, (int)v);
-        v = bitonic_stages<64, 16, true>(v > w ? v : w, lane);
+        if (lane == 0) wave_sums[threadIdx.x >> 6] = a;
+        if constexpr (FENCE) {
+            __syncthreads();
+            a = join_waves<NT, ENT>(a, c, wave_sums);
+        }
     }
-    return (uint32_t)__builtin_amdgcn_readlane((int)v, k - 1);
+    return a;
 }
 
+// A row's best keys as they are collected, in LDS.
+template <typename L, int NT, bool HELD>
+struct Best {
+    static constexpr int kListed = 64;                  // threads looked at
+    static constexpr int kScan = NT < 128 ? NT : 128;   // threads that read slots again
+    static constexpr int kRoom = (HELD ? kListed * kBatch : kScan) * L::VEC + WS_MAX_K;
+    static_assert(kRoom >= NT, "room for every thread's pair");
+    uint64_t keys[kRoom];
+    uint64_t sorted[WS_MAX_K];
+    uint32_t groups[64];
+    int single[kListed];           // slots to read again
+    int thread[kListed];           // threads all of whose slots are read again
+    uint32_t bound;
+    int last, picked, singles, threads, count;
+    bool all;
+};
+
 // Keeps the K best of the collected keys, in order, at the list's start.
-template <typename L, int NT>
-__device__ __forceinline__ int keep_best(Best<L, NT>& b, int k) {
+template <typename L, int NT, bool HELD>
+__device__ __forceinline__ int keep_best(Best<L, NT, HELD>& b, int k) {
     const int n = b.count;
     for (int i = threadIdx.x; i < n; i += NT) {
         const uint64_t x = b.keys[i];
@@ -198,35 +189,95 @@ __device__ __forceinline__ int keep_best(Best<L, NT>& b, int k) {
     return kept;
 }
 
+// The largest of a group of NT / 64 neighbouring lanes, in each of them.
+template <int NT>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v, int lane) {
+    const auto larger = [](uint32_t a, uint32_t b) { return a > b ? a : b; };
+    if constexpr (NT >= 128) v = larger(v, xor_lane32<1>(v, lane));
+    if constexpr (NT >= 256) v = larger(v, xor_lane32<2>(v, lane));
+    if constexpr (NT >= 512) v = larger(v, xor_lane32<4>(v, lane));
+    if constexpr (NT >= 1024) v = larger(v, xor_lane32<8>(v, lane));
+    return v;
+}
+
 // The K best keys of a part of a row into b.sorted; returns how many there are
-// (K, or the part's elements if fewer).  all: read every slot again (a row
-// with a NaN, which the running maxima skip).
-template <typename L, int NT>
-__device__ __forceinline__ int select_best(const Part<L>& part, SlotTrack t, bool all, int k,
-                                           Best<L, NT>& b) {
-    const int tid = threadIdx.x;
+// (K, or the part's elements if fewer).  Joins the sums on the way: in wave 0
+// afterwards.  HELD: the thread's slots are still in w.
+template <typename L, int NT, bool ENT, bool HELD>
+__device__ __forceinline__ int select_best(const Part<L>& part, SlotTrack t, Sums& a, float c,
+                                           Sums* wave_sums, const uint4 (&w)[kBatch], int k,
+                                           Best<L, NT, HELD>& b) {
+    using B = Best<L, NT, HELD>;
+    constexpr int kGroup = NT / 64;   // threads of a group
+    const int tid = threadIdx.x, lane = tid & 63;
     const bool has = tid < part.n;
     const uint32_t best = has ? value_image(t.best) : 0;
     const uint32_t second = value_image(t.second);
-    if (tid == 0) b.above = b.picked = b.singles = b.threads = b.count = 0;
-    uint32_t bound = group_kth_largest<NT>(best, k, b.tops);
+    // The bound from 64 groups of threads: the K-th largest of their bests,
+    // by one wave (a few more threads reach it than with every thread a group).
+    const uint32_t group = lanes_max<NT>(best, lane);
+    if (lane % kGroup == 0) b.groups[tid / kGroup] = group;
+    a = group_join<NT, ENT, false>(a, c, wave_sums);
     __syncthreads();
-    // Threads at the bound may be more than K when their bests are equal.
-    if (has && best >= bound) {
-        atomicAdd(&b.picked, 1);
-        if (best > bound) atomicAdd(&b.above, 1);
+    if (tid < 64) {
+        a = join_waves<NT, ENT>(a, c, wave_sums);
+        const uint32_t sorted = wave_sort<true>(b.groups[lane], lane);
+        if (lane == 0) {
+            b.all = a.s != a.s;   // a NaN in the row, which the maxima skip
+            b.last = 0x7fffffff;
+            b.picked = b.singles = b.threads = b.count = 0;
+        }
+        if (lane == k - 1) b.bound = sorted;
     }
     __syncthreads();
-    int last = 0x7fffffff;   // of the threads at the bound, those whose slot is not beyond
-    if (b.picked > Best<L, NT>::kListed) {
-        const int above = b.above;
-        const uint32_t early =
-            group_kth_largest<NT>(has && best == bound ? ~(uint32_t)t.slot : 0u, k - above, b.tops);
-        last = (int)~early;
+    const bool all = b.all;
+    if (has && best >= b.bound) atomicAdd(&b.picked, 1);
+    __syncthreads();
+    if (b.picked > B::kListed) {
+        // Many reach the bound (equal values): exactly K threads then, by best
+        // and slot, and the K-th's as the bound.
+        const uint64_t pair = has ? ((uint64_t)best << 32) | (uint32_t)~t.slot : 0;
+        b.keys[tid] = pair;
+        __syncthreads();
+        if (has && best >= b.bound && keys_above(b.keys, NT, pair) == k - 1) {
+            b.groups[0] = best;
+            b.last = t.slot;
+        }
+        __syncthreads();
+        if (tid == 0) b.bound = b.groups[0];
         __syncthreads();
     }
+    const uint32_t bound = b.bound;
+    const int last = b.last;
+    const uint32_t edge = last == 0x7fffffff ? 0xffffffffu
+                                             : (uint32_t)(part.e0 + last * L::VEC + L::VEC - 1);
+    uint64_t least = all ? 0 : ((uint64_t)bound << 32) | (uint32_t)~edge;
+    const bool chosen = has && !all && (best > bound || (best == bound && t.slot <= last));
+    const auto collect = [&](int slot, const float (&v)[L::VEC]) {
+#pragma unroll
+        for (int j = 0; j < L::VEC; ++j) {
+            const int e = part.e0 + slot * L::VEC + j;
+            const uint64_t key = value_key(v[j], (uint32_t)e);
+            if (key >= least && e >= 0 && e < part.vocab) b.keys[atomicAdd(&b.count, 1)] = key;
+        }
+    };
+    if constexpr (HELD) {
+        if (!all) {
+            if (chosen) {
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    float v[L::VEC];
+                    L::unpack(w[i], v);
+                    if (tid + i * NT < part.n && value_image(slot_max<L::VEC>(v)) >= bound)
+                        collect(tid + i * NT, v);
+                }
+            }
+            __syncthreads();
+            return keep_best(b, k);
+        }
+    }
     const int rounds_per_thread = (part.n + NT - 1) / NT;
-    if (has && !all && (best > bound || (best == bound && t.slot <= last))) {
+    if (chosen) {
         // A second slot at the bound counts only if it is not beyond `last`; it
         // comes at least NT slots after the first when both are at the bound.
         const bool more = second > bound ||
@@ -235,14 +286,11 @@ __device__ __forceinline__ int select_best(const Part<L>& part, SlotTrack t, boo
         else b.single[atomicAdd(&b.singles, 1)] = t.slot;
     }
     __syncthreads();
-    const uint32_t edge = last == 0x7fffffff ? 0xffffffffu
-                                             : (uint32_t)(part.e0 + last * L::VEC + L::VEC - 1);
-    uint64_t least = all ? 0 : ((uint64_t)bound << 32) | (uint32_t)~edge;
     const int singles = b.singles;
     const int items = all ? part.n : singles + b.threads * rounds_per_thread;
-    for (int from = 0;; from += Best<L, NT>::kScan) {
+    for (int from = 0;; from += B::kScan) {
         const int item = from + tid;
-        if (tid < Best<L, NT>::kScan && item < items) {
+        if (tid < B::kScan && item < items) {
             int slot = item;
             if (!all) {
                 if (item < singles) {
@@ -255,17 +303,11 @@ __device__ __forceinline__ int select_best(const Part<L>& part, SlotTrack t, boo
             if (slot < part.n) {
                 float v[L::VEC];
                 part.load_any(slot, v);
-#pragma unroll
-                for (int j = 0; j < L::VEC; ++j) {
-                    const int e = part.e0 + slot * L::VEC + j;
-                    const uint64_t key = value_key(v[j], (uint32_t)e);
-                    if (key >= least && e >= 0 && e < part.vocab)
-                        b.keys[atomicAdd(&b.count, 1)] = key;
-                }
+                collect(slot, v);
             }
         }
         __syncthreads();
-        const bool more = from + Best<L, NT>::kScan < items;
+        const bool more = from + B::kScan < items;
         if (!more || b.count > WS_MAX_K) {
             const int kept = keep_best(b, k);
             if (!more) return kept;
@@ -337,11 +379,11 @@ struct Select<false, T> {
     using Type = Nothing;
 };
 
-template <typename L, int NT, bool ENT, bool TOPK>
+// HELD: a part is at most kBatch slots a thread, which stay in registers.
+template <typename L, int NT, bool ENT, bool TOPK, bool HELD>
 __global__ void __launch_bounds__(NT) logprobs_kernel(LogprobsParams p) {
-    constexpr int VEC = L::VEC;
     __shared__ Sums wave_sums[NT / 64];
-    __shared__ typename Select<TOPK, Best<L, NT>>::Type best;
+    __shared__ typename Select<TOPK, Best<L, NT, HELD>>::Type best;
     const int tid = threadIdx.x;
     const int64_t row = blockIdx.x / (uint32_t)p.parts;
     const int index = (int)(blockIdx.x % (uint32_t)p.parts);
@@ -350,12 +392,29 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(LogprobsParams p) {
 
     Sums a;
     SlotTrack t;
-    stream_part<L, NT, ENT, TOPK, false>(part, p.c, nullptr, a, t);
-    a = group_join<NT, ENT, true>(a, p.c, wave_sums);
+    uint4 w[kBatch];
+    if constexpr (HELD) {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) w[i] = part.load_near(tid + i * NT);
+        float v[kBatch][L::VEC];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            part.settle(tid + i * NT, w[i]);
+            L::unpack(w[i], v[i]);
+        }
+        a.init();
+        t = {-INFINITY, -INFINITY, tid};
+        take_slots<L, NT, ENT, TOPK, false>(v, tid, p.c, nullptr, a, t);
+    } else {
+        stream_part<L, NT, ENT, TOPK, false>(part, p.c, nullptr, a, t);
+    }
     int kept = 0;
     if constexpr (TOPK) {
-        kept = select_best<L, NT>(part, t, a.s != a.s, p.k, best);
+        kept = select_best<L, NT, ENT, HELD>(part, t, a, p.c, wave_sums, w, p.k, best);
+    } else {
+        a = group_join<NT, ENT>(a, p.c, wave_sums);
     }
+    if (tid >= 64) return;
     if (p.parts == 1) {
         write_logprobs<L>(p, row, a, best.sorted);
     } else {
@@ -367,45 +426,51 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(LogprobsParams p) {
     }
 }
 
-// Joins the parts of a row (at most 64): one wave a row.
-
+// Joins the parts of a row (at most 64).
+constexpr int kJoin = 256;
 
 template <typename L, bool ENT>
-__global__ void __launch_bounds__(64) logprobs_join_kernel(LogprobsParams p) {
+__global__ void __launch_bounds__(kJoin) logprobs_join_kernel(LogprobsParams p) {
+    constexpr int kEach = kMaxRowParts * WS_MAX_K / kJoin;   // keys a thread
     __shared__ uint64_t keys[WS_MAX_K * WS_MAX_K + WS_MAX_K];
     __shared__ uint64_t sorted[WS_MAX_K];
-    const int lane = threadIdx.x;
+    __shared__ int count;
+    const int tid = threadIdx.x, lane = tid & 63;
     const int64_t row = blockIdx.x;
     Sums a;
     a.init();
     if (lane < p.parts) a = p.sums[row * p.parts + lane];
     if (p.k > 0) {
         const uint64_t* in = p.keys + row * p.parts * p.k;
+        const int all = p.parts * p.k;
         // The K-th largest of the lists' leading keys, as many from each as
         // fill a wave, bounds the K-th best from below.
         const int lead = 64 / p.parts < p.k ? 64 / p.parts : p.k;
-        uint64_t x = 0;
-        if (lane < p.parts * lead) x = in[lane / lead * p.k + lane % lead];
+        const int from = lane < p.parts * lead ? lane / lead * p.k + lane % lead : 0;
+        uint64_t x = in[from];
+        uint64_t mine[kEach];
+#pragma unroll
+        for (int i = 0; i < kEach; ++i)
+            mine[i] = in[tid + i * kJoin < all ? tid + i * kJoin : 0];
+        if (lane >= p.parts * lead) x = 0;
+        if (tid == 0) count = 0;
+        __syncthreads();
         x = wave_sort<true>(x, lane);
         const uint64_t least = umax64(readlane64(x, p.k - 1), 1);
-        int n = 0;
-        const int all = p.parts * p.k;
-        for (int i = 0; i < all; i += 64) {
-            const uint64_t key = i + lane < all ? in[i + lane] : 0;
-            const uint64_t hit = __ballot(key >= least);
-            if (key >= least) keys[n + lanes_below(hit)] = key;
-            n += __popcll(hit);
-        }
-        wave_lds_sync();
-        for (int i = lane; i < n; i += 64) {
+#pragma unroll
+        for (int i = 0; i < kEach; ++i)
+            if (tid + i * kJoin < all && mine[i] >= least) keys[atomicAdd(&count, 1)] = mine[i];
+        __syncthreads();
+        const int n = count;
+        for (int i = tid; i < n; i += kJoin) {
             const uint64_t key = keys[i];
             const int r = keys_above(keys, n, key);
             if (r < p.k) sorted[r] = key;
         }
-        wave_lds_sync();
+        __syncthreads();
     }
-    a = wave_join<ENT>(a, p.c, lane);
-    write_logprobs<L>(p, row, a, sorted);
+    if (tid >= 64) return;
+    write_logprobs<L>(p, row, wave_join<ENT>(a, p.c, lane), sorted);
 }
 
 // ---------------------------------------------------------------------------
@@ -485,18 +550,30 @@ struct Teacher {
     double rest;   // q_t
 };
 
-__device__ __forceinline__ void read_entries(Named& n, const ws_topk_entry* entries, int k,
-                                             int lane) {
+// A lane's two entries of a teacher's k, as they lie in memory (another's
+// where there are fewer): loaded first and looked at later.
+struct RawEntries {
+    uint2 e[2];
+
+    __device__ __forceinline__ void load(const ws_topk_entry* entries, int k, int lane) {
+        const uint2* p = reinterpret_cast<const uint2*>(entries);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        n.id[h] = kAbsent;
-        n.score[h] = -INFINITY;
-        if (lane + 64 * h < k) {
-            const ws_topk_entry e = entries[lane + 64 * h];
-            n.id[h] = (uint32_t)e.index;
-            if (n.id[h] != kAbsent) n.score[h] = e.score;
+        for (int h = 0; h < 2; ++h) e[h] = p[lane + 64 * h < k ? lane + 64 * h : k - 1];
+    }
+    __device__ __forceinline__ void into(Named& n, int k, int lane) const {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            n.id[h] = lane + 64 * h < k ? e[h].y : kAbsent;
+            n.score[h] = n.id[h] != kAbsent ? __uint_as_float(e[h].x) : -INFINITY;
         }
     }
+};
+
+__device__ __forceinline__ void read_entries(Named& n, const ws_topk_entry* entries, int k,
+                                             int lane) {
+    RawEntries raw;
+    raw.load(entries, k, lane);
+    raw.into(n, k, lane);
 }
 
 __device__ __forceinline__ Teacher weigh_teacher(Named& n, int k, int mode, int lane) {
@@ -737,7 +814,7 @@ __global__ void __launch_bounds__(NT) distill_kernel(DistillParams p) {
     SlotTrack unused;
     stream_part<L, NT, false, false, TAIL>(part, p.c, reinterpret_cast<const uint8_t*>(listed_marks),
                                            a, unused);
-    a = group_join<NT, false, false>(a, p.c, wave_sums);
+    a = group_join<NT, false>(a, p.c, wave_sums);
     if (p.parts > 1) {
         if (tid == 0) p.sums[blockIdx.x] = a;
     } else if (tid < 64) {
@@ -956,6 +1033,11 @@ __global__ void __launch_bounds__(256) grad_kernel(GradParams p) {
 // Loss and gradient of a row in one pass: the row stays in the registers of
 // its workgroup (R slots a thread), so it is read once.
 constexpr int kHeld = kHeldSlots;
+// With marks, slots asked for before the workgroup waits for them: a CU takes
+// so many loads at once, so a barrier behind all of a row's loads waits for
+// most of their data (2,048 x 131,072 BF16: 254 us with all 16 slots asked for
+// before it, 249 with 8, 243 with 4, 234 with 2).
+constexpr int kAhead = 2;
 
 // Has the compiler work a value out again where it is used again, rather than
 // hold what it derived the first time (a slot's elements, sixteen lane masks).
@@ -983,11 +1065,15 @@ __global__ void __launch_bounds__(NT, 4) distill_step_kernel(DistillParams p) {
     // The teacher's entries before the row, as loads return in order.
     Named n;
     Teacher t;
-    if (tid < 64) read_entries(n, p.teacher + row * p.k, p.k, lane);
+    RawEntries raw;
+    if (tid < 64) raw.load(p.teacher + row * p.k, p.k, lane);
     uint4 w[R];
 #pragma unroll
-    for (int i = 0; i < R; ++i) w[i] = part.load_near(tid + i * NT);
+    for (int i = 0; i < kAhead; ++i) w[i] = part.load_near(tid + i * NT);
+    if (tid < 64) raw.into(n, p.k, lane);
     if constexpr (TAIL) mark_listed<L, NT, R>(part, n, listed_marks, R * NT / 4);
+#pragma unroll
+    for (int i = kAhead; i < R; ++i) w[i] = part.load_near(tid + i * NT);
     if (tid < 64) {   // while the row is on its way
         read_named<L>(n, part.row, p.vocab);
         t = weigh_teacher(n, p.k, p.mode, lane);
@@ -1032,7 +1118,7 @@ __global__ void __launch_bounds__(NT, 4) distill_step_kernel(DistillParams p) {
         take_slots<L, NT, false, false, false>(x, 0, p.c, nullptr, a, unused);
         __builtin_amdgcn_sched_barrier(0);
     }
-    a = group_join<NT, false, false>(a, p.c, wave_sums);
+    a = group_join<NT, false>(a, p.c, wave_sums);
     if (tid < 64) {
         aside.get(n, t, lane);
         const Slope s = finish_distill(p, row, a, n, t, lane);
@@ -1091,19 +1177,18 @@ template <typename L>
 int run_logprobs(const ws_rows& r, const LogprobsPlan& plan, const LogprobsParams& p,
                  hipStream_t s) {
     const bool ent = p.entropy != nullptr, top = p.k > 0;
-    const auto wide = top ? (ent ? logprobs_kernel<L, 256, true, true>
-                                 : logprobs_kernel<L, 256, false, true>)
-                          : (ent ? logprobs_kernel<L, 256, true, false>
-                                 : logprobs_kernel<L, 256, false, false>);
-    const auto wave = top ? (ent ? logprobs_kernel<L, 64, true, true>
-                                 : logprobs_kernel<L, 64, false, true>)
-                          : (ent ? logprobs_kernel<L, 64, true, false>
-                                 : logprobs_kernel<L, 64, false, false>);
-    int v = launch(plan.threads == 64 ? wave : wide, (int64_t)r.rows * plan.parts, plan.threads, p,
-                   s);
+#define PICK(NT, HELD)                                                                       \
+    (top ? (ent ? logprobs_kernel<L, NT, true, true, HELD> : logprobs_kernel<L, NT, false, true, HELD>) \
+         : (ent ? logprobs_kernel<L, NT, true, false, HELD>                                  \
+                : logprobs_kernel<L, NT, false, false, HELD>))
+    const auto kernel = plan.threads == 64     ? PICK(64, false)
+                        : plan.threads == 256  ? PICK(256, false)
+                                               : PICK(1024, true);
+#undef PICK
+    const int v = launch(kernel, (int64_t)r.rows * plan.parts, plan.threads, p, s);
     if (v != WS_OK || plan.parts == 1) return v;
-    return launch(ent ? logprobs_join_kernel<L, true> : logprobs_join_kernel<L, false>, r.rows, 64,
-                  p, s);
+    return launch(ent ? logprobs_join_kernel<L, true> : logprobs_join_kernel<L, false>, r.rows,
+                  kJoin, p, s);
 }
 
 float scale_c(const ws_rows& r) { return (float)(1.4426950408889634074 / (double)r.temperature); }
@@ -1163,7 +1248,7 @@ extern "C" int ws_logprobs_workspace(const ws_rows* rows, int32_t top_k, size_t*
     const int v = ws::validate_rows(rows);
     if (v != WS_OK) return v;
     if (!bytes || ws::validate_top_k(*rows, top_k) != WS_OK) return WS_E_INVALID_ARG;
-    *bytes = ws::plan_logprobs(*rows, top_k).workspace;
+    *bytes = ws::plan_logprobs(*rows, top_k, false).workspace;
     return WS_OK;
 }
 
@@ -1172,7 +1257,8 @@ extern "C" int ws_logprobs(const ws_rows* rows, const ws_logprobs_args* args, vo
     if (v != WS_OK) return v;
     const ws_rows& r = *rows;
     if (r.rows == 0) return WS_OK;
-    const ws::LogprobsPlan plan = ws::plan_logprobs(r, args->top_k);
+    const ws::LogprobsPlan plan =
+        ws::plan_logprobs(r, args->top_k, ws::rows_aligned(r, args->logits));
     v = ws::validate_workspace(args->workspace, args->workspace_bytes, plan.workspace);
     if (v != WS_OK) return v;
     v = ws::device_ready(r.device);

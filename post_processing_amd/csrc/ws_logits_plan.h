@@ -146,29 +146,50 @@ inline int64_t slots_of(const ws_rows& r) {
     return (r.vocab + vec - 1) / vec;
 }
 
-// ws_logprobs: a row is split into `parts` of `chunk` 16-byte slots (the last
-// takes what is left, one slot more when the row's start is unaligned), one
-// workgroup each, joined by a second kernel.
+// Whether every row starts on 16 bytes.
+inline bool rows_aligned(const ws_rows& r, const void* logits) {
+    return aligned_to(logits, 16) &&
+           (r.rows == 1 || (r.row_stride * logit_bytes(r.dtype)) % 16 == 0);
+}
+
+// A row is split into `parts` of `chunk` 16-byte slots, the last of which takes
+// what is left (fewer than `parts` slots more, and one more still when the
+// row's start is not aligned); a second kernel joins them.
 constexpr int kMaxRowParts = 64;
+constexpr int kBatchSlots = 4;      // slots a thread has in flight in a pass
+constexpr int kHeldLeast = 16;      // from here a row has a slot that lies in it whole
 
 struct LogprobsPlan {
-    int32_t threads = 256;
+    int32_t threads = 256;   // 64 and 256 stream a part, 1024 hold it
     int32_t parts = 1;
     int32_t chunk = 0;
     size_t workspace = 0;
 };
 
-inline LogprobsPlan plan_logprobs(const ws_rows& r, int32_t top_k) {
+// aligned: as rows_aligned says; without it a row may take one slot more, and
+// the workspace (which is asked for before the rows' address is known) is at
+// least that of aligned rows.
+inline LogprobsPlan plan_logprobs(const ws_rows& r, int32_t top_k, bool aligned) {
     LogprobsPlan p;
     if (r.rows == 0) return p;
     const int64_t slots = slots_of(r);
-    p.threads = slots <= 256 ? 64 : 256;
-    int64_t parts = (512 + r.rows - 1) / r.rows;
-    if (parts > slots / 256) parts = slots / 256;
-    if (parts > kMaxRowParts) parts = kMaxRowParts;
-    if (parts < 1) parts = 1;
-    p.chunk = (int32_t)((slots + parts - 1) / parts);
-    p.parts = (int32_t)((slots + p.chunk - 1) / p.chunk);
+    int64_t parts = 1;
+    if (slots <= 256) {
+        p.threads = 64;
+    } else if (r.rows < 1024) {
+        p.threads = 1024;
+        parts = (128 + r.rows - 1) / r.rows;
+        if (parts > slots / 1024) parts = slots / 1024;
+        constexpr int64_t held = kBatchSlots * 1024;
+        const int64_t least = slots + (aligned ? 0 : 1) <= held ? 1 : slots / (held - kMaxRowParts) + 1;
+        if (parts < least) parts = least;
+        if (parts > kMaxRowParts) {
+            p.threads = 256;
+            parts = kMaxRowParts;
+        }
+    }
+    p.parts = (int32_t)parts;
+    p.chunk = (int32_t)(slots / parts);
     // Keys of the best K and the sums (three FP32) of every part.
     if (p.parts > 1)
         p.workspace = (size_t)r.rows * (size_t)p.parts * (8u * (size_t)top_k + 12u);
@@ -191,8 +212,8 @@ inline GradPlan plan_grad(const ws_rows& r) {
     int64_t want = (2048 + r.rows - 1) / r.rows;
     if (want > slots / 256) want = slots / 256;
     if (parts < want) parts = want;
-    p.chunk = (int32_t)((slots + parts - 1) / parts);
-    p.parts = (int32_t)((slots + p.chunk - 1) / p.chunk);
+    p.parts = (int32_t)parts;
+    p.chunk = (int32_t)(slots / parts);
     return p;
 }
 
@@ -200,9 +221,7 @@ inline GradPlan plan_grad(const ws_rows& r) {
 // from the marks of the listed tokens in LDS (a byte a slot); with a gradient,
 // rows that fit the registers of one workgroup (`held` slots a thread) are done
 // in one kernel, others by the loss and then the gradient.
-constexpr int kBatchSlots = 4;      // slots a thread has in flight in a pass
 constexpr int kHeldSlots = 16;
-constexpr int kHeldLeast = 16;      // from here a row has a slot that lies in it whole
 constexpr int kMaxMarkedSlots = 32768;
 
 struct DistillPlan {
@@ -215,15 +234,7 @@ struct DistillPlan {
     size_t workspace = 0;
 };
 
-// Whether every row starts on 16 bytes.
-inline bool rows_aligned(const ws_rows& r, const void* logits) {
-    return aligned_to(logits, 16) &&
-           (r.rows == 1 || (r.row_stride * logit_bytes(r.dtype)) % 16 == 0);
-}
-
-// aligned: as rows_aligned says; without it a row may take one slot more, and
-// the workspace (which is asked for before the rows' address is known) is at
-// least that of aligned rows.
+// aligned: as for plan_logprobs.
 inline DistillPlan plan_distill(const ws_rows& r, int32_t mode, bool gradient, bool aligned) {
     DistillPlan p;
     if (r.rows == 0) return p;
@@ -239,10 +250,10 @@ inline DistillPlan plan_distill(const ws_rows& r, int32_t mode, bool gradient, b
         if (parts > slots / 256) parts = slots / 256;
         if (parts > kMaxRowParts) parts = kMaxRowParts;
         if (parts < 1) parts = 1;
-        if (mode == WS_DISTILL_TAIL && parts * (kMaxMarkedSlots - 1) < slots)
-            parts = (slots + kMaxMarkedSlots - 2) / (kMaxMarkedSlots - 1);
-        p.chunk = (int32_t)((slots + parts - 1) / parts);
-        p.parts = (int32_t)((slots + p.chunk - 1) / p.chunk);
+        const int64_t marked = kMaxMarkedSlots - kMaxRowParts;
+        if (mode == WS_DISTILL_TAIL && parts < slots / marked + 1) parts = slots / marked + 1;
+        p.parts = (int32_t)parts;
+        p.chunk = (int32_t)(slots / parts);
         if (gradient) {
             p.tail_at = (size_t)r.rows * sizeof(ws_row_stats);
             p.sums_at = p.tail_at + (size_t)r.rows * sizeof(float);
@@ -254,7 +265,7 @@ inline DistillPlan plan_distill(const ws_rows& r, int32_t mode, bool gradient, b
     // slots a thread reaches.
     if (mode == WS_DISTILL_TAIL)
         p.mark_bytes = p.held > 0 ? p.held * p.threads
-                                  : (p.chunk + 1 + kBatchSlots * p.threads + 15) / 16 * 16;
+                                  : (p.chunk + p.parts + kBatchSlots * p.threads + 15) / 16 * 16;
     return p;
 }
 
