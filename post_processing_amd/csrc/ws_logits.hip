@@ -156,25 +156,27 @@ __device__ __forceinline__ Sums group_join(Sums a, float c, Sums* wave_sums) {
 }
 
 // A row's best keys as they are collected, in LDS.
-template <typename L, int NT, bool HELD>
+template <typename L, int NT>
 struct Best {
     static constexpr int kListed = 64;                  // threads looked at
-    static constexpr int kScan = NT < 128 ? NT : 128;   // threads that read slots again
-    static constexpr int kRoom = (HELD ? kListed * kBatch : kScan) * L::VEC + WS_MAX_K;
-    static_assert(kRoom >= NT, "room for every thread's pair");
+    static constexpr int kEach = 4;                     // elements a thread reads again
+    static constexpr int kScan = NT * kEach;
+    static constexpr int kFound = kScan + WS_MAX_K;
+    static constexpr int kRoom = kFound > NT ? kFound : NT;   // or a pair a thread
     uint64_t keys[kRoom];
     uint64_t sorted[WS_MAX_K];
     uint32_t groups[64];
     int single[kListed];           // slots to read again
     int thread[kListed];           // threads all of whose slots are read again
     uint32_t bound;
-    int last, picked, singles, threads, count;
+    int last, singles, threads, count;
     bool all;
 };
 
-// Keeps the K best of the collected keys, in order, at the list's start.
-template <typename L, int NT, bool HELD>
-__device__ __forceinline__ int keep_best(Best<L, NT, HELD>& b, int k) {
+// The K best of the collected keys into b.sorted, in order; returns how many
+// (K, or all there are).
+template <typename L, int NT>
+__device__ __forceinline__ int sort_best(Best<L, NT>& b, int k) {
     const int n = b.count;
     for (int i = threadIdx.x; i < n; i += NT) {
         const uint64_t x = b.keys[i];
@@ -182,11 +184,7 @@ __device__ __forceinline__ int keep_best(Best<L, NT, HELD>& b, int k) {
         if (r < k) b.sorted[r] = x;
     }
     __syncthreads();
-    const int kept = n < k ? n : k;
-    if ((int)threadIdx.x < kept) b.keys[threadIdx.x] = b.sorted[threadIdx.x];
-    if (threadIdx.x == 0) b.count = kept;
-    __syncthreads();
-    return kept;
+    return n < k ? n : k;
 }
 
 // The largest of a group of NT / 64 neighbouring lanes, in each of them.
@@ -202,117 +200,118 @@ __device__ __forceinline__ uint32_t lanes_max(uint32_t v, int lane) {
 
 // The K best keys of a part of a row into b.sorted; returns how many there are
 // (K, or the part's elements if fewer).  Joins the sums on the way: in wave 0
-// afterwards.  HELD: the thread's slots are still in w.
-template <typename L, int NT, bool ENT, bool HELD>
+// afterwards.
+template <typename L, int NT, bool ENT>
 __device__ __forceinline__ int select_best(const Part<L>& part, SlotTrack t, Sums& a, float c,
-                                           Sums* wave_sums, const uint4 (&w)[kBatch], int k,
-                                           Best<L, NT, HELD>& b) {
-    using B = Best<L, NT, HELD>;
-    constexpr int kGroup = NT / 64;   // threads of a group
+                                           Sums* wave_sums, int k, Best<L, NT>& b) {
+    using B = Best<L, NT>;
+    constexpr int kGroup = NT / 64;               // threads of a group
+    constexpr int kSorter = NT > 64 ? 64 : 0;     // first thread of the wave that sorts
     const int tid = threadIdx.x, lane = tid & 63;
     const bool has = tid < part.n;
     const uint32_t best = has ? value_image(t.best) : 0;
     const uint32_t second = value_image(t.second);
     // The bound from 64 groups of threads: the K-th largest of their bests,
-    // by one wave (a few more threads reach it than with every thread a group).
+    // by one wave (a few more threads reach it than with every thread a group)
+    // while wave 0 joins the sums.
     const uint32_t group = lanes_max<NT>(best, lane);
     if (lane % kGroup == 0) b.groups[tid / kGroup] = group;
+    if (tid == 0) {
+        b.last = 0x7fffffff;
+        b.singles = b.threads = b.count = 0;
+    }
     a = group_join<NT, ENT, false>(a, c, wave_sums);
     __syncthreads();
     if (tid < 64) {
         a = join_waves<NT, ENT>(a, c, wave_sums);
+        if (tid == 0) b.all = a.s != a.s;   // a NaN in the row, which the maxima skip
+    }
+    if (tid >= kSorter && tid < kSorter + 64) {
         const uint32_t sorted = wave_sort<true>(b.groups[lane], lane);
-        if (lane == 0) {
-            b.all = a.s != a.s;   // a NaN in the row, which the maxima skip
-            b.last = 0x7fffffff;
-            b.picked = b.singles = b.threads = b.count = 0;
-        }
         if (lane == k - 1) b.bound = sorted;
     }
     __syncthreads();
     const bool all = b.all;
-    if (has && best >= b.bound) atomicAdd(&b.picked, 1);
+    uint32_t bound = b.bound;
+    uint64_t least = all ? 0 : (uint64_t)bound << 32;
+    // A thread's slots that may hold elements at the bound: its best, or, if
+    // its second largest slot maximum is there too, any.  (With equal bests
+    // cut off behind slot `last`: a second slot at the bound comes at least NT
+    // slots after the first when both are.)
+    const auto list_slots = [&](bool chosen, int last) {
+        if (chosen) {
+            const bool more = second > bound ||
+                              (second == bound && (best > bound || (int64_t)t.slot + NT <= last));
+            int* list = more ? b.thread : b.single;
+            const int at = atomicAdd(more ? &b.threads : &b.singles, 1);
+            if (at < B::kListed) list[at] = more ? tid : t.slot;
+        }
+    };
+    const bool chosen = has && !all && best >= bound;
+    list_slots(chosen, 0x7fffffff);
     __syncthreads();
-    if (b.picked > B::kListed) {
+    if (b.singles > B::kListed || b.threads > B::kListed) {
         // Many reach the bound (equal values): exactly K threads then, by best
-        // and slot, and the K-th's as the bound.
+        // and slot; of elements equal to the K-th's best, those up to its slot.
+        __syncthreads();
         const uint64_t pair = has ? ((uint64_t)best << 32) | (uint32_t)~t.slot : 0;
         b.keys[tid] = pair;
+        if (tid == 0) b.singles = b.threads = b.count = 0;
         __syncthreads();
-        if (has && best >= b.bound && keys_above(b.keys, NT, pair) == k - 1) {
-            b.groups[0] = best;
+        const bool among = has && best >= bound && keys_above(b.keys, NT, pair) < k;
+        if (among && keys_above(b.keys, NT, pair) == k - 1) {
+            b.bound = best;
             b.last = t.slot;
         }
         __syncthreads();
-        if (tid == 0) b.bound = b.groups[0];
+        bound = b.bound;
+        const int last = b.last;
+        least = ((uint64_t)bound << 32) | (uint32_t)~(part.e0 + last * L::VEC + L::VEC - 1);
+        list_slots(among, last);
         __syncthreads();
     }
-    const uint32_t bound = b.bound;
-    const int last = b.last;
-    const uint32_t edge = last == 0x7fffffff ? 0xffffffffu
-                                             : (uint32_t)(part.e0 + last * L::VEC + L::VEC - 1);
-    uint64_t least = all ? 0 : ((uint64_t)bound << 32) | (uint32_t)~edge;
-    const bool chosen = has && !all && (best > bound || (best == bound && t.slot <= last));
-    const auto collect = [&](int slot, const float (&v)[L::VEC]) {
-#pragma unroll
-        for (int j = 0; j < L::VEC; ++j) {
-            const int e = part.e0 + slot * L::VEC + j;
-            const uint64_t key = value_key(v[j], (uint32_t)e);
-            if (key >= least && e >= 0 && e < part.vocab) b.keys[atomicAdd(&b.count, 1)] = key;
-        }
-    };
-    if constexpr (HELD) {
-        if (!all) {
-            if (chosen) {
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    float v[L::VEC];
-                    L::unpack(w[i], v);
-                    if (tid + i * NT < part.n && value_image(slot_max<L::VEC>(v)) >= bound)
-                        collect(tid + i * NT, v);
-                }
-            }
-            __syncthreads();
-            return keep_best(b, k);
-        }
-    }
-    const int rounds_per_thread = (part.n + NT - 1) / NT;
-    if (chosen) {
-        // A second slot at the bound counts only if it is not beyond `last`; it
-        // comes at least NT slots after the first when both are at the bound.
-        const bool more = second > bound ||
-                          (second == bound && (best > bound || (int64_t)t.slot + NT <= last));
-        if (more) b.thread[atomicAdd(&b.threads, 1)] = tid;
-        else b.single[atomicAdd(&b.singles, 1)] = t.slot;
-    }
-    __syncthreads();
-    const int singles = b.singles;
-    const int items = all ? part.n : singles + b.threads * rounds_per_thread;
+    // Element by element: little code, as it runs once a row, and few rounds.
+    const int each = (part.n + NT - 1) / NT * L::VEC;   // elements of a thread's slots
+    const int singles = b.singles * L::VEC;
+    const int items = all ? part.n * L::VEC : singles + b.threads * each;
     for (int from = 0;; from += B::kScan) {
-        const int item = from + tid;
-        if (tid < B::kScan && item < items) {
-            int slot = item;
-            if (!all) {
-                if (item < singles) {
-                    slot = b.single[item];
-                } else {
-                    const int j = item - singles;
-                    slot = b.thread[j / rounds_per_thread] + (j % rounds_per_thread) * NT;
+        typename L::Elem x[B::kEach];
+        int e[B::kEach];
+#pragma unroll
+        for (int i = 0; i < B::kEach; ++i) {
+            const int item = from + tid + i * NT;
+            e[i] = -1;
+            if (item < items) {
+                int at = item;   // element of the part
+                if (!all) {
+                    if (item < singles) {
+                        at = b.single[item / L::VEC] * L::VEC + item % L::VEC;
+                    } else {
+                        const int j = item - singles;
+                        const int slot = b.thread[j / each] + j % each / L::VEC * NT;
+                        at = slot < part.n ? slot * L::VEC + j % L::VEC : part.vocab - part.e0;
+                    }
                 }
+                e[i] = part.e0 + at;
             }
-            if (slot < part.n) {
-                float v[L::VEC];
-                part.load_any(slot, v);
-                collect(slot, v);
-            }
+            x[i] = part.row[e[i] < 0 ? 0 : e[i] < part.vocab ? e[i] : part.vocab - 1];
+        }
+#pragma unroll
+        for (int i = 0; i < B::kEach; ++i) {
+            const uint64_t key = value_key(L::up(x[i]), (uint32_t)e[i]);
+            if (key >= least && e[i] >= 0 && e[i] < part.vocab) b.keys[atomicAdd(&b.count, 1)] = key;
         }
         __syncthreads();
-        const bool more = from + B::kScan < items;
-        if (!more || b.count > WS_MAX_K) {
-            const int kept = keep_best(b, k);
-            if (!more) return kept;
-            if (kept == k) least = umax64(least, b.sorted[k - 1]);
-        }
+        if (from + B::kScan >= items) return sort_best(b, k);
+        const int found = b.count;
+        __syncthreads();   // everyone has read it before anyone adds to it
+        if (found <= WS_MAX_K) continue;
+        const int kept = sort_best(b, k);
+        // Room for the next round: the K best so far, and a higher bound.
+        if (tid < kept) b.keys[tid] = b.sorted[tid];
+        if (tid == 0) b.count = kept;
+        if (kept == k) least = umax64(least, b.sorted[k - 1]);
+        __syncthreads();
     }
 }
 
@@ -379,11 +378,10 @@ struct Select<false, T> {
     using Type = Nothing;
 };
 
-// HELD: a part is at most kBatch slots a thread, which stay in registers.
-template <typename L, int NT, bool ENT, bool TOPK, bool HELD>
+template <typename L, int NT, bool ENT, bool TOPK>
 __global__ void __launch_bounds__(NT) logprobs_kernel(LogprobsParams p) {
     __shared__ Sums wave_sums[NT / 64];
-    __shared__ typename Select<TOPK, Best<L, NT, HELD>>::Type best;
+    __shared__ typename Select<TOPK, Best<L, NT>>::Type best;
     const int tid = threadIdx.x;
     const int64_t row = blockIdx.x / (uint32_t)p.parts;
     const int index = (int)(blockIdx.x % (uint32_t)p.parts);
@@ -392,25 +390,10 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(LogprobsParams p) {
 
     Sums a;
     SlotTrack t;
-    uint4 w[kBatch];
-    if constexpr (HELD) {
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) w[i] = part.load_near(tid + i * NT);
-        float v[kBatch][L::VEC];
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            part.settle(tid + i * NT, w[i]);
-            L::unpack(w[i], v[i]);
-        }
-        a.init();
-        t = {-INFINITY, -INFINITY, tid};
-        take_slots<L, NT, ENT, TOPK, false>(v, tid, p.c, nullptr, a, t);
-    } else {
-        stream_part<L, NT, ENT, TOPK, false>(part, p.c, nullptr, a, t);
-    }
+    stream_part<L, NT, ENT, TOPK, false>(part, p.c, nullptr, a, t);
     int kept = 0;
     if constexpr (TOPK) {
-        kept = select_best<L, NT, ENT, HELD>(part, t, a, p.c, wave_sums, w, p.k, best);
+        kept = select_best<L, NT, ENT>(part, t, a, p.c, wave_sums, p.k, best);
     } else {
         a = group_join<NT, ENT>(a, p.c, wave_sums);
     }
@@ -1177,13 +1160,10 @@ template <typename L>
 int run_logprobs(const ws_rows& r, const LogprobsPlan& plan, const LogprobsParams& p,
                  hipStream_t s) {
     const bool ent = p.entropy != nullptr, top = p.k > 0;
-#define PICK(NT, HELD)                                                                       \
-    (top ? (ent ? logprobs_kernel<L, NT, true, true, HELD> : logprobs_kernel<L, NT, false, true, HELD>) \
-         : (ent ? logprobs_kernel<L, NT, true, false, HELD>                                  \
-                : logprobs_kernel<L, NT, false, false, HELD>))
-    const auto kernel = plan.threads == 64     ? PICK(64, false)
-                        : plan.threads == 256  ? PICK(256, false)
-                                               : PICK(1024, true);
+#define PICK(NT)                                                                           \
+    (top ? (ent ? logprobs_kernel<L, NT, true, true> : logprobs_kernel<L, NT, false, true>) \
+         : (ent ? logprobs_kernel<L, NT, true, false> : logprobs_kernel<L, NT, false, false>))
+    const auto kernel = plan.threads == 64 ? PICK(64) : PICK(256);
 #undef PICK
     const int v = launch(kernel, (int64_t)r.rows * plan.parts, plan.threads, p, s);
     if (v != WS_OK || plan.parts == 1) return v;
@@ -1248,7 +1228,7 @@ extern "C" int ws_logprobs_workspace(const ws_rows* rows, int32_t top_k, size_t*
     const int v = ws::validate_rows(rows);
     if (v != WS_OK) return v;
     if (!bytes || ws::validate_top_k(*rows, top_k) != WS_OK) return WS_E_INVALID_ARG;
-    *bytes = ws::plan_logprobs(*rows, top_k, false).workspace;
+    *bytes = ws::plan_logprobs(*rows, top_k).workspace;
     return WS_OK;
 }
 
@@ -1257,8 +1237,7 @@ extern "C" int ws_logprobs(const ws_rows* rows, const ws_logprobs_args* args, vo
     if (v != WS_OK) return v;
     const ws_rows& r = *rows;
     if (r.rows == 0) return WS_OK;
-    const ws::LogprobsPlan plan =
-        ws::plan_logprobs(r, args->top_k, ws::rows_aligned(r, args->logits));
+    const ws::LogprobsPlan plan = ws::plan_logprobs(r, args->top_k);
     v = ws::validate_workspace(args->workspace, args->workspace_bytes, plan.workspace);
     if (v != WS_OK) return v;
     v = ws::device_ready(r.device);

@@ -160,34 +160,21 @@ constexpr int kBatchSlots = 4;      // slots a thread has in flight in a pass
 constexpr int kHeldLeast = 16;      // from here a row has a slot that lies in it whole
 
 struct LogprobsPlan {
-    int32_t threads = 256;   // 64 and 256 stream a part, 1024 hold it
+    int32_t threads = 256;
     int32_t parts = 1;
     int32_t chunk = 0;
     size_t workspace = 0;
 };
 
-// aligned: as rows_aligned says; without it a row may take one slot more, and
-// the workspace (which is asked for before the rows' address is known) is at
-// least that of aligned rows.
-inline LogprobsPlan plan_logprobs(const ws_rows& r, int32_t top_k, bool aligned) {
+inline LogprobsPlan plan_logprobs(const ws_rows& r, int32_t top_k) {
     LogprobsPlan p;
     if (r.rows == 0) return p;
     const int64_t slots = slots_of(r);
-    int64_t parts = 1;
-    if (slots <= 256) {
-        p.threads = 64;
-    } else if (r.rows < 1024) {
-        p.threads = 1024;
-        parts = (128 + r.rows - 1) / r.rows;
-        if (parts > slots / 1024) parts = slots / 1024;
-        constexpr int64_t held = kBatchSlots * 1024;
-        const int64_t least = slots + (aligned ? 0 : 1) <= held ? 1 : slots / (held - kMaxRowParts) + 1;
-        if (parts < least) parts = least;
-        if (parts > kMaxRowParts) {
-            p.threads = 256;
-            parts = kMaxRowParts;
-        }
-    }
+    p.threads = slots <= 256 ? 64 : 256;
+    int64_t parts = (16 + r.rows - 1) / r.rows;
+    if (parts > slots / 256) parts = slots / 256;
+    if (parts > kMaxRowParts) parts = kMaxRowParts;
+    if (parts < 1) parts = 1;
     p.parts = (int32_t)parts;
     p.chunk = (int32_t)(slots / parts);
     // Keys of the best K and the sums (three FP32) of every part.
@@ -234,7 +221,9 @@ struct DistillPlan {
     size_t workspace = 0;
 };
 
-// aligned: as for plan_logprobs.
+// aligned: as rows_aligned says; without it a row may take one slot more, and
+// the workspace (which is asked for before the rows' address is known) is at
+// least that of aligned rows.
 inline DistillPlan plan_distill(const ws_rows& r, int32_t mode, bool gradient, bool aligned) {
     DistillPlan p;
     if (r.rows == 0) return p;

@@ -162,23 +162,7 @@ struct Part {
             v[j] = e >= 0 && e < vocab ? L::up(x[j]) : -INFINITY;
         }
     }
-    // Makes load_near's content of slot s right when s is not whole: the
-    // elements in the row, -inf elsewhere.
-    __device__ __forceinline__ void settle(int s, uint4& w) const {
-        if (__ballot(!whole(s)) == 0) return;
-        if (whole(s)) return;
-        w = L::none();
-        if (s < n) {
-            float v[VEC];
-            load_edge(s, v);
-            w = L::pack(v);
-        }
-    }
     __device__ __forceinline__ bool whole(int s) const { return s >= full_from && s < full_to; }
-    __device__ __forceinline__ void load_any(int s, float (&v)[VEC]) const {
-        if (whole(s)) L::unpack(load(s), v);
-        else load_edge(s, v);
-    }
     __device__ __forceinline__ float at(int e) const { return L::up(row[e]); }
 };
 
