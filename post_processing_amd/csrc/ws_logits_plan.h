@@ -159,6 +159,30 @@ constexpr int kMaxRowParts = 64;
 constexpr int kBatchSlots = 4;      // slots a thread has in flight in a pass
 constexpr int kHeldLeast = 16;      // from here a row has a slot that lies in it whole
 
+// Workgroups a row is split over.  The join costs about 4 us (MI355X, best 20;
+// 2 us without), so rows are split that would take a workgroup longer than
+// that and only while they leave CUs idle: 131,072 BF16 logits with the best 20
+// in 1 / 8 / 16 parts 17.0 / 11.3 / 10.6 us for 16 rows, 1 / 4 / 8 parts 17.3 /
+// 15.0 / 14.6 us for 64 rows, 1 / 2 parts 28.6 / 23.3 us for 256; 32,768 logits
+// 7.7 us whole, 10.5 in 4 parts.
+constexpr int64_t kSplitSlots = 6144, kPartSlots = 1024, kSplitGroups = 512;
+
+inline int64_t row_parts(const ws_rows& r) {
+    const int64_t slots = slots_of(r);
+    if (slots <= kSplitSlots) return 1;
+    int64_t parts = kSplitGroups / r.rows;
+    if (parts > slots / kPartSlots) parts = slots / kPartSlots;
+    if (parts > kMaxRowParts) parts = kMaxRowParts;
+    return parts < 1 ? 1 : parts;
+}
+
+// Threads of a workgroup that takes a row or part: one wave for short rows
+// (4,096 rows of 4,096 BF16 logits with the best 20: 15.4 us with one wave, 20.1
+// with four; of 8,192 logits 23.4 and 22.2), four otherwise.
+constexpr int64_t kWaveSlots = 512;
+
+inline int32_t row_threads(const ws_rows& r) { return slots_of(r) <= kWaveSlots ? 64 : 256; }
+
 struct LogprobsPlan {
     int32_t threads = 256;
     int32_t parts = 1;
@@ -169,14 +193,9 @@ struct LogprobsPlan {
 inline LogprobsPlan plan_logprobs(const ws_rows& r, int32_t top_k) {
     LogprobsPlan p;
     if (r.rows == 0) return p;
-    const int64_t slots = slots_of(r);
-    p.threads = slots <= 256 ? 64 : 256;
-    int64_t parts = (16 + r.rows - 1) / r.rows;
-    if (parts > slots / 256) parts = slots / 256;
-    if (parts > kMaxRowParts) parts = kMaxRowParts;
-    if (parts < 1) parts = 1;
-    p.parts = (int32_t)parts;
-    p.chunk = (int32_t)(slots / parts);
+    p.threads = row_threads(r);
+    p.parts = (int32_t)row_parts(r);
+    p.chunk = (int32_t)(slots_of(r) / p.parts);
     // Keys of the best K and the sums (three FP32) of every part.
     if (p.parts > 1)
         p.workspace = (size_t)r.rows * (size_t)p.parts * (8u * (size_t)top_k + 12u);
@@ -184,8 +203,11 @@ inline LogprobsPlan plan_logprobs(const ws_rows& r, int32_t top_k) {
 }
 
 // Gradients: parts of a row as above, each workgroup reading the row's named
-// tokens for itself.
-constexpr int kGradChunk = 4096;
+// tokens for itself.  2,048 slots a workgroup (MI355X, 4,096 rows of 65,536 BF16
+// with entropy, in us: 1,024 slots 195, 2,048 189, 4,096 205, 8,192 221), and
+// enough of them for few rows (255 rows of 50,001 FP16: 512 workgroups 14.8,
+// 1,024 12.8, 2,048 14.9, 4,096 17.2).
+constexpr int64_t kGradSlots = 2048, kGradLeast = 256, kGradGroups = 1024;
 
 struct GradPlan {
     int32_t parts = 1;
@@ -195,9 +217,9 @@ struct GradPlan {
 inline GradPlan plan_grad(const ws_rows& r) {
     GradPlan p;
     const int64_t slots = slots_of(r);
-    int64_t parts = (slots + kGradChunk - 1) / kGradChunk;
-    int64_t want = (2048 + r.rows - 1) / r.rows;
-    if (want > slots / 256) want = slots / 256;
+    int64_t parts = (slots + kGradSlots - 1) / kGradSlots;
+    int64_t want = (kGradGroups + r.rows - 1) / r.rows;
+    if (want > slots / kGradLeast) want = slots / kGradLeast;
     if (parts < want) parts = want;
     p.parts = (int32_t)parts;
     p.chunk = (int32_t)(slots / parts);
@@ -205,10 +227,14 @@ inline GradPlan plan_grad(const ws_rows& r) {
 }
 
 // ws_distill: the loss as ws_logprobs splits its rows, with a limit to a part
-// from the marks of the listed tokens in LDS (a byte a slot); with a gradient,
+// from the marks of the listed tokens in LDS (a byte a slot).  With a gradient,
 // rows that fit the registers of one workgroup (`held` slots a thread) are done
-// in one kernel, others by the loss and then the gradient.
+// in one kernel; longer ones, and long ones too few to fill the CUs, by the loss
+// and then the gradient (MI355X, 131,072 BF16 logits: 32 rows 21.3 us held, 17.7
+// in three kernels and the gaps between them, 64 rows 23.0 and 20.4, 128 rows
+// 25.0 and 26.4; 32,768 logits: 32 rows 12.6 and 15.5 us, 256 rows 15.0 and 21).
 constexpr int kHeldSlots = 16;
+constexpr int kHeldRows = 64;
 constexpr int kMaxMarkedSlots = 32768;
 
 struct DistillPlan {
@@ -229,16 +255,14 @@ inline DistillPlan plan_distill(const ws_rows& r, int32_t mode, bool gradient, b
     if (r.rows == 0) return p;
     const int64_t slots = slots_of(r);
     const int64_t most = slots + (aligned ? 0 : 1);
-    if (gradient && most <= kHeldSlots * 1024 && r.rows >= 128 && r.vocab >= kHeldLeast) {
+    if (gradient && most <= kHeldSlots * 1024 && r.vocab >= kHeldLeast &&
+        (slots <= kSplitSlots || r.rows >= kHeldRows)) {
         p.held = kHeldSlots;
         p.threads = most <= kHeldSlots * 256 ? 256 : most <= kHeldSlots * 512 ? 512 : 1024;
         p.chunk = (int32_t)slots;
     } else {
-        p.threads = slots <= 256 ? 64 : 256;
-        int64_t parts = (512 + r.rows - 1) / r.rows;
-        if (parts > slots / 256) parts = slots / 256;
-        if (parts > kMaxRowParts) parts = kMaxRowParts;
-        if (parts < 1) parts = 1;
+        p.threads = row_threads(r);
+        int64_t parts = row_parts(r);
         const int64_t marked = kMaxMarkedSlots - kMaxRowParts;
         if (mode == WS_DISTILL_TAIL && parts < slots / marked + 1) parts = slots / marked + 1;
         p.parts = (int32_t)parts;
