@@ -1163,7 +1163,7 @@ int run_logprobs(const ws_rows& r, const LogprobsPlan& plan, const LogprobsParam
 #define PICK(NT)                                                                           \
     (top ? (ent ? logprobs_kernel<L, NT, true, true> : logprobs_kernel<L, NT, false, true>) \
          : (ent ? logprobs_kernel<L, NT, true, false> : logprobs_kernel<L, NT, false, false>))
-    const auto kernel = plan.threads == 64 ? PICK(64) : PICK(256);
+    const auto kernel = plan.threads == 64 ? PICK(64) : plan.threads == 256 ? PICK(256) : PICK(1024);
 #undef PICK
     const int v = launch(kernel, (int64_t)r.rows * plan.parts, plan.threads, p, s);
     if (v != WS_OK || plan.parts == 1) return v;
@@ -1194,8 +1194,9 @@ int run_distill(const ws_rows& r, const DistillPlan& plan, const DistillParams& 
                                                   : distill_step_kernel<L, 1024, TAIL>;
         return launch(kernel, r.rows, plan.threads, p, s, lds);
     }
-    const int v = launch(plan.threads == 64 ? distill_kernel<L, 64, TAIL>
-                                            : distill_kernel<L, 256, TAIL>,
+    const int v = launch(plan.threads == 64    ? distill_kernel<L, 64, TAIL>
+                         : plan.threads == 256 ? distill_kernel<L, 256, TAIL>
+                                               : distill_kernel<L, 1024, TAIL>,
                          (int64_t)r.rows * plan.parts, plan.threads, p, s, lds);
     if (v != WS_OK || plan.parts == 1) return v;
     return launch(distill_join_kernel<L>, r.rows, 64, p, s);

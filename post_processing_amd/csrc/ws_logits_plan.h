@@ -176,12 +176,17 @@ inline int64_t row_parts(const ws_rows& r) {
     return parts < 1 ? 1 : parts;
 }
 
-// Threads of a workgroup that takes a row or part: one wave for short rows
-// (4,096 rows of 4,096 BF16 logits with the best 20: 15.4 us with one wave, 20.1
-// with four; of 8,192 logits 23.4 and 22.2), four otherwise.
-constexpr int64_t kWaveSlots = 512;
+// Threads of a workgroup that takes `slots` slots: one wave for short rows
+// (MI355X, 4,096 rows of 4,096 BF16 logits with the best 20: 15.4 us with one
+// wave, 20.1 with four; of 8,192 logits 23.4 and 22.2), sixteen for long ones,
+// where fewer rows are in flight at once (4,096 rows with entropy: of 131,072
+// logits 185 us with four waves, 172 with sixteen; of 100,001 152 and 141; of
+// 81,920, which end amid a batch, 120 and 129), four otherwise.
+constexpr int64_t kWaveSlots = 512, kWideSlots = 12288;
 
-inline int32_t row_threads(const ws_rows& r) { return slots_of(r) <= kWaveSlots ? 64 : 256; }
+inline int32_t row_threads(int64_t slots) {
+    return slots <= kWaveSlots ? 64 : slots < kWideSlots ? 256 : 1024;
+}
 
 struct LogprobsPlan {
     int32_t threads = 256;
@@ -193,9 +198,9 @@ struct LogprobsPlan {
 inline LogprobsPlan plan_logprobs(const ws_rows& r, int32_t top_k) {
     LogprobsPlan p;
     if (r.rows == 0) return p;
-    p.threads = row_threads(r);
     p.parts = (int32_t)row_parts(r);
     p.chunk = (int32_t)(slots_of(r) / p.parts);
+    p.threads = row_threads(p.chunk);
     // Keys of the best K and the sums (three FP32) of every part.
     if (p.parts > 1)
         p.workspace = (size_t)r.rows * (size_t)p.parts * (8u * (size_t)top_k + 12u);
@@ -261,12 +266,12 @@ inline DistillPlan plan_distill(const ws_rows& r, int32_t mode, bool gradient, b
         p.threads = most <= kHeldSlots * 256 ? 256 : most <= kHeldSlots * 512 ? 512 : 1024;
         p.chunk = (int32_t)slots;
     } else {
-        p.threads = row_threads(r);
         int64_t parts = row_parts(r);
         const int64_t marked = kMaxMarkedSlots - kMaxRowParts;
         if (mode == WS_DISTILL_TAIL && parts < slots / marked + 1) parts = slots / marked + 1;
         p.parts = (int32_t)parts;
         p.chunk = (int32_t)(slots / parts);
+        p.threads = row_threads(p.chunk);
         if (gradient) {
             p.tail_at = (size_t)r.rows * sizeof(ws_row_stats);
             p.sums_at = p.tail_at + (size_t)r.rows * sizeof(float);
