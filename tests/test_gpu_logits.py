@@ -306,6 +306,66 @@ def test_logprobs_many_short_rows(gpu_lib):
     check_logprobs(mat, 1.0, rng.integers(0, 37, 3001), k=4)
 
 
+def _repeated(rows, z):
+    """`rows` rows that repeat z's, so the later ones can be held to the first
+    bit for bit."""
+    return np.broadcast_to(z[np.arange(rows) % len(z)], (rows, z.shape[1]))
+
+
+@pytest.mark.parametrize("dtype,V,pad,shift", [("f32", 50003, 0, 0), ("bf16", 99001, 3, 1),
+                                               ("f16", 131072, 0, 0)])
+def test_logprobs_many_long_rows(gpu_lib, dtype, V, pad, shift):
+    """Rows too many to split, long enough for the widest workgroups: masked,
+    tied, NaN and ordinary ones, each several times over."""
+    z = special_rows(V, dtype)
+    mat = Matrix(_repeated(300, z), dtype, pad, shift, marker=1e4)
+    n = len(z)
+    targets = (np.arange(300) % n) * 1009 % V
+    got = run_logprobs(mat, 1.0, targets, k=32)
+    first = Matrix(z, dtype)
+    first.z = mat.z[:n]
+    check_logprobs(first, 1.0, targets[:n], k=32, got={key: got[key][:n] for key in got
+                                                       if key != "device"})
+    for key in ("logprob", "entropy", "stats", "top"):
+        np.testing.assert_array_equal(got[key].view(np.int32),
+                                      got[key][np.arange(300) % n].view(np.int32))
+    assert mat.outside_untouched()
+
+
+@pytest.mark.parametrize("V", [1 << 20, (1 << 20) + 5])
+def test_logprobs_very_long_row(gpu_lib, V):
+    rng = np.random.default_rng(V)
+    z = np.concatenate([_logits(rng, 2, V), special_rows(V, "bf16")[[4, 5, 8, 10, 13]]])
+    check_logprobs(Matrix(z, "bf16", 1, 1), 1.0, rng.integers(0, V, 7), k=32)
+
+
+@pytest.mark.parametrize("mode", [0, 1])
+@pytest.mark.parametrize("dtype,rows,V", [("f32", 3, 300001), ("f32", 300, 140001),
+                                          ("bf16", 2, 700001), ("bf16", 300, 99001)])
+def test_distill_long_rows(gpu_lib, mode, dtype, rows, V):
+    """Rows past what a workgroup holds, few and many, where the listed tokens'
+    marks limit a part."""
+    rng = np.random.default_rng(V)
+    z = _logits(rng, 2, V)
+    mat = Matrix(_repeated(rows, z), dtype, 1, 1)
+    ids, scores = make_teacher(rng, mat.z[:2], 70, mode)
+    ids[0, 3], ids[1, 5] = V - 1, 0
+    at = np.arange(rows) % 2
+    g = np.ones(rows)
+    loss, grad, _, _ = run_distill(mat, 1.0, ids[at], scores[at], mode, g)
+    # The same row at a start that lies alike within 16 bytes: the same bits.
+    vec = 4 if dtype == "f32" else 8
+    first = {}
+    for r in range(rows):
+        f = first.setdefault((r % 2, (1 + r * mat.stride) % vec), r)
+        assert loss[r] == loss[f] and (grad[r] == grad[f]).all()
+    small = Matrix(z, dtype, 1, 1)
+    check_distill(small, 1.0, ids, scores, mode, g[:2])
+    check_distill(small, 1.0, ids, scores, mode, g[:2], separate=True)
+    want, _, _ = ol.distill(mat.z[0], 1.0, scores[0].astype(np.float64), ids[0], mode)
+    assert abs(loss[0] - want) <= 4 * (_sum_tol(V) + 16 * E) * 20
+
+
 def test_logprobs_offsets_past_32_bits(gpu_lib):
     """Rows whose elements start past 2^31 and bytes past 2^32."""
     import torch
