@@ -475,16 +475,18 @@ struct Named {
     bool bad;          // some index lies outside the row (wave-uniform)
 };
 
-// The token's logits, and whether any index lies outside.  Read before any
-// thread writes a gradient over the logits.
+// The logits of the tokens in [from, to), and whether any index lies outside
+// the row.  Read before any thread writes a gradient over the logits (other
+// workgroups may be writing theirs outside that range).
 template <typename L>
-__device__ __forceinline__ void read_named(Named& n, const typename L::Elem* row, int V) {
+__device__ __forceinline__ void read_named(Named& n, const typename L::Elem* row, int V, int from,
+                                           int to) {
     bool bad = false;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         n.z[h] = -INFINITY;
-        if (n.id[h] < (uint32_t)V) n.z[h] = L::up(row[n.id[h]]);
-        else if (n.id[h] != kAbsent) bad = true;
+        if (n.id[h] >= (uint32_t)from && n.id[h] < (uint32_t)to) n.z[h] = L::up(row[n.id[h]]);
+        bad |= n.id[h] >= (uint32_t)V && n.id[h] != kAbsent;
     }
     n.bad = __ballot(bad) != 0;
 }
@@ -788,7 +790,7 @@ __global__ void __launch_bounds__(NT) distill_kernel(DistillParams p) {
     if (tid < 64) {
         read_entries(n, p.teacher + row * p.k, p.k, lane);
         if (p.parts == 1) {
-            read_named<L>(n, part.row, p.vocab);
+            read_named<L>(n, part.row, p.vocab, 0, p.vocab);
             t = weigh_teacher(n, p.k, p.mode, lane);
         }
     }
@@ -817,11 +819,12 @@ __global__ void __launch_bounds__(64) distill_join_kernel(DistillParams p) {
     const int64_t row = blockIdx.x;
     Sums a;
     a.init();
-    if (lane < p.parts) a = p.sums[row * p.parts + lane];
+    for (int i = lane; i < p.parts; i += 64) a.add<false>(p.sums[row * p.parts + i], p.c);
     Named n;
     read_entries(n, p.teacher + row * p.k, p.k, lane);
     Teacher t = weigh_teacher(n, p.k, p.mode, lane);
-    read_named<L>(n, static_cast<const typename L::Elem*>(p.logits) + row * p.stride, p.vocab);
+    read_named<L>(n, static_cast<const typename L::Elem*>(p.logits) + row * p.stride, p.vocab, 0,
+                  p.vocab);
     if (p.mode == WS_DISTILL_TAIL) {
         merge_named(n, p.k, ids, adds, lane);
         settle_rest(t, n, p.k, p.vocab);
@@ -914,12 +917,12 @@ struct GradParams {
 // The row's slope and named tokens, by wave 0.
 template <typename L, bool DISTILL>
 __device__ __forceinline__ Slope grad_slope(const GradParams& p, int64_t row,
-                                            const typename L::Elem* z, Named& n, uint32_t* ids,
-                                            float* adds, int lane) {
+                                            const typename L::Elem* z, int from, int to, Named& n,
+                                            uint32_t* ids, float* adds, int lane) {
     const ws_row_stats st = p.stats[row];
     if constexpr (DISTILL) {
         read_entries(n, p.entries + row * p.k, p.k, lane);
-        read_named<L>(n, z, p.vocab);
+        read_named<L>(n, z, p.vocab, from, to);
         Teacher t = weigh_teacher(n, p.k, p.mode, lane);
         merge_named(n, p.k, ids, adds, lane);
         double tail = 0.0;
@@ -939,7 +942,7 @@ __device__ __forceinline__ Slope grad_slope(const GradParams& p, int64_t row,
             n.id[0] = (uint32_t)p.targets[row];
             if (n.id[0] != kAbsent) n.add[0] = p.grad_target[row];
         }
-        read_named<L>(n, z, p.vocab);
+        read_named<L>(n, z, p.vocab, from, to);
         Slope s;
         s.none = false;
         s.max = st.max;
@@ -974,9 +977,11 @@ __global__ void __launch_bounds__(256) grad_kernel(GradParams p) {
               (int)(blockIdx.x % (uint32_t)p.parts));
     PartOut<L> out;
     out.init(part, p.grad, row * p.grad_stride);
+    const int from = part.e0 < 0 ? 0 : part.e0;
+    const int to = part.e0 + part.n * VEC < p.vocab ? part.e0 + part.n * VEC : p.vocab;
     Named n;
     if (tid < 64) {
-        const Slope s = grad_slope<L, DISTILL>(p, row, part.row, n, ids, adds, tid);
+        const Slope s = grad_slope<L, DISTILL>(p, row, part.row, from, to, n, ids, adds, tid);
         if (tid == 0) slope = s;
     }
     __syncthreads();   // every named logit is read before any is overwritten
@@ -1006,11 +1011,7 @@ __global__ void __launch_bounds__(256) grad_kernel(GradParams p) {
         }
     }
     __syncthreads();
-    if (tid < 64) {
-        const int from = part.e0 < 0 ? 0 : part.e0;
-        const int to = part.e0 + part.n * VEC;
-        store_named<L, ENT, DISTILL>(g, n, p.c, from, to, out.row);
-    }
+    if (tid < 64) store_named<L, ENT, DISTILL>(g, n, p.c, from, to, out.row);
 }
 
 // Loss and gradient of a row in one pass: the row stays in the registers of
@@ -1058,7 +1059,7 @@ __global__ void __launch_bounds__(NT, 4) distill_step_kernel(DistillParams p) {
 #pragma unroll
     for (int i = kAhead; i < R; ++i) w[i] = part.load_near(tid + i * NT);
     if (tid < 64) {   // while the row is on its way
-        read_named<L>(n, part.row, p.vocab);
+        read_named<L>(n, part.row, p.vocab, 0, p.vocab);
         t = weigh_teacher(n, p.k, p.mode, lane);
         merge_named(n, p.k, ids, adds, lane);
         if constexpr (TAIL) settle_rest(t, n, p.k, p.vocab);

@@ -188,6 +188,14 @@ struct Sums {
         s *= a;
         m = to;
     }
+    template <bool ENT>
+    __device__ __forceinline__ void add(Sums b, float c) {
+        const float to = fmaxf(m, b.m);
+        raise<ENT>(to, c);
+        b.raise<ENT>(to, c);
+        s += b.s;
+        if constexpr (ENT) u += b.u;
+    }
 };
 
 template <int J>

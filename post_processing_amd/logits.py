@@ -11,9 +11,10 @@ operator each time ``run`` is called, on the buffers' contents of that moment:
 
 Buffers are torch tensors (anything with ``data_ptr()``) or integer device
 addresses.  A tensor's element type, device and size are checked when the call
-object is built; an address is taken as it is.  The call object keeps the
-tensors alive.  ``stream`` is a hipStream_t handle (int) or None for the null
-stream, as in ``ws.run_noalloc``.
+object is built; an address is taken as it is.  ``stream`` is a hipStream_t
+handle (int) or None for the null stream, as in ``ws.run_noalloc``.  The call
+object keeps the tensors alive: keep it until the stream has passed its last
+run, and for as long as a graph that captured it may be replayed.
 
 When an operator needs a workspace and none is given, the call object holds
 one of its own, taken from torch; so two runs of one call object must not
@@ -91,13 +92,20 @@ def load():
     return lib
 
 
+def _int32(name, v) -> int:
+    """`v` as the ABI's 32-bit field takes it; ctypes would wrap it silently."""
+    if not -(1 << 31) <= v < 1 << 31:
+        raise ValueError(f"{name} = {v} does not fit 32 bits")
+    return v
+
+
 def make_rows(*, rows, vocab, dtype=ws.DTYPE_F32, row_stride=None, temperature=1.0,
               device=0) -> Rows:
     r = Rows()
-    r.device = device
-    r.dtype = dtype
-    r.rows = rows
-    r.vocab = vocab
+    r.device = _int32("device", device)
+    r.dtype = _int32("dtype", dtype)
+    r.rows = _int32("rows", rows)
+    r.vocab = _int32("vocab", vocab)
     r.row_stride = vocab if row_stride is None else row_stride
     r.temperature = temperature
     return r
@@ -106,14 +114,15 @@ def make_rows(*, rows, vocab, dtype=ws.DTYPE_F32, row_stride=None, temperature=1
 def logprobs_workspace(rows: Rows, top_k: int = 0) -> int:
     """Bytes of workspace ws_logprobs needs for this shape."""
     n = c_size_t(0)
-    _check(load().ws_logprobs_workspace(byref(rows), top_k, byref(n)), "ws_logprobs_workspace")
+    _check(load().ws_logprobs_workspace(byref(rows), _int32("top_k", top_k), byref(n)),
+           "ws_logprobs_workspace")
     return n.value
 
 
 def distill_workspace(rows: Rows, mode: int, gradient: bool) -> int:
     """Bytes of workspace ws_distill needs for this shape and mode."""
     n = c_size_t(0)
-    _check(load().ws_distill_workspace(byref(rows), mode, 1 if gradient else 0, byref(n)),
+    _check(load().ws_distill_workspace(byref(rows), _int32("mode", mode), 1 if gradient else 0, byref(n)),
            "ws_distill_workspace")
     return n.value
 
@@ -179,6 +188,9 @@ class _Call:
         if given is None and need:
             import torch
             given = torch.empty(need, dtype=torch.uint8, device=f"cuda:{rows.device}")
+        elif hasattr(given, "is_cuda") and (not given.is_cuda or not given.is_contiguous()
+                                            or given.device.index != rows.device):
+            raise ValueError(f"workspace must be contiguous and on cuda:{rows.device}")
         args.workspace = ws._addr(given)
         if given is not None:
             args.workspace_bytes = given.numel() * given.element_size() \
@@ -213,7 +225,7 @@ class LogProbs(_Call):
         a.entropy = _buffer("entropy", entropy, rows, _F32, n)
         a.top = _buffer("top", top, rows, _PAIR, 2 * n * top_k)
         a.stats = _buffer("stats", stats, rows, _F32, 2 * n)
-        a.top_k = top_k
+        a.top_k = _int32("top_k", top_k)
         workspace = self._own_workspace(rows, a, workspace, logprobs_workspace(rows, top_k))
         self._bind(rows, a, logits, targets, logprob, entropy, top, stats, workspace)
 
@@ -238,7 +250,7 @@ class LogProbsGrad(_Call):
         a.grad_entropy = _buffer("grad_entropy", grad_entropy, rows, _F32, n)
         a.top = _buffer("top", top, rows, _PAIR, 2 * n * top_k)
         a.grad_top = _buffer("grad_top", grad_top, rows, _F32, n * top_k)
-        a.top_k = top_k
+        a.top_k = _int32("top_k", top_k)
         self._bind(rows, a, logits, stats, grad_logits, targets, grad_logprob, entropy,
                    grad_entropy, top, grad_top)
 
@@ -262,8 +274,8 @@ class Distill(_Call):
         if grad_logits is not None:
             a.grad_stride = _stride(grad_logits, rows, grad_stride)
             a.grad_logits = _matrix("grad_logits", grad_logits, rows, a.grad_stride)
-        a.teacher_k = teacher_k
-        a.mode = mode
+        a.teacher_k = _int32("teacher_k", teacher_k)
+        a.mode = _int32("mode", mode)
         need = distill_workspace(rows, mode, grad_logits is not None)
         workspace = self._own_workspace(rows, a, workspace, need)
         self._bind(rows, a, logits, teacher, loss, stats, tail, grad_loss, grad_logits, workspace)
@@ -286,8 +298,8 @@ class DistillGrad(_Call):
         a.tail = _buffer("tail", tail, rows, _F32, n)
         a.grad_loss = _buffer("grad_loss", grad_loss, rows, _F32, n)
         a.grad_logits = _matrix("grad_logits", grad_logits, rows, a.grad_stride)
-        a.teacher_k = teacher_k
-        a.mode = mode
+        a.teacher_k = _int32("teacher_k", teacher_k)
+        a.mode = _int32("mode", mode)
         self._bind(rows, a, logits, teacher, stats, tail, grad_loss, grad_logits)
 
 

@@ -366,6 +366,48 @@ def test_distill_long_rows(gpu_lib, mode, dtype, rows, V):
     assert abs(loss[0] - want) <= 4 * (_sum_tol(V) + 16 * E) * 20
 
 
+def test_distill_row_of_more_parts_than_lanes(gpu_lib):
+    """A row so long that the marks' limit gives more than 64 parts; logits
+    spread so that every part's sum matters."""
+    V = 20_000_003
+    rng = np.random.default_rng(3)
+    mat = Matrix(rng.normal(size=(1, V)), "f16")
+    ids = np.array([[5, V - 1, V // 2]])
+    scores = np.log(np.array([[0.2, 0.3, 0.1]]))
+    z = mat.z[0]
+    e = np.exp(z - z.max())
+    lse = z.max() + np.log(e.sum())
+    rest = e.sum() - e[ids[0]].sum()
+    tail = z.max() + np.log(rest) - lse
+    s32 = scores.astype(np.float32).astype(np.float64)[0]
+    q = np.exp(s32)
+    want = (q * (s32 - (z[ids[0]] - lse))).sum() + (1 - q.sum()) * (np.log(1 - q.sum()) - tail)
+    loss, grad, stats, got_tail = run_distill(mat, 1.0, ids, scores, ol.TAIL, np.full(1, 1e6),
+                                              separate=True)
+    # A lane adds at most V / (64 parts of 256 lanes) terms before it joins.
+    tol = (V / (64 * 256) + 200) * E
+    assert abs(loss[0] - want) <= 4 * tol and abs(float(got_tail[0]) - tail) <= 4 * tol + 2 * E
+    p = np.exp(z - lse)
+    dz = 1e6 * np.where(np.isin(np.arange(V), ids[0]), p, p * (1 - (1 - q.sum()) / np.exp(tail)))
+    dz[ids[0]] -= 1e6 * q
+    # The listed tokens' 1e6 (p - q) is past FP16's largest: an infinity of its sign.
+    over = np.abs(dz) >= 65520
+    assert (grad[0][over] == np.sign(dz[over]) * np.inf).all() and over.sum() == 3
+    bad = np.abs(grad[0] - dz) > (HALF["f16"] + 8 * tol) * np.abs(dz) + 8 * tol * p * 1e6 + 2.0 ** -25
+    assert not bad[~over].any()
+
+
+def test_no_rows(gpu_lib):
+    import torch
+    z = torch.zeros((0, 50), device=_dev())
+    r = lg.make_rows(rows=0, vocab=50)
+    empty = torch.zeros((0,), device=_dev())
+    lg.LogProbs(r, z, entropy=empty).run()
+    lg.Distill(r, z, torch.zeros((0, 4, 2), dtype=torch.int32, device=_dev()), 4,
+               lg.DISTILL_TAIL, empty).run()
+    torch.cuda.synchronize()
+
+
 def test_logprobs_offsets_past_32_bits(gpu_lib):
     """Rows whose elements start past 2^31 and bytes past 2^32."""
     import torch

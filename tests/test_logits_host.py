@@ -125,3 +125,19 @@ def test_bound_call_refuses_bad_addresses(lib):
     assert call.submit() == ws.WS_E_INVALID_ARG
     with pytest.raises(ws.WsError):
         call.run()
+
+
+def test_sizes_past_the_abi_are_refused_not_wrapped(lib):
+    for bad in (dict(rows=2 ** 32 + 1), dict(vocab=2 ** 33), dict(dtype=2 ** 40)):
+        with pytest.raises(ValueError, match="32"):
+            lg.make_rows(**{**dict(rows=4, vocab=100), **bad})
+    with pytest.raises(ValueError, match="32"):
+        lg.LogProbs(lg.make_rows(rows=4, vocab=100), 4096, top_k=2 ** 32)
+    with pytest.raises(ValueError, match="32"):
+        lg.Distill(lg.make_rows(rows=4, vocab=100), 4096, 4096, 2 ** 32 + 4, 0, 4096)
+
+
+def test_workspace_tensor_is_checked(lib):
+    with pytest.raises(ValueError, match="workspace"):
+        lg.LogProbs(lg.make_rows(rows=1, vocab=131072, dtype=ws.DTYPE_BF16), 4096,
+                    workspace=torch.zeros(1 << 20, dtype=torch.uint8))
