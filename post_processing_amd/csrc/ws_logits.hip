@@ -874,7 +874,7 @@ struct PartOut {
     __device__ __forceinline__ void store(const Part<L>& part, int s,
                                           const float (&v)[L::VEC]) const {
         if (slots) {
-            *reinterpret_cast<uint4*>(base + (uint32_t)s * 16u) = L::pack(v);
+            store_slot<L>(base + (uint32_t)s * 16u, L::pack(v));
             return;
         }
         typename L::Elem* to = row + (part.e0 + s * L::VEC);
@@ -1175,11 +1175,20 @@ int device_ready(int32_t device) {
     return cur == device ? WS_OK : WS_E_INVALID_ARG;
 }
 
-#define WS_BY_DTYPE(dtype, CALL)                        \
-    do {                                                \
-        if ((dtype) == WS_DTYPE_F32) { CALL(F32); }     \
-        else if ((dtype) == WS_DTYPE_F16) { CALL(F16); } \
-        else { CALL(BF16); }                            \
+// CALL(type) for the matrix's element type and way through the caches.
+#define WS_BY_TYPE(r, CALL)                                        \
+    do {                                                           \
+        const bool stream = streams(r);                            \
+        if ((r).dtype == WS_DTYPE_F32) {                           \
+            if (stream) { CALL(Streamed<F32>); }                   \
+            else { CALL(F32); }                                    \
+        } else if ((r).dtype == WS_DTYPE_F16) {                    \
+            if (stream) { CALL(Streamed<F16>); }                   \
+            else { CALL(F16); }                                    \
+        } else {                                                   \
+            if (stream) { CALL(Streamed<BF16>); }                  \
+            else { CALL(BF16); }                                   \
+        }                                                          \
     } while (0)
 
 // Enqueues one kernel; its parameters are one struct, copied by the call.
@@ -1256,7 +1265,7 @@ int enqueue_distill_grad(const ws_rows& r, const ws_distill_grad_args& a, hipStr
     g.c = scale_c(r);
     g.inv_tau = scale_inv(r);
 #define CALL(L) return run_grad<L>(r, g, true, s)
-    WS_BY_DTYPE(r.dtype, CALL);
+    WS_BY_TYPE(r, CALL);
 #undef CALL
 }
 
@@ -1272,6 +1281,7 @@ extern "C" int ws_logprobs_workspace(const ws_rows* rows, int32_t top_k, size_t*
 }
 
 extern "C" int ws_logprobs(const ws_rows* rows, const ws_logprobs_args* args, void* stream) {
+    using namespace ws;
     int v = ws::validate_logprobs(rows, args);
     if (v != WS_OK) return v;
     const ws_rows& r = *rows;
@@ -1300,13 +1310,14 @@ extern "C" int ws_logprobs(const ws_rows* rows, const ws_logprobs_args* args, vo
         p.sums = reinterpret_cast<ws::Sums*>(p.keys + (int64_t)r.rows * plan.parts * p.k);
     }
     const hipStream_t s = static_cast<hipStream_t>(stream);
-#define CALL(L) return ws::run_logprobs<ws::L>(r, plan, p, s)
-    WS_BY_DTYPE(r.dtype, CALL);
+#define CALL(L) return run_logprobs<L>(r, plan, p, s)
+    WS_BY_TYPE(r, CALL);
 #undef CALL
 }
 
 extern "C" int ws_logprobs_grad(const ws_rows* rows, const ws_logprobs_grad_args* args,
                                 void* stream) {
+    using namespace ws;
     int v = ws::validate_logprobs_grad(rows, args);
     if (v != WS_OK) return v;
     if (rows->rows == 0) return WS_OK;
@@ -1330,8 +1341,8 @@ extern "C" int ws_logprobs_grad(const ws_rows* rows, const ws_logprobs_grad_args
     g.c = ws::scale_c(r);
     g.inv_tau = ws::scale_inv(r);
     const hipStream_t s = static_cast<hipStream_t>(stream);
-#define CALL(L) return ws::run_grad<ws::L>(r, g, false, s)
-    WS_BY_DTYPE(r.dtype, CALL);
+#define CALL(L) return run_grad<L>(r, g, false, s)
+    WS_BY_TYPE(r, CALL);
 #undef CALL
 }
 
@@ -1346,6 +1357,7 @@ extern "C" int ws_distill_workspace(const ws_rows* rows, int32_t mode, int32_t g
 }
 
 extern "C" int ws_distill(const ws_rows* rows, const ws_distill_args* args, void* stream) {
+    using namespace ws;
     int v = ws::validate_distill(rows, args);
     if (v != WS_OK) return v;
     const ws_rows& r = *rows;
@@ -1386,9 +1398,9 @@ extern "C" int ws_distill(const ws_rows* rows, const ws_distill_args* args, void
         if (!p.tail) p.tail = reinterpret_cast<float*>(space + plan.tail_at);
     }
 #define CALL(L)                                                                       \
-    v = args->mode == WS_DISTILL_TAIL ? ws::run_distill<ws::L, true>(r, plan, p, s)   \
-                                      : ws::run_distill<ws::L, false>(r, plan, p, s)
-    WS_BY_DTYPE(r.dtype, CALL);
+    v = args->mode == WS_DISTILL_TAIL ? run_distill<L, true>(r, plan, p, s)   \
+                                      : run_distill<L, false>(r, plan, p, s)
+    WS_BY_TYPE(r, CALL);
 #undef CALL
     if (v != WS_OK || !gradient || plan.held > 0) return v;
     ws_distill_grad_args g{};

@@ -152,6 +152,18 @@ inline bool rows_aligned(const ws_rows& r, const void* logits) {
            (r.rows == 1 || (r.row_stride * logit_bytes(r.dtype)) % 16 == 0);
 }
 
+// Whether slots go past the caches: matrices of more than half the 256 MB
+// last-level cache, of which the next reader would find little (MI355X, other
+// inputs from pass to pass: 4,096 x 131,072 BF16 with entropy 174 us through
+// them, 165 past; gradient of 4,096 x 65,536 189 and 176; 2,048 x 50,001 with the
+// best 20, 205 MB, 49 and 45; smaller ones, which the cache holds, lose: 64 x
+// 32,768 FP16 7.6 and 10.1, gradient of 255 x 50,001 12.9 and 15.4).
+constexpr int64_t kStreamBytes = 128ll << 20;
+
+inline bool streams(const ws_rows& r) {
+    return (int64_t)r.rows * r.vocab * logit_bytes(r.dtype) > kStreamBytes;
+}
+
 // A row is split into `parts` of `chunk` 16-byte slots, the last of which takes
 // what is left (fewer than `parts` slots more, and one more still when the
 // row's start is not aligned); a second kernel joins them.

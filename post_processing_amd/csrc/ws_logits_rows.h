@@ -28,8 +28,11 @@ constexpr float kFar = -1.0e6f;
 
 // ---- element types ---------------------------------------------------------
 
+// kStream: slots are read and written past the caches, for matrices too large
+// to find or leave anything there.
 struct F32 {
     using Elem = float;
+    static constexpr bool kStream = false;
     static constexpr int VEC = 4;
     static __device__ __forceinline__ uint4 none() {   // -inf
         return make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u);
@@ -50,6 +53,7 @@ struct F32 {
 
 struct F16 {
     using Elem = _Float16;
+    static constexpr bool kStream = false;
     static constexpr int VEC = 8;
     typedef _Float16 Pair __attribute__((ext_vector_type(2)));
     static __device__ __forceinline__ uint4 none() {   // -inf
@@ -81,6 +85,7 @@ struct F16 {
 
 struct BF16 {
     using Elem = __bf16;
+    static constexpr bool kStream = false;
     static constexpr int VEC = 8;
     typedef __bf16 Pair __attribute__((ext_vector_type(2)));
     static __device__ __forceinline__ uint4 none() {   // -inf
@@ -111,6 +116,33 @@ struct BF16 {
     }
 };
 
+template <typename B>
+struct Streamed : B {
+    static constexpr bool kStream = true;
+};
+
+typedef uint32_t Slot16 __attribute__((ext_vector_type(4)));
+
+template <typename L>
+__device__ __forceinline__ uint4 load_slot(const void* p) {
+    if constexpr (L::kStream) {
+        const Slot16 v = __builtin_nontemporal_load(static_cast<const Slot16*>(p));
+        return make_uint4(v.x, v.y, v.z, v.w);
+    } else {
+        return *static_cast<const uint4*>(p);
+    }
+}
+
+template <typename L>
+__device__ __forceinline__ void store_slot(void* p, uint4 w) {
+    if constexpr (L::kStream) {
+        const Slot16 v = {w.x, w.y, w.z, w.w};
+        __builtin_nontemporal_store(v, static_cast<Slot16*>(p));
+    } else {
+        *static_cast<uint4*>(p) = w;
+    }
+}
+
 // ---- a workgroup's part of a row ---------------------------------------------
 
 // Slots [first, first + n) of a row; slot numbers below are relative to first.
@@ -140,7 +172,7 @@ struct Part {
         full_to = whole < n ? whole : n;
     }
     __device__ __forceinline__ uint4 load(int s) const {
-        return *reinterpret_cast<const uint4*>(base + (uint32_t)s * 16u);
+        return load_slot<L>(base + (uint32_t)s * 16u);
     }
     // The nearest whole slot's content (there is one), whatever s: a load under
     // a condition would be waited for before the next is issued.

@@ -212,6 +212,39 @@ def test_logprobs_temperatures(gpu_lib, tau):
     check_logprobs(mat, tau, rng.integers(0, 777, 6), k=8)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("tau", [1e-3, 1.0, 1e3])
+def test_logprobs_huge_logits(gpu_lib, dtype, tau):
+    """Logits of every magnitude up to the type's largest, of either sign, alone
+    and with equals of the maximum: exponents whose parts would overflow."""
+    rng = np.random.default_rng(23)
+    top = {"f32": 3.0e38, "bf16": 3.0e38, "f16": 6.0e4}[dtype]
+    rows = []
+    for scale in [1e3, 1e5, 1.5e8, 2e8, 4e8, 1e12, 1e30, 1e38]:
+        scale = min(scale, top / 3)
+        z = rng.uniform(0.5, 1.0, 600) * scale
+        rows += [z, -z, np.concatenate([z[:300], -z[300:]]),
+                 np.where(np.arange(600) % 50 == 7, z.max(), rng.normal(size=600)),
+                 np.full(600, -scale), z.max() + rng.normal(size=600)]
+    z = np.stack(rows)
+    check_logprobs(Matrix(z, dtype), tau, rng.integers(0, 600, len(z)), k=8)
+    check_logprobs(Matrix(np.tile(z, (1, 20)), dtype), tau, rng.integers(0, 600, len(z)), k=8)
+
+
+@pytest.mark.parametrize("mode", [0, 1])
+def test_distill_huge_logits(gpu_lib, mode):
+    rng = np.random.default_rng(24)
+    for dtype, scale in [("bf16", 2e8), ("bf16", 1e30), ("f16", 5e4), ("f32", 1e12)]:
+        z = np.stack([rng.normal(size=900) * 10 + scale, rng.uniform(-1, 1, 900) * scale,
+                      np.full(900, -scale), rng.normal(size=900)])
+        mat = Matrix(z, dtype)
+        ids, scores = make_teacher(rng, mat.z, 12, mode)
+        ids[0, 0] = int(np.argmax(mat.z[0]))
+        ids[0, 1:] = np.where(ids[0, 1:] == ids[0, 0], -1, ids[0, 1:])
+        check_distill(mat, 1.0, ids, scores, mode, np.ones(4))
+        check_distill(mat, 1.0, ids, scores, mode, np.ones(4), separate=True)
+
+
 def special_rows(V, dtype):
     """Rows where a mask, a value or a tie makes the arithmetic go wrong."""
     rng = np.random.default_rng(17)
@@ -364,6 +397,54 @@ def test_distill_long_rows(gpu_lib, mode, dtype, rows, V):
     check_distill(small, 1.0, ids, scores, mode, g[:2], separate=True)
     want, _, _ = ol.distill(mat.z[0], 1.0, scores[0].astype(np.float64), ids[0], mode)
     assert abs(loss[0] - want) <= 4 * (_sum_tol(V) + 16 * E) * 20
+
+
+@pytest.mark.parametrize("dtype,rows,V,pad", [("bf16", 1100, 65537, 3), ("f32", 700, 50001, 0),
+                                              ("f16", 20000, 3501, 11), ("bf16", 300, 262144, 0),
+                                              ("bf16", 9000, 8192, 0)])
+def test_matrices_past_the_caches(gpu_lib, dtype, rows, V, pad):
+    """Every operator on matrices of more than 128 MiB: the first rows against
+    the oracle, the others, which repeat them, against those."""
+    rng = np.random.default_rng(rows)
+    few, k = 4, 20
+    z = _logits(rng, few, V)
+    z[2, rng.random(V) < 0.97] = -np.inf
+    mat = Matrix(_repeated(rows, z), dtype, pad)
+    first = Matrix(z, dtype, pad)
+    mat.z = first.z
+    at = np.arange(rows) % few
+    targets = np.array([3, V - 1, int(np.argmax(z[2])), 0])
+    got = run_logprobs(mat, 0.9, targets[at], k=k)
+    head = {key: got[key][:few] for key in got if key != "device"}
+    check_logprobs(first, 0.9, targets, k=k, got=head)
+    vec = 4 if dtype == "f32" else 8
+    same = {}
+    lead = np.array([same.setdefault((r % few, r * mat.stride % vec), r) for r in range(rows)])
+    for key in ("logprob", "entropy", "stats", "top"):
+        np.testing.assert_array_equal(got[key].view(np.int32), got[key][lead].view(np.int32))
+    ids, scores = make_teacher(rng, first.z, k, ol.TAIL)
+    g = np.ones(rows)
+    loss, grad, _, _ = run_distill(mat, 0.9, ids[at], scores[at], ol.TAIL, g)
+    lsep, gsep, _, _ = run_distill(mat, 0.9, ids[at], scores[at], ol.TAIL, g, separate=True)
+    check_distill(first, 0.9, ids, scores, ol.TAIL, g[:few])
+    small, sgrad, _, _ = run_distill(first, 0.9, ids, scores, ol.TAIL, g[:few])
+    for l, d in ((loss, grad), (lsep, gsep)):
+        np.testing.assert_allclose(l[:few], small, rtol=1e-5, atol=40 * _sum_tol(V))
+        for r in range(few):
+            np.testing.assert_allclose(d[r], sgrad[r], rtol=2.1 * HALF[dtype] + 4 * _sum_tol(V),
+                                       atol=8 * _sum_tol(V) + 2 * SMALLEST[dtype])
+        assert (l == l[lead]).all()
+        assert all(np.array_equal(d[r], d[lead[r]]) for r in range(0, rows, 7))
+    del grad, gsep, lsep
+    st = row_stats(first, 0.9)[at]
+    ent = np.array([ol.entropy(ol.log_softmax(r, _tau32(0.9))) for r in first.z])[at]
+    up = rng.normal(size=few)[at]
+    check_logprobs_grad(first, 0.9, targets, up[:few], up[:few])
+    want = run_logprobs_grad(first, 0.9, st[:few], targets, up[:few], ent[:few], up[:few])
+    whole = run_logprobs_grad(mat, 0.9, st, targets[at], up, ent, up, in_place=True)
+    for r in (0, 1, 2, 3, rows // 2, rows - 1):
+        np.testing.assert_allclose(whole[r], want[r % few], rtol=2.1 * HALF[dtype],
+                                   atol=1e-6 + 2 * SMALLEST[dtype])
 
 
 def test_distill_row_of_more_parts_than_lanes(gpu_lib):
