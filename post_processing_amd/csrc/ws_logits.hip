@@ -19,12 +19,12 @@ namespace {
 // Each thread keeps running sums of its own slots against its own running
 // maximum (raised once per batch of slots), joined across lanes, waves and, for
 // a row split over several workgroups, parts.  A row is read once (counted:
-// 1.0747e9 bytes for 4,096 x 131,072 BF16, 1.0737e9 of them logits).  16-bit
-// logits are bound by HBM and the vector unit about alike: 9.3 vector
-// instructions an element with entropy, one of them an exponential at a quarter
-// of the rate.  Measured on MI355X: 176 us for 4,096 x 131,072 BF16 with
-// entropy (6.1 TB/s), 170 us for 4,096 x 65,536 FP32 (6.3 TB/s); a plain copy
-// moves 4.84 TB/s read and written.
+// 1.0745e9 bytes for 4,096 x 131,072 BF16, 1.0737e9 of them logits), and HBM
+// bounds it: 169 us for that with entropy (6.4 TB/s; a plain copy moves 4.84
+// TB/s read and written).  The vector unit is close behind with 9.3
+// instructions an element, one of them an exponential at a quarter of the rate;
+// one instruction fewer (16-bit exponents in one fused multiply-add) changed
+// nothing.
 //
 // Best K: a thread also keeps its best slot (largest slot maximum, the first
 // one) and the second largest slot maximum, four instructions a slot.  The K-th
@@ -36,8 +36,8 @@ namespace {
 // selection running inside the pass.  What follows the pass is a chain of
 // latencies: 0.5 us to the bound, 0.3 to the list of slots, 1.3 for reading them
 // again and 0.8 for ordering and storing (one row of 131,072 BF16 in 16 parts, K
-// = 20, 5.7 us in all, and 4.0 for the join); 2,048 rows of 50,001 take 46 us,
-// 40 without the best 20.
+// = 20, 5.5 us in all, and 3.7 for the join); 2,048 rows of 50,001 take 42 us
+// (4.9 TB/s): one round of workgroups, so the chain at its end stays visible.
 
 constexpr int kBatch = kBatchSlots;   // slots a thread has in flight
 
@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(LogprobsParams p) {
 }
 
 // Joins the parts of a row (at most 64): every key asked for at once, then the
-// bound, the keys that reach it and their order (4.0 us for 16 lists of 20 keys,
+// bound, the keys that reach it and their order (3.7 us for 16 lists of 20 keys,
 // 2.1 us for sums alone; reading the lists in turn took 8.0 us for 64 of them).
 constexpr int kJoin = 256;
 
@@ -665,8 +665,8 @@ __device__ __forceinline__ void settle_rest(Teacher& t, const Named& n, int k, i
 // LDS marks the listed ones), and the few listed ones are added at the end: a
 // tail far below the listed tokens keeps its own maximum and its full
 // precision, which the difference of two sums near 1 would not.  Bound as the
-// forward pass above: 1,024 rows of 131,072 BF16 with 32 entries 52 us (5.2
-// TB/s), 4,096 rows 171 us (6.3 TB/s).
+// forward pass above: 1,024 rows of 131,072 BF16 with 32 entries 50 us (5.4
+// TB/s), in two rounds of workgroups whose starts and ends show.
 
 struct DistillParams {
     const void* logits;
@@ -852,10 +852,10 @@ __global__ void __launch_bounds__(64) distill_join_kernel(DistillParams p) {
 //
 // One pass that reads a slot, forms p from the row's statistics and stores the
 // gradient; the few named tokens are written over afterwards.  Bound by HBM:
-// 4,096 x 65,536 BF16 with entropy 190 us (5.65 TB/s read and written), 2,048 x
-// 65,536 FP16 with 32 teacher entries 101 us (5.3 TB/s); a copy of the same
+// 4,096 x 65,536 BF16 with entropy 175 us (6.1 TB/s read and written), 2,048 x
+// 65,536 FP16 with 32 teacher entries 98 us (5.5 TB/s); a copy of the same
 // bytes at 4.84 TB/s would take 222 and 111 us.  255 rows of 50,001 FP16, which
-// fit the last-level cache, 12 us.
+// fit the last-level cache, 13 us.
 
 // Where a part's gradient goes: slots at the same place as the logits' slots
 // when both rows start alike relative to 16 bytes, else element by element.
@@ -1038,17 +1038,17 @@ __global__ void __launch_bounds__(256) grad_kernel(GradParams p) {
 
 // Loss and gradient of a row in one pass: the row stays in the registers of
 // its workgroup (sixteen slots a thread), so it is read once and the gradient
-// written once (counted for 2,048 x 131,072 BF16: 541 MB and 543 MB, the logits
+// written once (counted for 2,048 x 131,072 BF16: 542 MB and 543 MB, the logits
 // being 537), where a loss kernel and a gradient kernel read it twice.  At most
 // 128 registers a thread, so that a CU holds sixteen waves: one row of up to
 // 131,072 16-bit logits, two of up to 65,536 or four of up to 32,768.
 //
-// Measured (MI355X, 64 entries, 1.07 GB read and written): 8,192 x 32,768 214
-// us, 4,096 x 65,536 204 us (5.3 TB/s), 2,048 x 131,072 228 us (4.7 TB/s) with a
-// tail and 217 us without.  With one row to a CU its phases follow one another:
-// loads and the sums, the join and FP64 finish by one wave (some 2 us a row),
-// then exponentials and stores.  777 rows of 50,001 FP32 take 74.6 us (4.2
-// TB/s): three full rounds over 256 CUs and a fourth of nine rows.  Tried and
+// Measured (MI355X, 64 entries, 1.07 GB read and written): 4,096 x 65,536 198 us
+// (5.4 TB/s), 2,048 x 131,072 217 us (5.0 TB/s).  With one row to a CU its
+// phases follow one another: loads and the sums, the join and FP64 finish by one
+// wave (some 2 us a row), then exponentials and stores.  777 rows of 50,001 FP32
+// take 71.6 us (4.3 TB/s): three full rounds over 256 CUs and a fourth of nine
+// rows.  Tried and
 // slower: walking the rows with the next row's loads issued as registers come
 // free (280 us for 2,048 x 131,072; loads and stores return in order), and
 // reading the row a second time from the last-level cache with two rows to a CU
