@@ -63,12 +63,12 @@ def logprobs_grad(z, tau, target=-1, g_target=0.0, g_entropy=0.0, ids=(), g_ids=
     """d(g_target logprob + g_entropy entropy + sum g_ids top) / dz of a row."""
     logp = log_softmax(z, tau)
     n = len(logp)
-    if np.isneginf(logp).all():
-        return np.zeros(n)
     named = [(target, g_target)] if target != -1 else []
     named += [(i, g) for i, g in zip(ids, g_ids) if i != -1]
     if np.isnan(logp).any() or any(not 0 <= i < n for i, _ in named):
         return np.full(n, np.nan)
+    if np.isneginf(logp).all():
+        return np.zeros(n)
     p = np.exp(logp)
     dx = np.zeros(n)
     for i, g in named:

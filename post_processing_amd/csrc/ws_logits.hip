@@ -516,18 +516,18 @@ __device__ __forceinline__ void merge_named(Named& n, int count, uint32_t* ids, 
     wave_lds_sync();
     n.first[0] = n.id[0] != kAbsent;
     n.first[1] = n.id[1] != kAbsent;
-    bool again = false;
+    bool again[2] = {false, false};
     const int padded = (count + 3) & ~3;   // entries past count are kAbsent
     for (int j = 0; j < padded; j += 4) {
         const uint4 x = *reinterpret_cast<const uint4*>(ids + j);
         const uint32_t q[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            again |= q[i] == n.id[0] && j + i < lane;
-            again |= q[i] == n.id[1] && j + i < lane + 64;
+            again[0] |= q[i] == n.id[0] && j + i < lane;
+            again[1] |= q[i] == n.id[1] && j + i < lane + 64;
         }
     }
-    if (__ballot(again && (n.first[0] || n.first[1])) == 0) return;
+    if (__ballot((again[0] && n.first[0]) || (again[1] && n.first[1])) == 0) return;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         if (n.id[h] == kAbsent) continue;
@@ -722,7 +722,7 @@ __device__ __forceinline__ Slope distill_slope(const Teacher& t, bool bad, float
         }
     }
     s.scale = scale;
-    if (logsum == -(double)INFINITY) s.clear();
+    if (logsum == -(double)INFINITY && !bad) s.clear();
     return s;
 }
 
@@ -980,7 +980,7 @@ __device__ __forceinline__ Slope grad_slope(const GradParams& p, int64_t row,
         if (n.bad) s.a = NAN;
         s.a_listed = s.a;
         s.scale = p.inv_tau;
-        if (st.logsum == -INFINITY) s.clear();
+        if (st.logsum == -INFINITY && !n.bad) s.clear();
         merge_named(n, p.k + 1, ids, adds, lane);
         return s;
     }
@@ -1048,11 +1048,10 @@ __global__ void __launch_bounds__(256) grad_kernel(GradParams p) {
 // phases follow one another: loads and the sums, the join and FP64 finish by one
 // wave (some 2 us a row), then exponentials and stores.  777 rows of 50,001 FP32
 // take 71.6 us (4.3 TB/s): three full rounds over 256 CUs and a fourth of nine
-// rows.  Tried and
-// slower: walking the rows with the next row's loads issued as registers come
-// free (280 us for 2,048 x 131,072; loads and stores return in order), and
-// reading the row a second time from the last-level cache with two rows to a CU
-// (266 us).
+// rows.  Tried when this took 253 us and not kept: walking the rows with the
+// next row's loads issued as registers come free (280 us; loads and stores
+// return in order), and reading the row a second time from the last-level cache
+// with two rows to a CU (266 us).
 constexpr int kHeld = kHeldSlots;
 // With marks, slots asked for before the workgroup waits for them: a CU takes
 // so many loads at once, so a barrier behind all of a row's loads waits for

@@ -195,7 +195,6 @@ struct Part {
         }
     }
     __device__ __forceinline__ bool whole(int s) const { return s >= full_from && s < full_to; }
-    __device__ __forceinline__ float at(int e) const { return L::up(row[e]); }
 };
 
 // ---- running sums --------------------------------------------------------------

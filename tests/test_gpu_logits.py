@@ -647,6 +647,23 @@ def test_logprobs_grad_indices_outside_and_absent(gpu_lib):
                         rng.normal(size=(6, 3)))
 
 
+def test_index_outside_a_row_without_a_distribution(gpu_lib):
+    """An index outside the row makes the whole gradient NaN, in a row of -inf
+    only as in any other."""
+    z = np.full((3, 40), -np.inf)
+    z[2] = 1.0
+    check_logprobs_grad(Matrix(z, "f32"), 1.0, [40, 3, 41], np.ones(3))
+    ids = np.array([[1, 40], [1, 2], [-3, 2]])
+    scores = np.log(np.full((3, 2), 0.25))
+    for mode in (ol.RENORM, ol.TAIL):
+        mat = Matrix(z, "f32")
+        check_distill(mat, 1.0, ids, scores, mode, np.ones(3))
+        _, grad, _, _ = run_distill(mat, 1.0, ids, scores, mode, np.ones(3))
+        _, apart, _, _ = run_distill(mat, 1.0, ids, scores, mode, np.ones(3), separate=True)
+        for got in (grad, apart):
+            assert np.isnan(got[0]).all() and (got[1] == 0).all() and np.isnan(got[2]).all()
+
+
 def test_logprobs_gradient_against_differences(gpu_lib):
     """The gradient against differences of the forward operator itself: FP32
     outputs carry about 1e-6, so a step of 1e-2 leaves 1e-4 of noise and the
