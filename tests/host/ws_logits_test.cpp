@@ -6,6 +6,7 @@
 #include <cstddef>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <limits>
 
 #include "ws_logits_plan.h"
@@ -84,6 +85,63 @@ static ws_distill_grad_args distill_grad() {
     a.teacher_k = 32;
     a.mode = WS_DISTILL_TAIL;
     return a;
+}
+
+// Launch geometry over the whole range of shapes: what the kernels assume of
+// their parts, marks and workspaces.
+static void plans() {
+    using namespace ws;
+    const int64_t vocabs[] = {1,     2,     7,      8,      9,      15,      16,       17,
+                              511,   512,   2047,   2048,   4096,   4104,    32768,    49151,
+                              49152, 49160, 65536,  65537,  98303,  98304,   131071,   131072,
+                              131073, 261632, 262144, 262145, 1000003, 20000003, WS_MAX_SCORES};
+    const int32_t counts[] = {1, 2, 3, 8, 63, 64, 65, 127, 255, 256, 257, 511, 512, 513, 1024,
+                              4096, 100000, WS_MAX_ROWS};
+    for (int32_t dtype : {WS_DTYPE_F32, WS_DTYPE_F16, WS_DTYPE_BF16})
+        for (int64_t vocab : vocabs)
+            for (int32_t count : counts) {
+                ws_rows r = rows();
+                r.dtype = dtype;
+                r.rows = count;
+                r.vocab = (int32_t)vocab;
+                r.row_stride = vocab;
+                const int64_t slots = slots_of(r);
+                const LogprobsPlan lp = plan_logprobs(r, 32 < vocab ? 32 : (int32_t)vocab);
+                CHECK(lp.parts >= 1 && lp.parts <= kMaxRowParts && lp.chunk >= 1);
+                CHECK((int64_t)(lp.parts - 1) * lp.chunk + lp.chunk <= slots);
+                CHECK(slots - (int64_t)(lp.parts - 1) * lp.chunk < lp.chunk + lp.parts);
+                CHECK(lp.parts == 1 || lp.chunk >= WS_MAX_K);
+                CHECK(lp.parts == 1 ? lp.workspace == 0
+                                    : lp.workspace >= (size_t)count * lp.parts * (8u * 32 + 12));
+                const GradPlan g = plan_grad(r);
+                CHECK(g.parts >= 1 && g.chunk >= 1 && (int64_t)g.parts * g.chunk <= slots);
+                CHECK(g.parts == 1 || g.chunk >= kGradLeast);
+                for (int mode : {WS_DISTILL_RENORM, WS_DISTILL_TAIL})
+                    for (bool gradient : {false, true}) {
+                        const DistillPlan any = plan_distill(r, mode, gradient, false);
+                        const DistillPlan even = plan_distill(r, mode, gradient, true);
+                        CHECK(any.workspace >= even.workspace);
+                        for (const DistillPlan& p : {any, even}) {
+                            if (p.held > 0) {
+                                CHECK(gradient && p.parts == 1 && r.vocab >= kHeldLeast);
+                                CHECK(slots <= (int64_t)p.held * p.threads);
+                                CHECK(mode != WS_DISTILL_TAIL || p.mark_bytes == p.held * p.threads);
+                                CHECK(p.workspace == 0);
+                                continue;
+                            }
+                            const int64_t last = slots - (int64_t)(p.parts - 1) * p.chunk + 1;   // unaligned
+                            CHECK(p.parts >= 1 && p.chunk >= 1 && last >= p.chunk);
+                            CHECK(mode == WS_DISTILL_TAIL
+                                      ? p.mark_bytes >= last + (kBatchSlots - 1) * p.threads &&
+                                            p.mark_bytes <= 60 * 1024 && p.mark_bytes % 16 == 0
+                                      : p.mark_bytes == 0);
+                            size_t need = gradient ? (size_t)count * 12 : 0;
+                            if (p.parts > 1) need += (size_t)count * (size_t)p.parts * 12;
+                            CHECK(p.workspace >= need);
+                        }
+                        if (any.held > 0) CHECK(slots + 1 <= (int64_t)any.held * any.threads);
+                    }
+            }
 }
 
 #define REFUSED(make, check, field, value)             \
@@ -254,6 +312,7 @@ static int selftest() {
     CHECK(validate_workspace(at<void>(0x1000), 63, 64) == WS_E_INVALID_ARG);
     CHECK(validate_workspace(at<void>(0x1008), 64, 64) == WS_E_INVALID_ARG);
     CHECK(validate_workspace(at<void>(0x1000), 64, 64) == WS_OK);
+    plans();
     std::printf("%d failures\n", failures);
     return failures ? 1 : 0;
 }
