@@ -36,7 +36,7 @@ namespace {
 // selection running inside the pass.  What follows the pass is a chain of
 // latencies: 0.5 us to the bound, 0.3 to the list of slots, 1.3 for reading them
 // again and 0.8 for ordering and storing (one row of 131,072 BF16 in 16 parts, K
-// = 20, 5.5 us in all, and 3.7 for the join); 2,048 rows of 50,001 take 42 us
+// = 20, 5.5 us in all, and 3.6 for the join); 2,048 rows of 50,001 take 42 us
 // (4.9 TB/s): one round of workgroups, so the chain at its end stays visible.
 
 constexpr int kBatch = kBatchSlots;   // slots a thread has in flight
@@ -344,26 +344,38 @@ struct LogprobsParams {
     float inv_tau;
 };
 
-// Row outputs from its sums; `sorted` holds its best keys.  Called by every
-// thread of a workgroup.
+// The token a row is asked for.  Its index is read before the pass and its logit
+// after it, so that neither is waited for at the end.
+struct Asked {
+    int32_t index;   // -1: none
+    float z;
+
+    __device__ __forceinline__ void read_index(const LogprobsParams& p, int64_t row) {
+        index = p.targets ? p.targets[row] : -1;
+    }
+    template <typename L>
+    __device__ __forceinline__ void read_logit(const LogprobsParams& p, int64_t row) {
+        const typename L::Elem* at =
+            static_cast<const typename L::Elem*>(p.logits) + row * p.stride;
+        z = L::up(at[index >= 0 && index < p.vocab ? index : 0]);
+    }
+};
+
+// Row outputs from its sums; `sorted` holds its best keys.  Called by wave 0.
 template <typename L>
 __device__ __forceinline__ void write_logprobs(const LogprobsParams& p, int64_t row, Sums t,
-                                               const uint64_t* sorted) {
+                                               const Asked& asked, const uint64_t* sorted) {
     const bool empty = t.s == 0.0f;
     const float logsum = empty ? -INFINITY : logf(t.s);
     if (threadIdx.x == 0) {
         if (p.stats) p.stats[row] = {empty ? -INFINITY : t.m, logsum};
         if (p.entropy) p.entropy[row] = empty ? 0.0f : logsum - t.u * p.inv_tau / t.s;
         if (p.logprob) {
-            const int32_t j = p.targets[row];
             float v = 0.0f;
-            if (j >= 0 && j < p.vocab) {
-                const float z =
-                    L::up(static_cast<const typename L::Elem*>(p.logits)[row * p.stride + j]);
-                v = empty ? -INFINITY : (z - t.m) * p.inv_tau - logsum;
-            } else if (j != -1) {
+            if (asked.index >= 0 && asked.index < p.vocab)
+                v = empty ? -INFINITY : (asked.z - t.m) * p.inv_tau - logsum;
+            else if (asked.index != -1)
                 v = NAN;
-            }
             p.logprob[row] = v;
         }
     }
@@ -399,9 +411,12 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(LogprobsParams p) {
     Part<L> part;
     part.init(p.logits, row * p.stride, p.vocab, p.chunk, p.parts, index);
 
+    Asked asked;
+    asked.read_index(p, row);
     Sums a;
     SlotTrack t;
     stream_part<L, NT, ENT, TOPK, false>(part, p.c, nullptr, a, t);
+    if (p.parts == 1) asked.read_logit<L>(p, row);
     int kept = 0;
     if constexpr (TOPK) {
         kept = select_best<L, NT, ENT>(part, t, a, p.c, wave_sums, p.k, best);
@@ -410,7 +425,7 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(LogprobsParams p) {
     }
     if (tid >= 64) return;
     if (p.parts == 1) {
-        write_logprobs<L>(p, row, a, best.sorted);
+        write_logprobs<L>(p, row, a, asked, best.sorted);
     } else {
         if (tid == 0) p.sums[blockIdx.x] = a;
         if constexpr (TOPK) {
@@ -421,7 +436,7 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(LogprobsParams p) {
 }
 
 // Joins the parts of a row (at most 64): every key asked for at once, then the
-// bound, the keys that reach it and their order (3.7 us for 16 lists of 20 keys,
+// bound, the keys that reach it and their order (3.6 us for 16 lists of 20 keys,
 // 2.1 us for sums alone; reading the lists in turn took 8.0 us for 64 of them).
 constexpr int kJoin = 256;
 
@@ -433,9 +448,12 @@ __global__ void __launch_bounds__(kJoin) logprobs_join_kernel(LogprobsParams p) 
     __shared__ int count;
     const int tid = threadIdx.x, lane = tid & 63;
     const int64_t row = blockIdx.x;
+    Asked asked;
+    asked.read_index(p, row);
     Sums a;
     a.init();
     if (lane < p.parts) a = p.sums[row * p.parts + lane];
+    asked.read_logit<L>(p, row);
     if (p.k > 0) {
         const uint64_t* in = p.keys + row * p.parts * p.k;
         const int all = p.parts * p.k;
@@ -466,7 +484,7 @@ __global__ void __launch_bounds__(kJoin) logprobs_join_kernel(LogprobsParams p) 
         __syncthreads();
     }
     if (tid >= 64) return;
-    write_logprobs<L>(p, row, wave_join<ENT>(a, p.c, lane), sorted);
+    write_logprobs<L>(p, row, wave_join<ENT>(a, p.c, lane), asked, sorted);
 }
 
 // ---------------------------------------------------------------------------
