@@ -63,6 +63,13 @@ extern "C" {
 #define WS_DISTILL_RENORM 0   /* the teacher's listed entries, renormalised   */
 #define WS_DISTILL_TAIL   1   /* the listed entries and one event for the rest */
 
+/* 2^-16, above what FP32 scores of a list that holds all of the mass leave of 1
+ * minus their sum: with E = 2^-24 at most 128 E for the additions of a sum over
+ * 128 tokens, 4 E log 128 for its logarithm, 3 E log 128 for the exponents (the
+ * weighted mean of their size), E log 128 for the scores' own rounding and 4 E
+ * for the exponentials: 171 E of 256 E. */
+#define WS_DISTILL_ROUNDING 1.52587890625e-5f
+
 /* A matrix of logits: `rows` rows of `vocab` elements, `row_stride` elements
  * from one row's start to the next.  Rows may start at any element address;
  * the elements between vocab and row_stride are neither read nor written.
@@ -153,7 +160,11 @@ int ws_logprobs_grad(const ws_rows *rows, const ws_logprobs_grad_args *args, voi
  *                             + q_t (log q_t - log p_t)
  * with terms of q = 0 counted as 0 (so a row without entries has loss 0); in
  * WS_DISTILL_TAIL, a list that names every token of the vocabulary has no
- * q_t.  A token listed twice counts with the sum of its q.  The gradient:
+ * q_t.  Where a list holds all of the teacher's mass, FP32 scores leave a q_t of
+ * either sign and about 1e-7; against a p_t of 0 (every unlisted token masked,
+ * by -inf or the type's lowest value) half of such rows would have an infinite
+ * loss.  So where p_t is 0 in FP32 (log p_t below log 2^-150), a q_t of at most
+ * WS_DISTILL_ROUNDING counts as 0.  A token listed twice counts with the sum of its q.  The gradient:
  *   dz_j = g / tau (M p_j - sum_{k: id(k) = j} q_k)   for a listed token
  *   dz_j = g / tau (M - q_t / p_t) p_j                otherwise
  * with g = grad_loss[r] and M = sum_k q_k + q_t.  Where the student gives a

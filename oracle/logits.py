@@ -8,7 +8,8 @@ losses against a teacher's listed entries, and the gradients of all of them.
 Rows without a distribution follow the header's rules: a row of -inf only has
 log probabilities -inf, entropy 0 and gradient 0; a NaN or +inf makes the
 row's results NaN; an index of -1 is no token, and any other index outside the
-row makes what depends on it NaN.
+row makes what depends on it NaN.  A teacher's q_t of at most ROUNDING counts as
+0 where p_t is 0 in FP32.
 """
 from __future__ import annotations
 
@@ -16,6 +17,8 @@ import numpy as np
 
 RENORM = 0
 TAIL = 1
+ROUNDING = 2.0 ** -16
+LOG_NONE = -150 * np.log(2.0)      # log p_t below which p_t is 0 in FP32
 
 
 def log_softmax(z, tau):
@@ -115,6 +118,8 @@ def distill(z, tau, scores, ids, mode, g=1.0):
         tail = -np.inf
         if left.size and not np.isneginf(left).all():
             tail = left.max() + np.log(np.exp(left - left.max()).sum())
+        if rest <= ROUNDING and tail < LOG_NONE:
+            rest = 0.0
         if rest > 0:
             loss += rest * (np.log(rest) - tail)
             if not np.isneginf(tail):

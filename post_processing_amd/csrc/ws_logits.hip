@@ -676,6 +676,16 @@ __device__ __forceinline__ void settle_rest(Teacher& t, const Named& n, int k, i
     t.mass += t.rest;
 }
 
+// With WS_DISTILL_TAIL, once log p_t is known: a q_t that the scores' rounding
+// may have left counts as 0 where the student has no p_t for it.
+constexpr float kNoTail = -103.972077f;   // log 2^-150
+__device__ __forceinline__ void drop_rounding(Teacher& t, double tail) {
+    if (t.rest <= (double)WS_DISTILL_ROUNDING && (float)tail < kNoTail) {
+        t.mass -= t.rest;
+        t.rest = 0.0;
+    }
+}
+
 // ---------------------------------------------------------------------------
 // Distillation: the loss.
 //
@@ -746,7 +756,7 @@ __device__ __forceinline__ Slope distill_slope(const Teacher& t, bool bad, float
 
 // Row outputs from its sums, by wave 0; the slope for a gradient that follows.
 __device__ __forceinline__ Slope finish_distill(const DistillParams& p, int64_t row, Sums sums,
-                                                const Named& n, const Teacher& t, int lane) {
+                                                const Named& n, Teacher t, int lane) {
     float m = sums.m, s = sums.s;
     if (p.mode == WS_DISTILL_TAIL) {
         m = fmaxf(m, wave_max(fmaxf(n.z[0], n.z[1]), lane));
@@ -763,6 +773,7 @@ __device__ __forceinline__ Slope finish_distill(const DistillParams& p, int64_t 
     double tail = -(double)INFINITY;
     if (p.mode == WS_DISTILL_TAIL && sums.s != 0.0f)
         tail = ((double)sums.m - (double)m) * p.inv_tau + lane_d(logs, 1) - logsum;
+    if (p.mode == WS_DISTILL_TAIL) drop_rounding(t, tail);
     double loss = 0.0;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -969,6 +980,7 @@ __device__ __forceinline__ Slope grad_slope(const GradParams& p, int64_t row,
         if (p.mode == WS_DISTILL_TAIL) {
             settle_rest(t, n, p.k, p.vocab);
             tail = (double)p.tail[row];
+            drop_rounding(t, tail);
         }
         return distill_slope(t, n.bad, st.max, (double)st.logsum, tail,
                              p.grad_loss[row] * p.inv_tau);

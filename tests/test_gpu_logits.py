@@ -921,6 +921,46 @@ def test_distill_tail_far_below_the_listed_tokens(gpu_lib):
     check_distill(Matrix(z, "f32"), 1.0, ids, scores, ol.TAIL, np.ones(3), separate=True)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("rows,V", [(40, 1000), (70, 40001), (30, 70001)])
+def test_distill_rows_masked_to_fewer_tokens_than_are_listed(gpu_lib, dtype, rows, V):
+    """As a grammar leaves them: 12 allowed tokens, teacher entries from
+    ws_logprobs with K = 20, so the list holds all of the mass and 1 - sum q is
+    rounding.  The loss is the divergence over the allowed tokens and the
+    gradient of every other token 0, whichever value masks them."""
+    rng = np.random.default_rng(V)
+    low = {"f32": -3.4028234663852886e38, "f16": -65504.0, "bf16": -3.3895313892515355e38}[dtype]
+    for mask in (-np.inf, low):
+        zt, zs = np.full((rows, V), mask), np.full((rows, V), mask)
+        allowed = np.stack([rng.choice(V, 12, replace=False) for _ in range(rows)])
+        np.put_along_axis(zt, allowed, rng.normal(size=(rows, 12)) * 3, 1)
+        np.put_along_axis(zs, allowed, rng.normal(size=(rows, 12)) * 3, 1)
+        top = run_logprobs(Matrix(zt, dtype), 1.0, None, k=20)
+        ids, scores = top["top_id"], top["top_score"]
+        student = Matrix(zs, dtype)
+        g = np.ones(rows)
+        for separate in (False, True):
+            loss, grad, st, _ = run_distill(student, 1.0, ids, scores, ol.TAIL, g,
+                                            separate=separate)
+            assert np.isfinite(loss).all()
+            for r in range(rows):
+                at = ids[r][:12]
+                assert set(at) == set(allowed[r])
+                q = np.exp(scores[r][:12].astype(np.float64))
+                z = student.z[r][at]
+                lp = ol.log_softmax(z, 1.0)
+                m, logsum = ol.stats(z, 1.0)
+                want = (q * (np.log(q) - lp)).sum()
+                tol = (q * (2 * E * (m - z))).sum() + q.sum() * (_sum_tol(V) + 8 * E * (1 + logsum))
+                assert abs(loss[r] - want) <= tol + 2 * E * abs(want)
+                p, mass = np.exp(lp), q.sum()
+                dz = mass * p - q
+                tol = (grad_tol(z, 1.0, m, logsum, dtype, mass, p, V) + 4 * E * (q + mass * p))
+                tol = tol + HALF[dtype] * (np.abs(dz) + tol) + SMALLEST[dtype]
+                assert_close(grad[r][at], dz, tol, f"gradient of row {r}")
+                assert not np.delete(grad[r], at).any()
+
+
 def test_distill_gradient_against_differences(gpu_lib):
     """As for the log probabilities: noise 1e-4, truncation below 1e-4."""
     rng = np.random.default_rng(14)

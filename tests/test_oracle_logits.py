@@ -127,3 +127,25 @@ def test_distill_edges():
     # The student rules out what the teacher wants.
     loss, grad, _ = ol.distill(np.array([-np.inf, 0.0]), 1.0, [-0.5, -1.0], [0, 1], ol.RENORM)
     assert loss == np.inf and np.isfinite(grad).all() and grad[0] < 0
+
+
+def test_distill_rounding_of_a_list_that_holds_all_of_the_mass():
+    """Rows constrained to fewer tokens than are listed: FP32 scores leave 1 -
+    sum q of either sign, which no loss may turn into an infinity."""
+    rng = np.random.default_rng(4)
+    for mask in (-np.inf, -3.4028234663852886e38, -65504.0):
+        for _ in range(50):
+            allowed = rng.choice(300, 12, replace=False)
+            t, z = np.full(300, mask), np.full(300, mask)
+            t[allowed] = rng.normal(size=12) * 3
+            z[allowed] = rng.normal(size=12) * 3
+            ids = ol.best(t, 20)
+            scores = ol.log_softmax(t, 1.0)[ids].astype(np.float32).astype(np.float64)
+            loss, grad, _ = ol.distill(z, 1.0, scores, ids, ol.TAIL)
+            lt, lz = ol.log_softmax(t[allowed], 1.0), ol.log_softmax(z[allowed], 1.0)
+            # Each score is off by at most 2^-24 of itself.
+            assert abs(loss - (np.exp(lt) * (lt - lz)).sum()) < 1e-5
+            np.testing.assert_allclose(grad[allowed], np.exp(lz) - np.exp(lt), atol=1e-6)
+            assert np.abs(np.delete(grad, allowed)).max() == 0
+    # What rounding cannot explain stays: the student rules out a real tail.
+    assert ol.distill(np.array([0.0, -np.inf]), 1.0, [-1e-3], [0], ol.TAIL)[0] == np.inf
