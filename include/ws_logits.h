@@ -158,7 +158,8 @@ int ws_logprobs_grad(const ws_rows *rows, const ws_logprobs_grad_args *args, voi
  *                      p_t = the sum of p over the tokens not listed,
  *                      loss = sum_k q_k (log q_k - log p_id(k))
  *                             + q_t (log q_t - log p_t)
- * with terms of q = 0 counted as 0 (so a row without entries has loss 0); in
+ * with terms of q = 0 counted as 0 (so a row without entries has loss 0, unless
+ * it holds a NaN or +inf: its loss and gradient are NaN whatever is listed); in
  * WS_DISTILL_TAIL, a list that names every token of the vocabulary has no
  * q_t.  Where a list holds all of the teacher's mass, FP32 scores leave a q_t of
  * either sign and about 1e-7; against a p_t of 0 (every unlisted token masked,

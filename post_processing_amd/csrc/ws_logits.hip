@@ -785,7 +785,8 @@ __device__ __forceinline__ Slope finish_distill(const DistillParams& p, int64_t 
     loss = wave_sum_d(loss, lane);
     if (t.rest > 0.0) loss += t.rest * (lane_d(logs, 2) - tail);
     if (lane == 0) {
-        p.loss[row] = n.bad ? NAN : (float)loss;
+        // A NaN or +inf in the row reaches its sum, but not a loss without terms.
+        p.loss[row] = n.bad || s != s ? NAN : (float)loss;
         if (p.stats) p.stats[row] = {empty ? -INFINITY : m, (float)logsum};
         if (p.tail) p.tail[row] = (float)tail;
     }

@@ -961,6 +961,31 @@ def test_distill_rows_masked_to_fewer_tokens_than_are_listed(gpu_lib, dtype, row
                 assert not np.delete(grad[r], at).any()
 
 
+@pytest.mark.parametrize("mode", [ol.RENORM, ol.TAIL])
+@pytest.mark.parametrize("dtype,V,repeat", [("f32", 300, 1), ("f16", 2500, 9), ("bf16", 70001, 1),
+                                            ("bf16", 70001, 6), ("f32", 9, 1)])
+def test_distill_special_rows_without_entries(gpu_lib, mode, dtype, V, repeat):
+    """A row that holds a NaN or +inf has a NaN loss and gradient whatever is
+    listed: nothing, or tokens of probability 0 only; in a held row, a whole
+    one and one in parts."""
+    z = np.tile(special_rows(V, dtype), (repeat, 1))
+    rows = len(z)
+    held_bad = np.isnan(z).any(1) | np.isposinf(z).any(1)
+    assert held_bad.sum() == 3 * repeat
+    absent = np.full((rows, 9), -1)
+    zero = np.tile(np.arange(9), (rows, 1))
+    for ids, scores in ((absent, np.zeros((rows, 9))), (zero, np.full((rows, 9), -np.inf))):
+        for kw in ({}, {"separate": True}):
+            mat = Matrix(z, dtype)
+            loss, grad, _, _ = run_distill(mat, 1.0, ids, scores, mode, np.ones(rows), **kw)
+            assert (np.isnan(loss) == held_bad).all()
+            assert (np.isnan(grad).any(1) == held_bad).all()
+            assert np.isnan(grad[held_bad]).all()
+            if mode == ol.RENORM:
+                assert (loss[~held_bad] == 0).all() and (grad[~held_bad] == 0).all()
+        check_distill(Matrix(z[:16], dtype), 1.0, ids[:16], scores[:16], mode, np.ones(16))
+
+
 def test_distill_gradient_against_differences(gpu_lib):
     """As for the log probabilities: noise 1e-4, truncation below 1e-4."""
     rng = np.random.default_rng(14)
