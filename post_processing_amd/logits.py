@@ -18,7 +18,12 @@ run, and for as long as a graph that captured it may be replayed.
 
 When an operator needs a workspace and none is given, the call object holds
 one of its own, taken from torch; so two runs of one call object must not
-overlap in time, while two call objects may.
+overlap in time, while two call objects may.  torch hands out memory whose last
+user may still be queued on its current stream, so building such a call object
+waits for that stream: the runs may then go to any stream.  Built while torch
+captures that stream there is nothing to wait for, and the call object belongs
+to that graph: run it on the capturing stream, or one that waits for it, and
+nowhere else.  Buffers and workspaces that are given are the caller's to order.
 """
 from __future__ import annotations
 
@@ -188,6 +193,8 @@ class _Call:
         if given is None and need:
             import torch
             given = torch.empty(need, dtype=torch.uint8, device=f"cuda:{rows.device}")
+            if not torch.cuda.is_current_stream_capturing():
+                torch.cuda.current_stream(rows.device).synchronize()
         elif hasattr(given, "is_cuda") and (not given.is_cuda or not given.is_contiguous()
                                             or given.device.index != rows.device):
             raise ValueError(f"workspace must be contiguous and on cuda:{rows.device}")

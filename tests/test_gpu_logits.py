@@ -1176,6 +1176,49 @@ def test_two_captured_graphs_with_a_workspace_each(gpu_lib):
             np.testing.assert_array_equal(a, b)
 
 
+def test_own_workspace_is_free_when_the_call_is_built(gpu_lib):
+    """A call object built on one torch stream, over memory that stream still
+    has writes queued for, and run on another: those writes come first."""
+    import torch
+    rng = np.random.default_rng(62)
+    mat = Matrix(_logits(rng, 2, 60000), "bf16")
+    r = mat.rows()
+    want = run_logprobs(mat, 1.0, None, k=12)
+    top = torch.zeros((2, 12, 2), dtype=torch.int32, device=_dev())
+    big = torch.zeros(1 << 28, dtype=torch.float32, device=_dev())
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        before = torch.zeros(lg.logprobs_workspace(r, 12), dtype=torch.uint8, device=_dev())
+        for _ in range(20):
+            big.add_(1.0)
+        before.fill_(0xff)
+        del before
+        call = lg.LogProbs(r, mat.view, top_k=12, top=top)
+    call.run()
+    torch.cuda.synchronize()
+    np.testing.assert_array_equal(top.cpu().numpy(), want["top"])
+
+
+def test_call_built_and_captured_in_one_graph(gpu_lib):
+    """A call object with a workspace of its own, built while torch captures."""
+    import torch
+    mat = Matrix(_logits(np.random.default_rng(63), 2, 60000), "bf16")
+    want = run_logprobs(mat, 1.0, None, k=12)
+    top = torch.zeros((2, 12, 2), dtype=torch.int32, device=_dev())
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call = lg.LogProbs(mat.rows(), mat.view, top_k=12, top=top)
+        call.run(torch.cuda.current_stream().cuda_stream)
+    for _ in range(3):
+        top.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        np.testing.assert_array_equal(top.cpu().numpy(), want["top"])
+
+
 def test_workspace_contents_do_not_matter(gpu_lib):
     """A workspace filled with NaN patterns, larger than needed, and a call
     without one where one is needed."""

@@ -141,3 +141,28 @@ def test_workspace_tensor_is_checked(lib):
     with pytest.raises(ValueError, match="workspace"):
         lg.LogProbs(lg.make_rows(rows=1, vocab=131072, dtype=ws.DTYPE_BF16), 4096,
                     workspace=torch.zeros(1 << 20, dtype=torch.uint8))
+
+
+@pytest.mark.parametrize("capturing", [False, True])
+def test_own_workspace_is_free_before_any_stream_may_use_it(lib, monkeypatch, capturing):
+    """torch's memory is free in the order of its current stream only, and a run
+    may go to any stream: building waits for that stream (unless it is being
+    captured, where waiting is an error)."""
+    done = []
+
+    class Stream:
+        def synchronize(self):
+            done.append("wait")
+
+    def empty(*size, **kw):
+        done.append("memory")
+        return torch.zeros(*size, dtype=kw["dtype"])
+
+    monkeypatch.setattr(torch, "empty", empty)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream())
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing)
+    lg.LogProbs(lg.make_rows(rows=1, vocab=131072, dtype=ws.DTYPE_BF16), 4096)
+    assert done == (["memory"] if capturing else ["memory", "wait"])
+    done.clear()
+    lg.LogProbs(lg.make_rows(rows=1, vocab=100), 4096)          # needs none
+    assert done == []
