@@ -97,11 +97,19 @@ def load():
     return lib
 
 
-def _int32(name, v) -> int:
-    """`v` as the ABI's 32-bit field takes it; ctypes would wrap it silently."""
-    if not -(1 << 31) <= v < 1 << 31:
-        raise ValueError(f"{name} = {v} does not fit 32 bits")
+def _field(name, v, bits) -> int:
+    """`v` as the ABI's field of `bits` takes it; ctypes would wrap it silently."""
+    if not -(1 << bits - 1) <= v < 1 << bits - 1:
+        raise ValueError(f"{name} = {v} does not fit {bits} bits")
     return v
+
+
+def _int32(name, v) -> int:
+    return _field(name, v, 32)
+
+
+def _int64(name, v) -> int:
+    return _field(name, v, 64)
 
 
 def make_rows(*, rows, vocab, dtype=ws.DTYPE_F32, row_stride=None, temperature=1.0,
@@ -111,7 +119,7 @@ def make_rows(*, rows, vocab, dtype=ws.DTYPE_F32, row_stride=None, temperature=1
     r.dtype = _int32("dtype", dtype)
     r.rows = _int32("rows", rows)
     r.vocab = _int32("vocab", vocab)
-    r.row_stride = vocab if row_stride is None else row_stride
+    r.row_stride = _int64("row_stride", vocab if row_stride is None else row_stride)
     r.temperature = temperature
     return r
 
@@ -313,7 +321,7 @@ class DistillGrad(_Call):
 def _stride(grad_logits, rows: Rows, given) -> int:
     """The gradient's row stride: as given, a tensor's own, or packed rows."""
     if given is not None:
-        return given
+        return _int64("grad_stride", given)
     if rows.rows > 1 and hasattr(grad_logits, "stride"):
         return grad_logits.stride(0)
     return rows.vocab

@@ -166,3 +166,19 @@ def test_own_workspace_is_free_before_any_stream_may_use_it(lib, monkeypatch, ca
     done.clear()
     lg.LogProbs(lg.make_rows(rows=1, vocab=100), 4096)          # needs none
     assert done == []
+
+
+def test_strides_past_the_abi_are_refused_not_wrapped(lib):
+    """2^64 + 100 is no stride of 100."""
+    for bad in (2 ** 64 + 100, 2 ** 63, -2 ** 64 + 100):
+        with pytest.raises(ValueError, match="64 bits"):
+            lg.make_rows(rows=4, vocab=100, row_stride=bad)
+        r = lg.make_rows(rows=4, vocab=100)
+        with pytest.raises(ValueError, match="64 bits"):
+            lg.LogProbsGrad(r, 4096, 4096, 1 << 20, grad_stride=bad)
+        with pytest.raises(ValueError, match="64 bits"):
+            lg.Distill(r, 4096, 4096, 4, lg.DISTILL_TAIL, 4096, grad_loss=4096,
+                       grad_logits=1 << 20, grad_stride=bad)
+        with pytest.raises(ValueError, match="64 bits"):
+            lg.DistillGrad(r, 4096, 4096, 4, lg.DISTILL_RENORM, 4096, 4096, 1 << 20,
+                           grad_stride=bad)
