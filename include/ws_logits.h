@@ -127,7 +127,8 @@ int ws_logprobs(const ws_rows *rows, const ws_logprobs_args *args, void *stream)
  * read; -1 adds nothing) with grad_top and top_k, entropy (the forward's
  * output) with grad_entropy; each may be left out.  grad_logits may be the
  * logits themselves (same address and stride): each element is read before it
- * is written.  Otherwise the two must not overlap. */
+ * is written.  Otherwise no element may belong to both: apart, or with equal
+ * strides in one buffer, each row of one in the other's padding. */
 typedef struct ws_logprobs_grad_args {
     const void          *logits;
     const ws_row_stats  *stats;         /* [rows]                             */

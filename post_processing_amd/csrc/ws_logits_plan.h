@@ -37,7 +37,9 @@ inline int64_t rows_extent(const ws_rows& r, int64_t stride) {
     return ((int64_t)(r.rows - 1) * stride + r.vocab) * logit_bytes(r.dtype);
 }
 
-// The gradient's matrix: the logits themselves, or apart from them.
+// The gradient's matrix: the logits themselves, or apart from them, or between
+// their rows (equal strides: two rows then lie a fixed distance modulo the
+// stride apart, wherever the two extents meet).
 inline int validate_gradient(const ws_rows& r, const void* logits, const void* grad,
                              int64_t stride) {
     if (stride < r.vocab || stride > WS_MAX_ROW_STRIDE) return WS_E_INVALID_ARG;
@@ -48,8 +50,13 @@ inline int validate_gradient(const ws_rows& r, const void* logits, const void* g
     const uintptr_t a = (uintptr_t)logits, b = (uintptr_t)grad;
     const uintptr_t an = (uintptr_t)rows_extent(r, r.row_stride);
     const uintptr_t bn = (uintptr_t)rows_extent(r, stride);
-    if (a < b ? b - a < an : a - b < bn) return WS_E_INVALID_ARG;
-    return WS_OK;
+    const uintptr_t apart = a < b ? b - a : a - b;
+    if (apart >= (a < b ? an : bn)) return WS_OK;
+    if (stride != r.row_stride) return WS_E_INVALID_ARG;
+    const uintptr_t step = (uintptr_t)(stride * logit_bytes(r.dtype));
+    const uintptr_t row = (uintptr_t)(r.vocab * logit_bytes(r.dtype));
+    const uintptr_t into = apart % step;
+    return into >= row && step - into >= row ? WS_OK : WS_E_INVALID_ARG;
 }
 
 inline bool logits_ok(const ws_rows& r, const void* logits) {

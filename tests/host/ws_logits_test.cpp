@@ -263,6 +263,35 @@ static int selftest() {
         REFUSED(logprobs_grad, validate_logprobs_grad, reserved, 1);
     }
     {
+        // Rows of logits and of gradients in turn in one buffer: every distance
+        // against a count of the elements both hold.
+        for (int64_t vocab : {1, 3, 5})
+            for (int64_t stride : {5, 8, 10, 11})
+                for (int32_t count : {1, 2, 4})
+                    for (int64_t gstride : {stride, stride + 1})
+                        for (int64_t d = -60; d <= 60; ++d) {
+                            ws_rows r = rows();
+                            r.rows = count;
+                            r.vocab = (int32_t)vocab;
+                            r.row_stride = stride;
+                            ws_logprobs_grad_args a = logprobs_grad();
+                            a.grad_logits = at<void>((uintptr_t)(0x10000 + 2 * d));
+                            a.grad_stride = gstride;
+                            bool both = false;
+                            for (int32_t i = 0; i < count; ++i)
+                                for (int32_t j = 0; j < count; ++j) {
+                                    const int64_t apart = d + j * gstride - i * stride;
+                                    both |= apart < vocab && apart > -vocab;
+                                }
+                            const int64_t extent = (count - 1) * stride + vocab;
+                            const int64_t gextent = (count - 1) * gstride + vocab;
+                            const bool meet = d < extent && -d < gextent;
+                            const bool ok = d == 0 ? gstride == stride || count == 1
+                                            : gstride == stride || count == 1 ? !both : !meet;
+                            CHECK((validate_logprobs_grad(&r, &a) == WS_OK) == ok);
+                        }
+    }
+    {
         ws_rows r = rows();
         ws_distill_args a = distill();
         CHECK(validate_distill(&r, &a) == WS_OK);

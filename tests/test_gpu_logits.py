@@ -1176,6 +1176,39 @@ def test_two_captured_graphs_with_a_workspace_each(gpu_lib):
             np.testing.assert_array_equal(a, b)
 
 
+@pytest.mark.parametrize("dtype,rows,V,gap", [("f32", 5, 1003, 3), ("bf16", 5, 1003, 0),
+                                              ("f16", 90, 2000, 5), ("bf16", 3, 70001, 1)])
+def test_gradient_rows_between_the_logits_rows(gpu_lib, dtype, rows, V, gap):
+    """One buffer that holds a row of logits and a row of gradients in turn:
+    the bits of a gradient apart from them, and the logits left as they were."""
+    import torch
+    rng = np.random.default_rng(V + gap)
+    z = _logits(rng, rows, V)
+    pad = V + 2 * gap
+    apart, both = Matrix(z, dtype, pad), Matrix(z, dtype, pad)
+    start = V + gap
+    grad = torch.as_strided(both.flat, (rows, V), (both.stride, 1), start)
+    ids, scores = make_teacher(rng, apart.z, 9, ol.TAIL)
+    top = teacher_entries(ids, scores)
+    st, g = _dev32(row_stats(apart, 1.0)), _dev32(rng.normal(size=rows))
+    targets = torch.from_numpy(ids[:, 2].astype(np.int32)).to(_dev())
+    loss = torch.zeros(rows, device=_dev())
+    out = Matrix(np.zeros((rows, V)), dtype, pad, start)
+    for make in (lambda m, d: lg.LogProbsGrad(m.rows(), m.view, st, d, targets=targets,
+                                              grad_logprob=g),
+                 lambda m, d: lg.Distill(m.rows(), m.view, top, 9, lg.DISTILL_TAIL, loss,
+                                         grad_loss=g, grad_logits=d)):
+        make(apart, out.view).run()
+        make(both, grad).run()
+        torch.cuda.synchronize()
+        assert torch.equal(grad, out.view) and torch.equal(both.view, apart.view)
+        assert apart.outside_untouched() and out.outside_untouched()
+        if gap:
+            edges = torch.as_strided(both.flat, (rows - 1, gap), (both.stride, 1), both.stride - gap)
+            assert (edges == both.marker).all()
+            assert (torch.as_strided(both.flat, (rows, gap), (both.stride, 1), V) == both.marker).all()
+
+
 def test_own_workspace_is_free_when_the_call_is_built(gpu_lib):
     """A call object built on one torch stream, over memory that stream still
     has writes queued for, and run on another: those writes come first."""
