@@ -15,6 +15,7 @@
 #include <cfloat>
 #include <cstdint>
 
+#include "ws_fp64.h"
 #include "ws_lanes.h"
 #include "ws_logits.h"
 
@@ -268,25 +269,6 @@ __device__ __forceinline__ double wave_sum_d(double v, int lane) {
     v += xor_lane_d<4>(v, lane);
     v += xor_lane_d<2>(v, lane);
     return v + xor_lane_d<1>(v, lane);
-}
-
-// e^x in FP64 for x <= 88, to about 1e-15 (1 + x^2) relative; 0 below -200.
-// (sum of (x / 1024)^n / n! up to n = 7) squared ten times: a few constants,
-// where a library routine's would crowd the registers of a held row.
-__device__ __forceinline__ double small_exp(double x) {
-    if (x < -200.0) return 0.0;
-    const double y = x * 0.0009765625;
-    double e = 1.0 / 5040.0;
-    e = fma(e, y, 1.0 / 720.0);
-    e = fma(e, y, 1.0 / 120.0);
-    e = fma(e, y, 1.0 / 24.0);
-    e = fma(e, y, 1.0 / 6.0);
-    e = fma(e, y, 0.5);
-    e = fma(e, y, 1.0);
-    e = fma(e, y, 1.0);
-#pragma unroll
-    for (int i = 0; i < 10; ++i) e *= e;
-    return e;
 }
 
 // log x in FP64 for x between 1e-30 and 1e30: the FP32 logarithm L, and what

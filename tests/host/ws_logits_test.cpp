@@ -3,12 +3,14 @@
 // tests/test_logits_host.py.
 //   ws_logits_test selftest  -> argument checks
 //   ws_logits_test layout    -> "struct field offset" for the ABI structs
+#include <cmath>
 #include <cstddef>
 #include <cstdio>
 #include <cstring>
 #include <initializer_list>
 #include <limits>
 
+#include "ws_fp64.h"
 #include "ws_logits_plan.h"
 
 static int failures = 0;
@@ -142,6 +144,28 @@ static void plans() {
                         if (any.held > 0) CHECK(slots + 1 <= (int64_t)any.held * any.threads);
                     }
             }
+}
+
+// The kernels' own exponential against the 80-bit one: its series leaves 5e-18,
+// its argument 6e-17, and its last two steps round to 1.6e-16; near 0, and with
+// it 1 minus a teacher's probabilities, half a step of the result.
+static void exponential() {
+    double worst = 0.0;
+    for (int i = 0; i <= 288000; ++i) {
+        const double x = -200.0 + i * 1e-3;
+        const long double want = expl((long double)x);
+        const double off = (double)fabsl(((long double)ws::small_exp(x) - want) / want);
+        if (off > worst) worst = off;
+    }
+    CHECK(worst < 3e-16);
+    for (double x : {-1e-16, -1e-12, -1e-10, -1e-8, -1e-4, 1e-12, 1e-8})
+        CHECK(fabsl((1.0L - ws::small_exp(x)) + expm1l((long double)x)) <= 1.2e-16L);
+    CHECK(ws::small_exp(0.0) == 1.0);
+    CHECK(ws::small_exp(-200.5) == 0.0);
+    CHECK(ws::small_exp(-std::numeric_limits<double>::infinity()) == 0.0);
+    CHECK(ws::small_exp(std::numeric_limits<double>::infinity()) ==
+          std::numeric_limits<double>::infinity());
+    CHECK(std::isnan(ws::small_exp(std::numeric_limits<double>::quiet_NaN())));
 }
 
 #define REFUSED(make, check, field, value)             \
@@ -342,6 +366,7 @@ static int selftest() {
     CHECK(validate_workspace(at<void>(0x1008), 64, 64) == WS_E_INVALID_ARG);
     CHECK(validate_workspace(at<void>(0x1000), 64, 64) == WS_OK);
     plans();
+    exponential();
     std::printf("%d failures\n", failures);
     return failures ? 1 : 0;
 }

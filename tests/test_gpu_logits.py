@@ -986,6 +986,18 @@ def test_distill_special_rows_without_entries(gpu_lib, mode, dtype, V, repeat):
         check_distill(Matrix(z[:16], dtype), 1.0, ids[:16], scores[:16], mode, np.ones(16))
 
 
+def test_distill_teacher_nearly_certain_of_one_token(gpu_lib):
+    """A q_t far below FP32's half step at 1, against a p_t of its size or
+    below: what 1 - sum q keeps in FP64 shows in the gradient."""
+    V = 40
+    z = np.zeros((3, V))
+    z[:, 4] = [24.0, 30.0, 27.0]
+    ids = np.full((3, 1), 4)
+    scores = np.array([[-1e-9], [-1e-10], [-1e-10]])
+    for kw in ({}, {"separate": True}):
+        check_distill(Matrix(z, "f32"), 1.0, ids, scores, ol.TAIL, np.ones(3), **kw)
+
+
 def test_distill_gradient_against_differences(gpu_lib):
     """As for the log probabilities: noise 1e-4, truncation below 1e-4."""
     rng = np.random.default_rng(14)
