@@ -253,12 +253,17 @@ inline GradPlan plan_grad(const ws_rows& r) {
 // ws_distill: the loss as ws_logprobs splits its rows, with a limit to a part
 // from the marks of the listed tokens in LDS (a byte a slot).  With a gradient,
 // rows that fit the registers of one workgroup (`held` slots a thread) are done
-// in one kernel; longer ones, and long ones too few to fill the CUs, by the loss
-// and then the gradient (MI355X, 131,072 BF16 logits: 32 rows 21.3 us held, 17.7
-// in three kernels and the gaps between them, 64 rows 23.0 and 20.4, 128 rows
-// 25.0 and 26.4; 32,768 logits: 32 rows 12.6 and 15.5 us, 256 rows 15.0 and 21).
+// in one kernel; longer ones, and few 16-bit rows that take sixteen waves, by
+// the loss and then the gradient.  A 16-bit slot is twice the elements to work
+// through on the CU that holds it, so splitting its row pays until there are
+// rows for a third of the CUs (MI355X, 32 entries with a tail, whole calls in us,
+// held and in three kernels; 131,072 BF16 logits: 4 rows 20.5 and 13.7, 64 rows
+// 23.4 and 21.3, 80 rows 23.7 and 23.8, 128 rows 25.5 and 28.5; 98,301: 64 rows
+// 20.8 and 20.0, 80 rows 21.1 and 21.7; 51,197, eight waves: 4 rows 13.4 and
+// 15.2, 64 rows 14.4 and 18.7; 65,536 FP32: 4 rows 12.3 and 13.0, 64 rows 15.1
+// and 20.2).
 constexpr int kHeldSlots = 16;
-constexpr int kHeldRows = 64;
+constexpr int kHeldRows = 80;
 constexpr int kMaxMarkedSlots = 32768;
 
 struct DistillPlan {
@@ -280,7 +285,7 @@ inline DistillPlan plan_distill(const ws_rows& r, int32_t mode, bool gradient, b
     const int64_t slots = slots_of(r);
     const int64_t most = slots + (aligned ? 0 : 1);
     if (gradient && most <= kHeldSlots * 1024 && r.vocab >= kHeldLeast &&
-        (slots <= kSplitSlots || r.rows >= kHeldRows)) {
+        (most <= kHeldSlots * 512 || r.dtype == WS_DTYPE_F32 || r.rows >= kHeldRows)) {
         p.held = kHeldSlots;
         p.threads = most <= kHeldSlots * 256 ? 256 : most <= kHeldSlots * 512 ? 512 : 1024;
         p.chunk = (int32_t)slots;

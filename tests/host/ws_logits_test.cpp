@@ -146,6 +146,28 @@ static void plans() {
             }
 }
 
+// Which rows a workgroup holds for loss and gradient: the sides that measured
+// faster (see kHeldRows).
+static void held_rows() {
+    const struct {
+        int32_t dtype, rows, vocab;
+        bool held;
+    } cases[] = {{WS_DTYPE_BF16, 4, 131072, false}, {WS_DTYPE_BF16, 64, 131072, false},
+                 {WS_DTYPE_F16, 79, 98301, false},  {WS_DTYPE_BF16, 80, 131072, true},
+                 {WS_DTYPE_BF16, 4, 51197, true},   {WS_DTYPE_F16, 64, 51197, true},
+                 {WS_DTYPE_F32, 4, 65536, true},    {WS_DTYPE_F32, 32, 50001, true},
+                 {WS_DTYPE_F32, 64, 65541, false},  {WS_DTYPE_BF16, 4096, 131073, false}};
+    for (const auto& c : cases) {
+        ws_rows r = rows();
+        r.dtype = c.dtype;
+        r.rows = c.rows;
+        r.vocab = c.vocab;
+        r.row_stride = c.vocab;
+        for (int mode : {WS_DISTILL_RENORM, WS_DISTILL_TAIL})
+            CHECK((ws::plan_distill(r, mode, true, true).held > 0) == c.held);
+    }
+}
+
 // The kernels' own exponential against the 80-bit one: its series leaves 5e-18,
 // its argument 6e-17, and its last two steps round to 1.6e-16; near 0, and with
 // it 1 minus a teacher's probabilities, half a step of the result.
@@ -366,6 +388,7 @@ static int selftest() {
     CHECK(validate_workspace(at<void>(0x1008), 64, 64) == WS_E_INVALID_ARG);
     CHECK(validate_workspace(at<void>(0x1000), 64, 64) == WS_OK);
     plans();
+    held_rows();
     exponential();
     std::printf("%d failures\n", failures);
     return failures ? 1 : 0;

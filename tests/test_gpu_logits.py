@@ -1297,6 +1297,54 @@ def test_workspace_contents_do_not_matter(gpu_lib):
     assert (space[need:] == 0xff).all()
 
 
+def test_calls_with_a_distillation_workspace_each(gpu_lib):
+    """Loss and gradient in three kernels, whose statistics, tail and part sums
+    lie in the workspace: two streams at once, a graph replayed, and a workspace
+    of NaN patterns all give the bits of the calls alone."""
+    import torch
+    sets = [_all_calls(71, 2, 100001, "bf16"), _all_calls(72, 3, 90001, "f16")]
+    for mat, _, _ in sets:
+        assert lg.distill_workspace(mat.rows(1.1), lg.DISTILL_TAIL, True) > 0
+    alone = []
+    for _, calls, outs in sets:
+        for c in calls:
+            c.run()
+        torch.cuda.synchronize()
+        alone.append(_bits(outs))
+    graphs = []
+    for _, calls, _ in sets:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            for c in calls:
+                c.run(torch.cuda.current_stream().cuda_stream)
+    streams = [torch.cuda.Stream() for _ in sets]
+
+    def clear():
+        for _, calls, outs in sets:
+            for o in outs:
+                o.zero_()
+            calls[-1]._keep[-1].fill_(0xff)
+        torch.cuda.synchronize()
+
+    def check():
+        torch.cuda.synchronize()
+        for (_, _, outs), want in zip(sets, alone):
+            for a, b in zip(_bits(outs), want):
+                np.testing.assert_array_equal(a, b)
+
+    for _ in range(3):
+        clear()
+        for (_, calls, _), s in zip(sets, streams):
+            for c in calls:
+                c.run(s.cuda_stream)
+        check()
+        clear()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        check()
+
+
 def test_refusals_on_the_device(gpu_lib):
     import torch
     z = torch.zeros((4, 100), device=_dev())
