@@ -708,7 +708,7 @@ struct DistillParams {
     void* grad;
     int64_t grad_stride;
     int32_t vocab, k, mode;
-    int32_t rows, chunk, parts;
+    int32_t chunk, parts;
     int32_t mark_words;   // LDS words of marks
     float c, inv_tau;
 };
@@ -1407,7 +1407,6 @@ extern "C" int ws_distill(const ws_rows* rows, const ws_distill_args* args, void
     p.loss = args->loss;
     p.stats = args->stats;
     p.tail = args->tail;
-    p.rows = r.rows;
     p.vocab = r.vocab;
     p.k = args->teacher_k;
     p.mode = args->mode;
