@@ -885,6 +885,93 @@ def test_distill_many_special_rows(gpu_lib, mode, dtype, V):
 
 
 @pytest.mark.parametrize("mode", [ol.RENORM, ol.TAIL])
+@pytest.mark.parametrize("dtype,rows,V,pad,shift", [
+    ("f32", 6, 15001, 0, 0), ("f32", 6, 30001, 3, 2), ("f32", 6, 65536, 0, 0),
+    ("f32", 5, 65530, 3, 1), ("f16", 6, 30001, 1, 1), ("f16", 6, 60001, 0, 0),
+    ("f16", 80, 131072, 0, 0), ("bf16", 6, 30001, 0, 0), ("bf16", 6, 60001, 5, 3),
+    ("bf16", 81, 131064, 1, 0)])
+def test_distill_held_rows_against_the_oracle(gpu_lib, mode, dtype, rows, V, pad, shift):
+    """Loss and gradient of every row and token of the kernel that holds a row,
+    with four, eight and sixteen waves and rows that fill them."""
+    rng = np.random.default_rng(V + mode)
+    few = min(rows, 6)
+    z = _logits(rng, few, V)
+    z[2, rng.random(V) < 0.9] = -np.inf
+    at = np.arange(rows) % few
+    mat = Matrix(z[at], dtype, pad, shift)
+    ids, scores = make_teacher(rng, mat.z[:few], 50, mode)
+    ids[1, 4:9] = -1
+    ids[3, 1] = V - 1 if V - 1 not in ids[3] else ids[3, 1]
+    check_distill(mat, 1.3, ids[at], scores[at], mode, (rng.random(rows) + 0.5) * 1e3,
+                  pad=pad, shift=shift)
+
+
+@pytest.mark.parametrize("mode", [ol.RENORM, ol.TAIL])
+@pytest.mark.parametrize("dtype,V", [("f32", 900), ("f32", 20004), ("f32", 50004), ("f16", 40000),
+                                     ("f16", 100008), ("bf16", 9008), ("bf16", 131072)])
+def test_distill_rows_that_repeat_have_the_same_bits(gpu_lib, mode, dtype, V):
+    """130 rows of five kinds at starts that lie alike: loss and gradient of
+    every row are those of its kind's first, bit for bit, in place as well."""
+    rng = np.random.default_rng(V)
+    rows, few = 130, 5
+    at = np.arange(rows) % few
+    mat = Matrix(_logits(rng, few, V)[at], dtype)
+    ids, scores = make_teacher(rng, mat.z[:few], 40, mode)
+    ids[3, 0] = -1
+    g = (np.arange(few) + 1.0)[at]
+    loss, grad, _, _ = run_distill(mat, 1.2, ids[at], scores[at], mode, g)
+    small = Matrix(mat.z[:few], dtype)
+    check_distill(small, 1.2, ids, scores, mode, g[:few])
+    here, dhere, _, _ = run_distill(mat, 1.2, ids[at], scores[at], mode, g, in_place=True)
+    for l, d in ((loss, grad), (here, dhere)):
+        assert (l == loss[at]).all()
+        for r in range(rows):
+            assert np.array_equal(d[r], grad[r % few])
+
+
+@pytest.mark.parametrize("mode", [ol.RENORM, ol.TAIL])
+@pytest.mark.parametrize("dtype,rows,V", [("f32", 6, 5000), ("bf16", 80, 70001), ("f16", 4, 90001)])
+def test_distill_one_call_against_two(gpu_lib, mode, dtype, rows, V):
+    """Loss and gradient of one call against those of ws_distill and then
+    ws_distill_grad: each is within its tolerance of the formula, so the two are
+    within twice that of each other; statistics in FP32 between the two calls
+    are half a step of each more."""
+    rng = np.random.default_rng(15 + V)
+    few = min(rows, 6)
+    at = np.arange(rows) % few
+    mat = Matrix(_logits(rng, few, V)[at], dtype)
+    ids, scores = make_teacher(rng, mat.z[:few], 40, mode)
+    g = rng.random(rows)
+    one, done, _, _ = run_distill(mat, 1.0, ids[at], scores[at], mode, g)
+    two, dtwo, st, _ = run_distill(mat, 1.0, ids[at], scores[at], mode, g, separate=True)
+    listed = np.zeros(V, dtype=bool)
+    for r in range(rows):
+        z, i = mat.z[r], ids[r % few]
+        want, dz, tail = ol.distill(z, 1.0, scores[r % few].astype(np.float64), i, mode)
+        q, _, rest = ol.teacher_weights(scores[r % few].astype(np.float64), i, V, mode)
+        m, logsum = ol.stats(z, 1.0)
+        step = _sum_tol(V) + 8 * E * (1 + logsum)
+        tol = (q * 2 * E * (m - z[i])).sum() + (q.sum() + 2 * rest) * step + 2 * E * abs(want)
+        tol += 8 * E * rest * abs(tail) if mode == ol.TAIL else 0.0
+        assert abs(float(one[r]) - float(two[r])) <= 2 * tol
+        lp = z - m - logsum
+        listed[:] = False
+        listed[i] = True
+        weight = np.exp(lp) * (q.sum() + rest)
+        if mode == ol.TAIL:
+            share = np.exp(np.where(listed, -np.inf, lp - tail))
+            weight = np.where(listed, weight, share * (np.exp(tail) + rest))
+            step += 2 * _sum_tol(V) + 8 * E * (1 + abs(tail))
+        alone = np.zeros(V)
+        alone[i] = q
+        tol = (4 * E * (m - z + logsum) + 11 * E + step) * weight + 4 * E * (alone + weight)
+        tol = (tol + 2.0 ** -126) * g[r]
+        tol = tol + HALF[dtype] * (np.abs(dz) * g[r] + tol) + SMALLEST[dtype]
+        off = np.abs(done[r] - dtwo[r]) - 2 * tol
+        assert (off <= 0).all(), f"row {r}, token {off.argmax()}: {off.max()} past the tolerance"
+
+
+@pytest.mark.parametrize("mode", [ol.RENORM, ol.TAIL])
 def test_distill_entries(gpu_lib, mode):
     """Absent entries, none at all, the same token twice, scores of -inf,
     indices outside the row, every token listed, a teacher certain of one."""
