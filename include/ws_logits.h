@@ -21,7 +21,8 @@
  * the caller's buffers, allocates nothing, does not synchronise and can be
  * captured into a graph.  rows->device must be the calling thread's current
  * device.  Arguments are read during the call and not retained; the buffers
- * must stay until the stream has passed the call.  Calls share no state: two
+ * must stay until the stream has passed the call.  No output may overlap an
+ * input, the workspace or another output, but for gradients as said there.  Calls share no state: two
  * may run at once from any threads and streams as long as neither writes what
  * the other uses, the workspace included (two captured graphs that may run at
  * once need a workspace each).  A workspace needs no initialisation and its
@@ -166,7 +167,8 @@ int ws_logprobs_grad(const ws_rows *rows, const ws_logprobs_grad_args *args, voi
  * either sign and about 1e-7; against a p_t of 0 (every unlisted token masked,
  * by -inf or the type's lowest value) half of such rows would have an infinite
  * loss.  So where p_t is 0 in FP32 (log p_t below log 2^-150), a q_t of at most
- * WS_DISTILL_ROUNDING counts as 0.  A token listed twice counts with the sum of its q.  The gradient:
+ * WS_DISTILL_ROUNDING counts as 0.  A token listed twice is two terms of the
+ * loss, but one listed token to p_t and to the gradient, which is
  *   dz_j = g / tau (M p_j - sum_{k: id(k) = j} q_k)   for a listed token
  *   dz_j = g / tau (M - q_t / p_t) p_j                otherwise
  * with g = grad_loss[r] and M = sum_k q_k + q_t.  Where the student gives a

@@ -149,3 +149,12 @@ def test_distill_rounding_of_a_list_that_holds_all_of_the_mass():
             assert np.abs(np.delete(grad, allowed)).max() == 0
     # What rounding cannot explain stays: the student rules out a real tail.
     assert ol.distill(np.array([0.0, -np.inf]), 1.0, [-1e-3], [0], ol.TAIL)[0] == np.inf
+
+
+def test_distill_token_listed_twice_by_hand():
+    """Two terms of the loss, one token of p_t and of the gradient: teacher 0.25
+    and 0.25 on one token of a uniform student's four, 0.5 left."""
+    loss, grad, tail = ol.distill(np.zeros(4), 1.0, np.log([0.25, 0.25]), [2, 2], ol.TAIL)
+    want = 2 * 0.25 * math.log(0.25 / 0.25) + 0.5 * math.log(0.5 / 0.75)
+    assert abs(loss - want) < 1e-15 and abs(tail - math.log(0.75)) < 1e-15
+    np.testing.assert_allclose(grad, [0.25 / 3, 0.25 / 3, -0.25, 0.25 / 3], atol=1e-16)
