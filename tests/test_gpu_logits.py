@@ -478,6 +478,135 @@ def test_distill_row_of_more_parts_than_lanes(gpu_lib):
     assert not bad[~over].any()
 
 
+def test_most_rows(gpu_lib):
+    """WS_MAX_ROWS short rows of five kinds: each has the bits of the first of
+    its kind and start, and the first rows are the oracle's."""
+    import torch
+    rows, V, few, k = lg.MAX_ROWS, 17, 5, 4
+    rng = np.random.default_rng(2)
+    z = _logits(rng, few, V)
+    z[3, 4:] = -np.inf
+    d = _dev()
+    at = torch.arange(rows, device=d)
+    kind = at % few
+    mat = Matrix(np.zeros((0, V)), "bf16")
+    mat.shape, mat.stride = (rows, V), V
+    mat.view = torch.from_numpy(z).to(d).bfloat16()[kind].contiguous()
+    head = Matrix(z[np.arange(40) % few], "bf16")
+    ids, scores = make_teacher(rng, head.z[:few], k, ol.TAIL)
+    targets, up = rng.integers(0, V, few), rng.normal(size=few)
+    f = lambda *s: torch.zeros(s, dtype=torch.float32, device=d)  # noqa: E731
+    teacher = teacher_entries(ids, scores)[kind].contiguous()
+    tgt = torch.from_numpy(targets.astype(np.int32)).to(d)[kind].contiguous()
+    g = _dev32(up)[kind].contiguous()
+    lp, ent, st, loss, tail, dst = f(rows), f(rows), f(rows, 2), f(rows), f(rows), f(rows, 2)
+    top = torch.zeros((rows, k, 2), dtype=torch.int32, device=d)
+    grads = [torch.zeros((rows, V), dtype=torch.bfloat16, device=d) for _ in range(3)]
+    r = mat.rows(1.1)
+    for call in (lg.LogProbs(r, mat.view, targets=tgt, logprob=lp, entropy=ent, top_k=k, top=top,
+                             stats=st),
+                 lg.LogProbsGrad(r, mat.view, st, grads[0], targets=tgt, grad_logprob=g,
+                                 entropy=ent, grad_entropy=g),
+                 lg.Distill(r, mat.view, teacher, k, lg.DISTILL_TAIL, loss, stats=dst, tail=tail),
+                 lg.DistillGrad(r, mat.view, teacher, k, lg.DISTILL_TAIL, dst, g, grads[1],
+                                tail=tail),
+                 lg.Distill(r, mat.view, teacher, k, lg.DISTILL_TAIL, loss, grad_loss=g,
+                            grad_logits=grads[2])):
+        call.run(torch.cuda.current_stream().cuda_stream)
+    lead = at % 40                       # rows of 17 start alike every 8th
+    for x in (lp, ent, st, top, loss, tail, dst, *grads):
+        bits = x.view(torch.int16 if x.dtype == torch.bfloat16 else torch.int32)
+        assert torch.equal(bits, bits[:40][lead])
+    few_at = np.arange(40) % few
+    check_logprobs(head, 1.1, targets[few_at], k=k, got={
+        "logprob": lp[:40].cpu().numpy(), "entropy": ent[:40].cpu().numpy(),
+        "stats": st[:40].cpu().numpy(), "top_id": top[:40, :, 1].cpu().numpy(),
+        "top_score": top[:40].view(torch.float32)[:, :, 0].cpu().numpy()})
+    a = run_logprobs_grad(head, 1.1, st[:40].cpu().numpy(), targets[few_at], up[few_at],
+                          ent[:40].cpu().numpy(), up[few_at])
+    b = run_distill(head, 1.1, ids[few_at], scores[few_at], ol.TAIL, up[few_at])
+    c = run_distill(head, 1.1, ids[few_at], scores[few_at], ol.TAIL, up[few_at], separate=True)
+    check_logprobs_grad(head, 1.1, targets[few_at], up[few_at], up[few_at])
+    check_distill(head, 1.1, ids[few_at], scores[few_at], ol.TAIL, up[few_at])
+    check_distill(head, 1.1, ids[few_at], scores[few_at], ol.TAIL, up[few_at], separate=True)
+    for x, want in zip(grads, (a, c[1], b[1])):
+        assert np.array_equal(x[:40].double().cpu().numpy(), want)
+
+
+def test_longest_row(gpu_lib):
+    """One row of WS_MAX_SCORES FP32 logits through every operator, against sums
+    in 64 bits.  A thread adds 2^30 / 65,536 of them before it joins."""
+    import torch
+    V, k = 1 << 30, 8
+    d = _dev()
+    gen = torch.Generator(device=d)
+    gen.manual_seed(9)
+    z = torch.randn((1, V), device=d, generator=gen)
+    hot = torch.tensor([3, V - 1, 1 << 29, V // 3, 77, V - 2, 12345678, V // 7], device=d)
+    z[0, hot] += torch.arange(8, device=d) * 0.5 + 14.0
+    step = 1 << 26
+    m = float(z.max())
+    total = u = 0.0
+    for i in range(0, V, step):
+        x = z[0, i:i + step].double() - m
+        e = torch.exp(x)
+        total += float(e.sum())
+        u += float((e * x).sum())
+        del x, e
+    logsum = math.log(total)
+    entropy = logsum - u / total
+    order = hot[torch.argsort(z[0, hot], descending=True)]
+    lp = {int(i): float(z[0, i]) - m - logsum for i in hot}
+    f = lambda *s: torch.zeros(s, dtype=torch.float32, device=d)  # noqa: E731
+    r = lg.make_rows(rows=1, vocab=V)
+    got, ent, st, top = f(1), f(1), f(1, 2), torch.zeros((1, k, 2), dtype=torch.int32, device=d)
+    target = torch.tensor([V - 1], dtype=torch.int32, device=d)
+    lg.LogProbs(r, z, targets=target, logprob=got, entropy=ent, top_k=k, top=top, stats=st).run()
+    torch.cuda.synchronize()
+    tol = (V / 65536 + 100) * E + 8 * E * (1 + logsum)
+    assert torch.equal(top[0, :, 1].long(), order) and float(st[0, 0]) == np.float32(m)
+    assert abs(float(got) - lp[V - 1]) <= tol + 4 * E * abs(lp[V - 1])
+    assert abs(float(st[0, 1]) - logsum) <= tol
+    assert abs(float(ent) - entropy) <= 4 * tol * (1 + abs(logsum - entropy))
+    scores = top.view(torch.float32)[0, :, 0].double().cpu().numpy()
+    np.testing.assert_allclose(scores, [lp[int(i)] for i in order], atol=2 * tol + 100 * E)
+    # Gradients, token by token: with upstreams of 1, p's relative error.
+    rel = tol + 4 * E * (m + 8 + logsum) + 16 * E
+    one = torch.ones(1, device=d)
+    grad = torch.full((1, V), 7.0, device=d)
+    lg.LogProbsGrad(r, z, st, grad, targets=target, grad_logprob=one).run()
+    torch.cuda.synchronize()
+    for i in range(0, V, step):
+        want = -torch.exp(z[0, i:i + step].double() - m - logsum)
+        if i <= V - 1 < i + step:
+            want[V - 1 - i] += 1.0
+        off = (grad[0, i:i + step].double() - want).abs() - rel * want.abs() - 8 * E * (want > 0)
+        assert float(off.max()) <= 2.0 ** -126
+        del want, off
+    # The list holds part of the mass; the tail is the rest of the row.
+    entries = top.clone()
+    q = torch.arange(1, 9, device=d, dtype=torch.float64) / 48
+    entries.view(torch.float32)[0, :, 0] = torch.log(q).float()
+    q = torch.exp(entries.view(torch.float32)[0, :, 0].double())
+    listed = sum(math.exp(v) for v in lp.values())
+    tail, rest = math.log1p(-listed), 1.0 - float(q.sum())
+    want = sum(float(w) * (math.log(w) - lp[int(i)]) for w, i in zip(q, order))
+    want += rest * (math.log(rest) - tail)
+    loss = f(1)
+    lg.Distill(r, z, entries, k, lg.DISTILL_TAIL, loss, grad_loss=one, grad_logits=grad).run()
+    torch.cuda.synchronize()
+    assert abs(float(loss) - want) <= 4 * tol
+    for i in range(0, V, step):
+        p = torch.exp(z[0, i:i + step].double() - m - logsum)
+        dz = p * (1.0 - rest / math.exp(tail))
+        for w, j in zip(q, order):
+            if i <= int(j) < i + step:
+                dz[int(j) - i] = p[int(j) - i] - w
+        off = (grad[0, i:i + step].double() - dz).abs() - 4 * rel * p - 8 * E * (p > 1e-4)
+        assert float(off.max()) <= 2.0 ** -126
+        del p, dz, off
+
+
 def test_no_rows(gpu_lib):
     import torch
     z = torch.zeros((0, 50), device=_dev())
