@@ -22,11 +22,11 @@
  * captured into a graph.  rows->device must be the calling thread's current
  * device.  Arguments are read during the call and not retained; the buffers
  * must stay until the stream has passed the call.  No output may overlap an
- * input, the workspace or another output, but for gradients as said there.  Calls share no state: two
- * may run at once from any threads and streams as long as neither writes what
- * the other uses, the workspace included (two captured graphs that may run at
- * once need a workspace each).  A workspace needs no initialisation and its
- * contents do not matter between calls.
+ * input, the workspace or another output, but for gradients as said there.
+ * Calls share no state: two may run at once from any threads and streams as
+ * long as neither writes what the other uses, the workspace included (two
+ * captured graphs that may run at once need a workspace each).  A workspace
+ * needs no initialisation and its contents do not matter between calls.
  *
  * Numbers: logits are FP32, FP16 or BF16; everything else, and every sum, is
  * FP32 or wider.  Gradients are computed in FP32 and rounded once to the
