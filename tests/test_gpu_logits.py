@@ -1513,6 +1513,45 @@ def test_workspace_contents_do_not_matter(gpu_lib):
     assert (space[need:] == 0xff).all()
 
 
+def test_two_threads_at_once(gpu_lib):
+    """Two host threads, each with its own call objects and stream."""
+    import threading
+
+    import torch
+    sets = [_all_calls(81, 2, 100001, "bf16"), _all_calls(82, 40, 5003, "f32")]
+    alone = []
+    for _, calls, outs in sets:
+        for c in calls:
+            c.run()
+        torch.cuda.synchronize()
+        alone.append(_bits(outs))
+        for o in outs:
+            o.zero_()
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(calls, stream):
+        try:
+            for _ in range(50):
+                for c in calls:
+                    c.run(stream)
+        except Exception as e:      # reported by the test's own thread
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(calls, s.cuda_stream))
+               for (_, calls, _), s in zip(sets, streams)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed
+    for (_, _, outs), want in zip(sets, alone):
+        for a, b in zip(_bits(outs), want):
+            np.testing.assert_array_equal(a, b)
+
+
 def test_calls_with_a_distillation_workspace_each(gpu_lib):
     """Loss and gradient in three kernels, whose statistics, tail and part sums
     lie in the workspace: two streams at once, a graph replayed, and a workspace
