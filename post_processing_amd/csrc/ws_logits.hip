@@ -5,6 +5,7 @@
 #include <cfloat>
 #include <cstdint>
 
+#include "ws_enqueue.h"
 #include "ws_lanes.h"
 #include "ws_logits.h"
 #include "ws_logits_plan.h"
@@ -1197,14 +1198,6 @@ __global__ void __launch_bounds__(NT, 4) distill_step_kernel(DistillParams p) {
 
 // ---------------------------------------------------------------------------
 
-int device_ready(int32_t device) {
-    int ndev = 0;
-    if (hipGetDeviceCount(&ndev) != hipSuccess || device >= ndev) return WS_E_NO_DEVICE;
-    int cur = -1;
-    if (hipGetDevice(&cur) != hipSuccess) return WS_E_HIP;
-    return cur == device ? WS_OK : WS_E_INVALID_ARG;
-}
-
 // CALL(type) for the matrix's element type and way through the caches.
 #define WS_BY_TYPE(r, CALL)                                        \
     do {                                                           \
@@ -1220,18 +1213,6 @@ int device_ready(int32_t device) {
             else { CALL(BF16); }                                   \
         }                                                          \
     } while (0)
-
-// Enqueues one kernel; its parameters are one struct, copied by the call.
-template <typename P>
-int launch(void (*kernel)(P), int64_t groups, int threads, const P& params, hipStream_t s,
-           size_t lds = 0) {
-    P copy = params;
-    void* args[] = {&copy};
-    const hipError_t e =
-        hipLaunchKernel(reinterpret_cast<const void*>(kernel), dim3((uint32_t)groups),
-                        dim3((uint32_t)threads), args, lds, s);
-    return e == hipSuccess ? WS_OK : WS_E_HIP;
-}
 
 template <typename L>
 int run_logprobs(const ws_rows& r, const LogprobsPlan& plan, const LogprobsParams& p,

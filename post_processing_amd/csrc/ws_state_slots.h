@@ -1,0 +1,134 @@
+// ws_state_slots.h -- device code shared by the kernels over rows of hidden
+// states: 16-byte slots of a row at any element address, and a workgroup's
+// sums.  Internal to the library.
+//
+// Slot s of a row is its elements s * VEC .. s * VEC + VEC - 1, read and
+// written as one 16-byte access wherever the row starts: gfx950 takes global
+// accesses of dwords at any byte address (a row that starts off 16 bytes
+// straddles a cache line in every fourth slot or so).  The elements of a last
+// slot that ends behind the row are read and written one by one.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "ws_logits_rows.h"
+
+namespace ws {
+
+typedef uint32_t Slot2 __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t Slot4 __attribute__((ext_vector_type(4), aligned(4)));
+
+template <typename L>
+__device__ __forceinline__ uint4 load_loose(const typename L::Elem* p) {
+    Slot16 v;
+    if constexpr (sizeof(typename L::Elem) == 2) {
+        const Slot2* q = reinterpret_cast<const Slot2*>(p);
+        if constexpr (L::kStream) v = __builtin_nontemporal_load(q);
+        else v = *q;
+    } else {
+        const Slot4* q = reinterpret_cast<const Slot4*>(p);
+        if constexpr (L::kStream) v = __builtin_nontemporal_load(q);
+        else v = *q;
+    }
+    return make_uint4(v.x, v.y, v.z, v.w);
+}
+
+template <typename L>
+__device__ __forceinline__ void store_loose(typename L::Elem* p, uint4 w) {
+    const Slot16 v = {w.x, w.y, w.z, w.w};
+    if constexpr (sizeof(typename L::Elem) == 2) {
+        Slot2* q = reinterpret_cast<Slot2*>(p);
+        if constexpr (L::kStream) __builtin_nontemporal_store((Slot2)v, q);
+        else *q = v;
+    } else {
+        Slot4* q = reinterpret_cast<Slot4*>(p);
+        if constexpr (L::kStream) __builtin_nontemporal_store((Slot4)v, q);
+        else *q = v;
+    }
+}
+
+// Elements c .. c + VEC - 1 of a row of `width`, 0 behind it.
+template <typename L>
+__device__ __forceinline__ uint4 load_columns(const typename L::Elem* row, int c, int width) {
+    if (c + L::VEC <= width) return load_loose<L>(row + c);
+    float v[L::VEC];
+#pragma unroll
+    for (int j = 0; j < L::VEC; ++j) v[j] = c + j < width ? L::up(row[c + j]) : 0.0f;
+    return L::pack(v);
+}
+
+template <typename L>
+__device__ __forceinline__ void store_columns(typename L::Elem* row, int c, int width,
+                                              const float (&v)[L::VEC]) {
+    if (c + L::VEC <= width) {
+        store_loose<L>(row + c, L::pack(v));
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < L::VEC; ++j)
+        if (c + j < width) row[c + j] = L::down(v[j]);
+}
+
+// The same of a row of N FP32 or L values (a weight, a sum), as `f32` says.
+template <typename L>
+__device__ __forceinline__ void load_either(const void* row, bool f32, int c, int width,
+                                            float (&v)[L::VEC]) {
+    if (f32) {
+        const float* p = static_cast<const float*>(row);
+        if (c + L::VEC <= width) {
+#pragma unroll
+            for (int j = 0; j < L::VEC; j += 4) {
+                float part[4];
+                F32::unpack(load_loose<F32>(p + c + j), part);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[j + i] = part[i];
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < L::VEC; ++j) v[j] = c + j < width ? p[c + j] : 0.0f;
+        }
+    } else {
+        L::unpack(load_columns<L>(static_cast<const typename L::Elem*>(row), c, width), v);
+    }
+}
+
+template <typename L>
+__device__ __forceinline__ void store_either(void* row, bool f32, int c, int width,
+                                             const float (&v)[L::VEC]) {
+    if (f32) {
+        float* p = static_cast<float*>(row);
+        if (c + L::VEC <= width) {
+#pragma unroll
+            for (int j = 0; j < L::VEC; j += 4) {
+                const float part[4] = {v[j], v[j + 1], v[j + 2], v[j + 3]};
+                store_loose<F32>(p + c + j, F32::pack(part));
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < L::VEC; ++j)
+                if (c + j < width) p[c + j] = v[j];
+        }
+    } else {
+        store_columns<L>(static_cast<typename L::Elem*>(row), c, width, v);
+    }
+}
+
+// The sum over a workgroup, in every thread.  `waves` (LDS) must not be
+// written again before every thread has read it: two sums in turn take two.
+template <int NT>
+__device__ __forceinline__ float group_sum(float v, float* waves) {
+    const int lane = threadIdx.x & 63;
+    v = wave_sum(v, lane);
+    if constexpr (NT > 64) {
+        if (lane == 0) waves[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NT / 64; ++i) v += waves[i];
+    }
+    return v;
+}
+
+}  // namespace ws

@@ -1,0 +1,256 @@
+// ws_states_plan.h -- host-side checks and launch geometry of the operators
+// over rows of hidden states (ws_states.h).
+//
+// Plain C++17 with no HIP dependency, so the same code the library runs can
+// be compiled and tested on a host without a GPU.
+#pragma once
+
+#include <cmath>
+#include <cstddef>
+#include <cstdint>
+
+#include "ws_logits_plan.h"
+#include "ws_states.h"
+
+namespace ws {
+
+inline bool stride_ok(int64_t stride, int32_t width) {
+    return stride >= width && stride <= WS_MAX_ROW_STRIDE;
+}
+
+inline int validate_states(const ws_states* t) {
+    if (!t) return WS_E_INVALID_ARG;
+    if (t->device < 0) return WS_E_INVALID_ARG;
+    if (t->dtype != WS_DTYPE_F32 && t->dtype != WS_DTYPE_F16 && t->dtype != WS_DTYPE_BF16)
+        return WS_E_INVALID_ARG;
+    if (t->rows < 0 || t->rows > WS_MAX_ROWS) return WS_E_INVALID_ARG;
+    if (t->width < 1 || t->width > WS_MAX_WIDTH) return WS_E_INVALID_ARG;
+    return stride_ok(t->row_stride, t->width) ? WS_OK : WS_E_INVALID_ARG;
+}
+
+// A matrix of `rows` rows in memory.
+struct Extent {
+    const void* at;
+    int64_t rows, width, stride;   // elements
+    int32_t dtype;
+
+    uintptr_t begin() const { return (uintptr_t)at; }
+    uintptr_t bytes() const {
+        return rows == 0 ? 0 : (uintptr_t)(((rows - 1) * stride + width) * logit_bytes(dtype));
+    }
+    bool aligned() const { return aligned_to(at, (uintptr_t)logit_bytes(dtype)); }
+};
+
+// Whether no byte belongs to both: apart, or between each other's rows (equal
+// steps: two rows then lie a fixed distance modulo the step apart, wherever the
+// two extents meet).
+inline bool disjoint(const Extent& a, const Extent& b) {
+    if (a.rows == 0 || b.rows == 0) return true;
+    const uintptr_t apart = a.begin() < b.begin() ? b.begin() - a.begin() : a.begin() - b.begin();
+    if (apart >= (a.begin() < b.begin() ? a.bytes() : b.bytes())) return true;
+    const uintptr_t step = (uintptr_t)(a.stride * logit_bytes(a.dtype));
+    if (step != (uintptr_t)(b.stride * logit_bytes(b.dtype))) return false;
+    // From the lower one's row to the next row of the upper one, and back.
+    const Extent& low = a.begin() < b.begin() ? a : b;
+    const Extent& high = a.begin() < b.begin() ? b : a;
+    const uintptr_t into = apart % step;
+    return into >= (uintptr_t)(low.width * logit_bytes(low.dtype)) &&
+           step - into >= (uintptr_t)(high.width * logit_bytes(high.dtype));
+}
+
+// The same rows of the same elements.
+inline bool same_rows(const Extent& a, const Extent& b) {
+    return a.at == b.at && a.dtype == b.dtype && (a.stride == b.stride || a.rows <= 1);
+}
+
+inline Extent extent_of(const ws_states& t, const void* at, int64_t stride) {
+    return {at, t.rows, t.width, stride, t.dtype};
+}
+
+// ---- embedding -----------------------------------------------------------------
+
+inline int validate_embed(const ws_states* t, const ws_embed_args* a) {
+    const int v = validate_states(t);
+    if (v != WS_OK) return v;
+    if (!a || a->vocab < 1 || a->vocab > WS_MAX_TOKENS) return WS_E_INVALID_ARG;
+    if (!stride_ok(a->table_stride, t->width) || !std::isfinite(a->scale)) return WS_E_INVALID_ARG;
+    if (t->rows == 0) return WS_OK;
+    const Extent out = extent_of(*t, a->out, t->row_stride);
+    const Extent table = {a->table, a->vocab, t->width, a->table_stride, t->dtype};
+    const Extent ids = {a->ids, 1, t->rows, t->rows, WS_DTYPE_F32};
+    if (!a->table || !a->out || !a->ids) return WS_E_INVALID_ARG;
+    if (!out.aligned() || !table.aligned() || !ids.aligned()) return WS_E_INVALID_ARG;
+    return disjoint(out, table) && disjoint(out, ids) ? WS_OK : WS_E_INVALID_ARG;
+}
+
+inline int validate_weight_dtype(const ws_states& t, int32_t dtype) {
+    return dtype == t.dtype || dtype == WS_DTYPE_F32 ? WS_OK : WS_E_INVALID_ARG;
+}
+
+inline int validate_embed_grad(const ws_states* t, const ws_embed_grad_args* a) {
+    const int v = validate_states(t);
+    if (v != WS_OK) return v;
+    if (!a || a->vocab < 1 || a->vocab > WS_MAX_TOKENS) return WS_E_INVALID_ARG;
+    if (!stride_ok(a->grad_stride, t->width) || !std::isfinite(a->scale)) return WS_E_INVALID_ARG;
+    if (validate_weight_dtype(*t, a->grad_dtype) != WS_OK) return WS_E_INVALID_ARG;
+    if (a->accumulate != 0 && a->accumulate != 1) return WS_E_INVALID_ARG;
+    const Extent grad = {a->grad_table, a->vocab, t->width, a->grad_stride, a->grad_dtype};
+    if (!a->grad_table || !grad.aligned()) return WS_E_INVALID_ARG;
+    if (t->rows == 0) return WS_OK;
+    const Extent rows = extent_of(*t, a->grad_out, t->row_stride);
+    const Extent ids = {a->ids, 1, t->rows, t->rows, WS_DTYPE_F32};
+    if (!a->grad_out || !a->ids || !rows.aligned() || !ids.aligned()) return WS_E_INVALID_ARG;
+    return disjoint(grad, rows) && disjoint(grad, ids) ? WS_OK : WS_E_INVALID_ARG;
+}
+
+inline int64_t slots_in(int32_t width, int32_t dtype) {
+    const int64_t vec = 16 / logit_bytes(dtype);
+    return (width + vec - 1) / vec;
+}
+
+// Lookup: a workgroup of 256 threads takes 256 / lanes rows, `lanes` (a power
+// of two) threads to a row's 16-byte slots.
+constexpr int kLookupThreads = 256;
+
+struct EmbedPlan {
+    int32_t lanes = 8;
+    int64_t groups = 0;
+};
+
+inline EmbedPlan plan_embed(const ws_states& t) {
+    EmbedPlan p;
+    const int64_t slots = slots_in(t.width, t.dtype);
+    while (p.lanes < slots && p.lanes < kLookupThreads) p.lanes *= 2;
+    const int64_t each = kLookupThreads / p.lanes;
+    p.groups = (t.rows + each - 1) / each;
+    return p;
+}
+
+// Gradient: tokens sorted in tiles of kSortTile, one digit of kDigitBits a pass;
+// the sorted rows are added in blocks of `block` rows.
+constexpr int kSortTile = 2048, kDigitBits = 9, kDigits = 1 << kDigitBits;
+constexpr int kMostBlocks = 8192, kBlockRows = 32, kSumThreads = 256;
+
+struct EmbedGradPlan {
+    int32_t tiles = 0;
+    int32_t passes = 0;
+    int32_t block = kBlockRows;    // sorted rows added by one workgroup
+    int32_t blocks = 0;
+    int32_t columns = 0;           // workgroups over a row's slots
+    size_t keys_at[2] = {0, 0}, rows_at[2] = {0, 0}, counts_at = 0, partial_at = 0;
+    size_t workspace = 0;
+};
+
+inline size_t round16(size_t n) { return (n + 15) / 16 * 16; }
+
+inline EmbedGradPlan plan_embed_grad(const ws_states& t, int32_t vocab) {
+    EmbedGradPlan p;
+    if (t.rows == 0) return p;
+    const int64_t n = t.rows;
+    p.tiles = (int32_t)((n + kSortTile - 1) / kSortTile);
+    // Keys are 0..vocab, vocab standing for no token.
+    int bits = 1;
+    while ((vocab >> bits) != 0) ++bits;
+    p.passes = (bits + kDigitBits - 1) / kDigitBits;
+    if (n > (int64_t)p.block * kMostBlocks) p.block = (int32_t)((n + kMostBlocks - 1) / kMostBlocks);
+    p.blocks = (int32_t)((n + p.block - 1) / p.block);
+    p.columns = (int32_t)((slots_in(t.width, t.dtype) + kSumThreads - 1) / kSumThreads);
+    const size_t each = round16((size_t)n * 4);
+    size_t at = 0;
+    for (int i = 0; i < 2; ++i) {
+        p.keys_at[i] = at;
+        p.rows_at[i] = at + each;
+        at += 2 * each;
+    }
+    p.counts_at = at;
+    at += (size_t)p.tiles * kDigits * 4;
+    // Two rows of FP32 sums a block: of the token that began before it, and of
+    // the one that goes on behind it.
+    p.partial_at = at;
+    at += (size_t)p.blocks * 2 * round16((size_t)t.width * 4);
+    p.workspace = at;
+    return p;
+}
+
+// ---- layer norm ------------------------------------------------------------------
+
+inline bool in_place_or_apart(const Extent& out, const Extent& in) {
+    return same_rows(out, in) || disjoint(out, in);
+}
+
+inline int validate_layernorm(const ws_states* t, const ws_layernorm_args* a) {
+    const int v = validate_states(t);
+    if (v != WS_OK) return v;
+    if (!a || validate_weight_dtype(*t, a->weight_dtype) != WS_OK) return WS_E_INVALID_ARG;
+    if (!stride_ok(a->y_stride, t->width)) return WS_E_INVALID_ARG;
+    if (!(a->eps >= 0.0f) || !std::isfinite(a->eps)) return WS_E_INVALID_ARG;
+    if (t->rows == 0) return WS_OK;
+    const Extent x = extent_of(*t, a->x, t->row_stride), y = extent_of(*t, a->y, a->y_stride);
+    const Extent weight = {a->weight, a->weight ? 1 : 0, t->width, t->width, a->weight_dtype};
+    const Extent bias = {a->bias, a->bias ? 1 : 0, t->width, t->width, a->weight_dtype};
+    const Extent stats = {a->stats, a->stats ? 1 : 0, 2ll * t->rows, 2ll * t->rows, WS_DTYPE_F32};
+    if (!a->x || !a->y || !x.aligned() || !y.aligned() || !aligned_to(a->stats, 8))
+        return WS_E_INVALID_ARG;
+    if (!weight.aligned() || !bias.aligned()) return WS_E_INVALID_ARG;
+    if (!in_place_or_apart(y, x) || !disjoint(y, weight) || !disjoint(y, bias) ||
+        !disjoint(y, stats) || !disjoint(stats, x) || !disjoint(stats, weight) ||
+        !disjoint(stats, bias))
+        return WS_E_INVALID_ARG;
+    return WS_OK;
+}
+
+inline int validate_layernorm_grad(const ws_states* t, const ws_layernorm_grad_args* a) {
+    const int v = validate_states(t);
+    if (v != WS_OK) return v;
+    if (!a || a->reserved != 0) return WS_E_INVALID_ARG;
+    if (validate_weight_dtype(*t, a->weight_dtype) != WS_OK) return WS_E_INVALID_ARG;
+    if (!stride_ok(a->grad_y_stride, t->width)) return WS_E_INVALID_ARG;
+    if (a->grad_x && !stride_ok(a->grad_x_stride, t->width)) return WS_E_INVALID_ARG;
+    if (!a->grad_x && !a->grad_weight && !a->grad_bias) return WS_E_INVALID_ARG;
+    const Extent gw = {a->grad_weight, a->grad_weight ? 1 : 0, t->width, t->width, a->weight_dtype};
+    const Extent gb = {a->grad_bias, a->grad_bias ? 1 : 0, t->width, t->width, a->weight_dtype};
+    if (!gw.aligned() || !gb.aligned() || !disjoint(gw, gb)) return WS_E_INVALID_ARG;
+    if (t->rows == 0) return WS_OK;
+    const Extent x = extent_of(*t, a->x, t->row_stride);
+    const Extent gy = extent_of(*t, a->grad_y, a->grad_y_stride);
+    Extent gx = extent_of(*t, a->grad_x, a->grad_x_stride);
+    if (!a->grad_x) gx.rows = 0;
+    const Extent weight = {a->weight, a->weight ? 1 : 0, t->width, t->width, a->weight_dtype};
+    const Extent stats = {a->stats, 1, 2ll * t->rows, 2ll * t->rows, WS_DTYPE_F32};
+    if (!a->x || !a->grad_y || !a->stats || !x.aligned() || !gy.aligned() || !gx.aligned() ||
+        !weight.aligned() || !aligned_to(a->stats, 8))
+        return WS_E_INVALID_ARG;
+    if (!in_place_or_apart(gx, x) || !in_place_or_apart(gx, gy) || !disjoint(gx, weight) ||
+        !disjoint(gx, stats))
+        return WS_E_INVALID_ARG;
+    for (const Extent* out : {&gw, &gb})
+        if (!disjoint(*out, x) || !disjoint(*out, gy) || !disjoint(*out, gx) ||
+            !disjoint(*out, weight) || !disjoint(*out, stats))
+            return WS_E_INVALID_ARG;
+    return WS_OK;
+}
+
+constexpr int kNormThreads = 256;
+
+// Sums over the rows: `groups` workgroups' sums of every column, then their sum.
+constexpr int64_t kColumnGroups = 512;
+
+struct NormGradPlan {
+    int32_t columns = 1;   // workgroups over the columns
+    int32_t groups = 1;    // over the rows
+    size_t workspace = 0;
+};
+
+inline NormGradPlan plan_layernorm_grad(const ws_states& t) {
+    NormGradPlan p;
+    p.columns = (int32_t)((slots_in(t.width, t.dtype) + kNormThreads - 1) / kNormThreads);
+    int64_t groups = kColumnGroups / p.columns;
+    const int64_t most = (t.rows + 7) / 8;
+    if (groups > most) groups = most;
+    if (groups < 1) groups = 1;
+    p.groups = (int32_t)groups;
+    p.workspace = (size_t)groups * 2 * round16((size_t)t.width * 4);
+    return p;
+}
+
+}  // namespace ws

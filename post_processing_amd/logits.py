@@ -191,7 +191,7 @@ class _Call:
     _name = ""
 
     def _bind(self, rows: Rows, args, *keep):
-        self._rows = Rows.from_buffer_copy(rows)
+        self._rows = type(rows).from_buffer_copy(rows)
         self._args = args
         self._keep = keep
         self._fn = getattr(load(), self._name)
