@@ -9,6 +9,8 @@
  *   ws_distill        distillation loss against a teacher's top entries, and
  *                     on request its gradient in the same call
  *   ws_distill_grad   that gradient alone, from the loss call's statistics
+ *   ws_sample         a token drawn from every row, with temperature, top-k,
+ *                     top-p and min-p, by given random numbers
  *
  * The alternatives ws_logprobs reports for a teacher's logits are, as they
  * lie in memory, the teacher entries ws_distill takes.
@@ -218,6 +220,52 @@ typedef struct ws_distill_grad_args {
 } ws_distill_grad_args;
 
 int ws_distill_grad(const ws_rows *rows, const ws_distill_grad_args *args, void *stream);
+
+/* ---- sampling --------------------------------------------------------------
+ * Per row, with its temperature tau, top_k k, top_p p, min_p q and uniform
+ * number u in [0, 1): w_j = exp((z_j - max z) / tau), and the tokens in order of
+ * their logits (equal ones by index, as ws_logprobs orders them):
+ *   A     the first k tokens of the order; all for k = 0 or k >= V
+ *   B     the first n tokens of the order, n the smallest with
+ *         sum_B w >= p sum_A w, at least 1; A itself for p = 1
+ *   kept  the tokens of A and B with w_j >= q
+ *   token the first kept token, in the order of the vocabulary, for which the
+ *         sum of w over the kept tokens up to and including it exceeds u times
+ *         that over all of them
+ *   logprob  log(w_token / sum_kept w): the log of the probability it was
+ *         drawn with
+ * A temperature of 0 is greedy: the best token, whatever the other settings,
+ * with logprob 0.  The settings are arrays of the rows, so that a batch may mix
+ * requests; each may be NULL: rows->temperature, k = 0, p = 1, q = 0 then hold
+ * for every row.
+ *
+ * w and its sums are FP64 (a token is a whole number: with sums in FP32 one draw
+ * in a hundred from a large vocabulary would be another token), sums_A and the
+ * sum it is compared with are held in steps of max(V, 2^10) 2^-62 or finer; a w
+ * below e^-200 counts as 0.
+ *
+ * A row that holds a NaN or +inf has token -1 and logprob NaN, and so has one
+ * whose settings lie outside their ranges (tau 0 or WS_MIN_TEMPERATURE..
+ * WS_MAX_TEMPERATURE, k >= 0, p and q 0..1, u 0 <= u < 1; the device sees them,
+ * the call does not).  A row of -inf only has token -1 and logprob -inf. */
+typedef struct ws_sample_args {
+    const void    *logits;
+    const float   *uniform;          /* [rows]                                */
+    const float   *temperature;      /* [rows] or NULL                        */
+    const int32_t *top_k;            /* [rows] or NULL                        */
+    const float   *top_p;            /* [rows] or NULL                        */
+    const float   *min_p;            /* [rows] or NULL                        */
+    int32_t       *token;            /* [rows]                                */
+    float         *logprob;          /* [rows] or NULL                        */
+    void          *workspace;        /* ws_sample_workspace bytes, 16-byte
+                                        aligned; NULL when 0                  */
+    size_t         workspace_bytes;
+} ws_sample_args;
+
+/* Workspace bytes of ws_sample for this shape (0 for many shapes). */
+int ws_sample_workspace(const ws_rows *rows, size_t *bytes);
+
+int ws_sample(const ws_rows *rows, const ws_sample_args *args, void *stream);
 
 #ifdef __cplusplus
 }

@@ -128,3 +128,40 @@ def distill(z, tau, scores, ids, mode, g=1.0):
     if np.isneginf(logp).all():
         grad = np.zeros(n)
     return float(loss), grad, tail
+
+
+def kept_tokens(z, tau, k=0, p=1.0, q=0.0):
+    """The tokens sampling keeps, in vocabulary order, and their weights: the
+    first k by logit (equal ones by index), of them the shortest run that holds
+    p of their mass, of them those of at least q times the best one's weight."""
+    z = np.asarray(z, dtype=np.float64)
+    if tau == 0:
+        tau, k, p, q = 1.0, 1, 1.0, 0.0
+    with np.errstate(under="ignore"):
+        x = (z - z.max()) / tau
+        w = np.where(x < -200, 0.0, np.exp(x))
+    order = np.argsort(-z, kind="stable")
+    if k:
+        order = order[:k]
+    if p < 1:
+        upto = np.cumsum(w[order])
+        order = order[:max(1, int((upto < p * upto[-1]).sum()) + 1)]
+    with np.errstate(divide="ignore"):
+        order = order[(x[order] >= np.log(q)) & (w[order] > 0)]
+    kept = np.sort(order)
+    return kept, w[kept]
+
+
+def sample(z, u, tau, k=0, p=1.0, q=0.0):
+    """(token, log of the probability it was drawn with)."""
+    z = np.asarray(z, dtype=np.float64)
+    fine = (0 <= u < 1 and k >= 0 and 0 <= p <= 1 and 0 <= q <= 1
+            and (tau == 0 or 1e-3 <= np.float32(tau) * (1 + 1e-7) and tau <= 1e3))
+    if not fine or np.isnan(z).any() or np.isposinf(z).any():
+        return -1, np.nan
+    if np.isneginf(z.max()):
+        return -1, -np.inf
+    kept, w = kept_tokens(z, tau, k, p, q)
+    upto = np.cumsum(w)
+    at = min(int((upto <= u * upto[-1]).sum()), len(kept) - 1)
+    return int(kept[at]), float(np.log(w[at] / upto[-1]))

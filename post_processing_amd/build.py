@@ -18,7 +18,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libws.so")
 SOURCES = ["ws_preprocess.hip", "ws_topk.hip", "ws_detect.hip", "ws_runtime.hip",
-           "ws_noalloc.hip", "ws_logits.hip", "ws_norm.hip", "ws_embed.hip"]
+           "ws_noalloc.hip", "ws_logits.hip", "ws_norm.hip", "ws_embed.hip",
+           "ws_sample.hip"]
 ARCH = "gfx950"
 
 

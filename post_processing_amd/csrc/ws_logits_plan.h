@@ -8,6 +8,7 @@
 #include <cmath>
 #include <cstddef>
 #include <cstdint>
+#include <initializer_list>
 
 #include "ws_logits.h"
 
@@ -137,6 +138,20 @@ inline int validate_distill_grad(const ws_rows* r, const ws_distill_grad_args* a
         if (!a->grad_loss || !aligned_to(a->grad_loss, 4)) return WS_E_INVALID_ARG;
     }
     return validate_gradient(*r, a->logits, a->grad_logits, a->grad_stride);
+}
+
+inline int validate_sample(const ws_rows* r, const ws_sample_args* a) {
+    const int v = validate_rows(r);
+    if (v != WS_OK) return v;
+    if (!a) return WS_E_INVALID_ARG;
+    if (r->rows == 0) return WS_OK;
+    if (!logits_ok(*r, a->logits)) return WS_E_INVALID_ARG;
+    if (!a->uniform || !a->token) return WS_E_INVALID_ARG;
+    for (const void* p : {(const void*)a->uniform, (const void*)a->temperature,
+                          (const void*)a->top_k, (const void*)a->top_p, (const void*)a->min_p,
+                          (const void*)a->token, (const void*)a->logprob})
+        if (!aligned_to(p, 4)) return WS_E_INVALID_ARG;
+    return WS_OK;
 }
 
 inline int validate_workspace(const void* workspace, size_t given, size_t needed) {
@@ -308,6 +323,19 @@ inline DistillPlan plan_distill(const ws_rows& r, int32_t mode, bool gradient, b
     if (mode == WS_DISTILL_TAIL)
         p.mark_bytes = p.held > 0 ? p.held * p.threads
                                   : (p.chunk + p.parts + kBatchSlots * p.threads + 15) / 16 * 16;
+    return p;
+}
+
+// ws_sample: a workgroup a row.
+struct SamplePlan {
+    int32_t threads = 1024;
+    size_t workspace = 0;
+};
+
+inline SamplePlan plan_sample(const ws_rows& r) {
+    SamplePlan p;
+    if (r.rows == 0) return p;
+    p.threads = slots_of(r) <= 1024 ? 256 : 1024;
     return p;
 }
 

@@ -75,6 +75,13 @@ class DistillGradArgs(Structure):
                 ("grad_stride", c_int64), ("teacher_k", c_int32), ("mode", c_int32)]
 
 
+class SampleArgs(Structure):
+    _fields_ = [("logits", c_void_p), ("uniform", c_void_p), ("temperature", c_void_p),
+                ("top_k", c_void_p), ("top_p", c_void_p), ("min_p", c_void_p),
+                ("token", c_void_p), ("logprob", c_void_p), ("workspace", c_void_p),
+                ("workspace_bytes", c_size_t)]
+
+
 _lib = None
 
 
@@ -90,8 +97,11 @@ def load():
     lib.ws_logprobs_grad.argtypes = [POINTER(Rows), POINTER(LogProbsGradArgs), c_void_p]
     lib.ws_distill.argtypes = [POINTER(Rows), POINTER(DistillArgs), c_void_p]
     lib.ws_distill_grad.argtypes = [POINTER(Rows), POINTER(DistillGradArgs), c_void_p]
+    lib.ws_sample_workspace.argtypes = [POINTER(Rows), POINTER(c_size_t)]
+    lib.ws_sample.argtypes = [POINTER(Rows), POINTER(SampleArgs), c_void_p]
     for name in ("ws_logprobs_workspace", "ws_distill_workspace", "ws_logprobs",
-                 "ws_logprobs_grad", "ws_distill", "ws_distill_grad"):
+                 "ws_logprobs_grad", "ws_distill", "ws_distill_grad", "ws_sample_workspace",
+                 "ws_sample"):
         getattr(lib, name).restype = c_int
     _lib = lib
     return lib
@@ -137,6 +147,13 @@ def distill_workspace(rows: Rows, mode: int, gradient: bool) -> int:
     n = c_size_t(0)
     _check(load().ws_distill_workspace(byref(rows), _int32("mode", mode), 1 if gradient else 0, byref(n)),
            "ws_distill_workspace")
+    return n.value
+
+
+def sample_workspace(rows: Rows) -> int:
+    """Bytes of workspace ws_sample needs for this shape."""
+    n = c_size_t(0)
+    _check(load().ws_sample_workspace(byref(rows), byref(n)), "ws_sample_workspace")
     return n.value
 
 
@@ -316,6 +333,30 @@ class DistillGrad(_Call):
         a.teacher_k = _int32("teacher_k", teacher_k)
         a.mode = _int32("mode", mode)
         self._bind(rows, a, logits, teacher, stats, tail, grad_loss, grad_logits)
+
+
+class Sample(_Call):
+    """ws_sample: a token of every row, drawn by `uniform`; `temperature`,
+    `top_k`, `top_p` and `min_p` are one value a row (float32, top_k int32), and
+    what is None is the rows' temperature, or off."""
+
+    _name = "ws_sample"
+
+    def __init__(self, rows: Rows, logits, uniform, token, *, temperature=None, top_k=None,
+                 top_p=None, min_p=None, logprob=None, workspace=None):
+        n = rows.rows
+        a = SampleArgs()
+        a.logits = _matrix("logits", logits, rows, rows.row_stride)
+        a.uniform = _buffer("uniform", uniform, rows, _F32, n)
+        a.temperature = _buffer("temperature", temperature, rows, _F32, n)
+        a.top_k = _buffer("top_k", top_k, rows, _I32, n)
+        a.top_p = _buffer("top_p", top_p, rows, _F32, n)
+        a.min_p = _buffer("min_p", min_p, rows, _F32, n)
+        a.token = _buffer("token", token, rows, _I32, n)
+        a.logprob = _buffer("logprob", logprob, rows, _F32, n)
+        workspace = self._own_workspace(rows, a, workspace, sample_workspace(rows))
+        self._bind(rows, a, logits, uniform, token, temperature, top_k, top_p, min_p, logprob,
+                   workspace)
 
 
 def _stride(grad_logits, rows: Rows, given) -> int:

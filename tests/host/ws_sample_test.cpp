@@ -1,0 +1,106 @@
+// Host-only driver for the checks and launch geometry of sampling
+// (ws_logits_plan.h): compiled with g++ and no HIP by tests/test_sample_host.py.
+//   ws_sample_test selftest  -> argument checks and plans
+//   ws_sample_test layout    -> "struct field offset" for the ABI structs
+#include <cstddef>
+#include <cstdio>
+#include <cstring>
+#include <initializer_list>
+
+#include "ws_logits_plan.h"
+
+static int failures = 0;
+#define CHECK(cond)                                                    \
+    do {                                                               \
+        if (!(cond)) {                                                 \
+            std::printf("FAIL %s:%d %s\n", __FILE__, __LINE__, #cond); \
+            ++failures;                                                \
+        }                                                              \
+    } while (0)
+
+template <typename T>
+static T* at(uintptr_t a) {
+    return reinterpret_cast<T*>(a);
+}
+
+static ws_rows rows() {
+    ws_rows r;
+    std::memset(&r, 0, sizeof r);
+    r.dtype = WS_DTYPE_BF16;
+    r.rows = 8;
+    r.vocab = 1000;
+    r.row_stride = 1024;
+    r.temperature = 1.0f;
+    return r;
+}
+
+static ws_sample_args sample() {
+    ws_sample_args a;
+    std::memset(&a, 0, sizeof a);
+    a.logits = at<void>(0x10000);
+    a.uniform = at<float>(0x80000);
+    a.temperature = at<float>(0x81000);
+    a.top_k = at<int32_t>(0x82000);
+    a.top_p = at<float>(0x83000);
+    a.min_p = at<float>(0x84000);
+    a.token = at<int32_t>(0x85000);
+    a.logprob = at<float>(0x86000);
+    return a;
+}
+
+template <typename F>
+static int with(F change) {
+    ws_rows r = rows();
+    ws_sample_args a = sample();
+    change(r, a);
+    return ws::validate_sample(&r, &a);
+}
+
+#define NO(...) \
+    CHECK(with([](ws_rows& r, ws_sample_args& a) { (void)r; (void)a; __VA_ARGS__; }) == WS_E_INVALID_ARG)
+#define YES(...) \
+    CHECK(with([](ws_rows& r, ws_sample_args& a) { (void)r; (void)a; __VA_ARGS__; }) == WS_OK)
+
+static void test_arguments() {
+    const ws_rows r = rows();
+    const ws_sample_args a = sample();
+    CHECK(ws::validate_sample(nullptr, &a) == WS_E_INVALID_ARG);
+    CHECK(ws::validate_sample(&r, nullptr) == WS_E_INVALID_ARG);
+    YES();
+    YES(a.temperature = nullptr; a.top_k = nullptr; a.top_p = nullptr; a.min_p = nullptr;
+        a.logprob = nullptr);
+    NO(a.logits = nullptr);
+    NO(a.uniform = nullptr);
+    NO(a.token = nullptr);
+    NO(a.logits = at<void>(0x10001));
+    YES(a.logits = at<void>(0x10002));
+    NO(a.uniform = at<float>(0x80002));
+    NO(a.temperature = at<float>(0x81002));
+    NO(a.top_k = at<int32_t>(0x82001));
+    NO(a.top_p = at<float>(0x83003));
+    NO(a.min_p = at<float>(0x84002));
+    NO(a.token = at<int32_t>(0x85002));
+    NO(a.logprob = at<float>(0x86001));
+    NO(r.temperature = 0.0f);          // the rows' own must hold, array or not
+    NO(r.rows = -1);
+    NO(r.vocab = 0);
+    NO(r.row_stride = 999);
+    YES(r.rows = 0; std::memset(&a, 0, sizeof a));
+}
+
+static void layout() {
+#define FIELD(f) std::printf("ws_sample_args " #f " %zu\n", offsetof(ws_sample_args, f))
+    std::printf("ws_sample_args sizeof %zu\n", sizeof(ws_sample_args));
+    FIELD(logits); FIELD(uniform); FIELD(temperature); FIELD(top_k); FIELD(top_p); FIELD(min_p);
+    FIELD(token); FIELD(logprob); FIELD(workspace); FIELD(workspace_bytes);
+}
+
+int main(int argc, char** argv) {
+    if (argc == 2 && !std::strcmp(argv[1], "layout")) {
+        layout();
+        return 0;
+    }
+    test_arguments();
+    std::printf("%d failures\n", failures);
+    return failures != 0;
+}
