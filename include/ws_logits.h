@@ -240,9 +240,9 @@ int ws_distill_grad(const ws_rows *rows, const ws_distill_grad_args *args, void 
  * for every row.
  *
  * w and its sums are FP64 (a token is a whole number: with sums in FP32 one draw
- * in a hundred from a large vocabulary would be another token), sums_A and the
- * sum it is compared with are held in steps of max(V, 2^10) 2^-62 or finer; a w
- * below e^-200 counts as 0.
+ * in a hundred from a large vocabulary would be another token), or, where tokens
+ * are counted by their values, in whole steps of V 2^-62; a w below e^-200 counts
+ * as 0.
  *
  * A row that holds a NaN or +inf has token -1 and logprob NaN, and so has one
  * whose settings lie outside their ranges (tau 0 or WS_MIN_TEMPERATURE..

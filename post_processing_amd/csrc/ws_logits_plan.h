@@ -326,16 +326,39 @@ inline DistillPlan plan_distill(const ws_rows& r, int32_t mode, bool gradient, b
     return p;
 }
 
-// ws_sample: a workgroup a row.
+// ws_sample: a workgroup a row; few long rows are read by `parts` workgroups
+// each, whose waves leave 24 bytes and their lanes' largest logits in the
+// workspace, and drawn from by a second kernel.
+constexpr int kMaxSampleParts = 32;
+constexpr int64_t kSampleSlots = 1024;   // of a part, at least
+constexpr int kStretchBytes = 24 + 64 * 4;
+
 struct SamplePlan {
     int32_t threads = 1024;
+    int32_t parts = 1;
+    int32_t chunk = 0;
+    int32_t unit = 0;
     size_t workspace = 0;
 };
 
 inline SamplePlan plan_sample(const ws_rows& r) {
     SamplePlan p;
     if (r.rows == 0) return p;
-    p.threads = slots_of(r) <= 1024 ? 256 : 1024;
+    const int64_t slots = slots_of(r);
+    p.threads = slots <= 1024 ? 256 : r.rows > 256 ? 512 : 1024;
+    if (slots > kSplitSlots) {
+        int64_t parts = kSplitGroups / r.rows;
+        if (parts > slots / kSampleSlots) parts = slots / kSampleSlots;
+        if (parts > kMaxSampleParts) parts = kMaxSampleParts;
+        if (parts > 1) p.parts = (int32_t)parts;
+    }
+    p.chunk = (int32_t)(slots / p.parts);
+    if (p.parts > 1)
+        p.workspace = (size_t)r.rows * (size_t)p.parts * 4u * (size_t)kStretchBytes;
+    // Sums of `vocab` weights of at most 1 stay at 2^62 or below.
+    int bits = 0;
+    while ((1ll << bits) < r.vocab) ++bits;
+    p.unit = 62 - bits;
     return p;
 }
 
