@@ -53,14 +53,25 @@ __global__ void __launch_bounds__(kLookupThreads) embed_kernel(EmbedParams p) {
 // Gradient.
 //
 // Tokens are sorted by a stable radix sort, a digit of kDigitBits a pass: every
-// tile counts its digits, the counts are summed, every tile puts its tokens
-// where they belong.  Then blocks of sorted rows are added, each thread its
-// columns: a token whose rows lie in one block is written at once; of a token
-// that goes over a border each block leaves a partial sum, and the block where
-// the token begins has them added in order.  So no sum depends on timing, and
-// one token that half the rows name is as many blocks' work as half the rows.
+// tile counts its digits, and from all tiles' counts puts its tokens where they
+// belong; a pass counts the next one's digits where it puts them, and up to
+// kSortTile tokens are sorted by one workgroup in LDS.  Then blocks of sorted
+// rows are added, each thread its columns: a token whose rows lie in one block is
+// written at once; of a token that goes over a border each block leaves a partial
+// sum, and the block where the token begins has them added in order.  So no sum
+// depends on timing, and one token that half the rows name is as many blocks' work
+// as half the rows.  The table's zeros are written by workgroups beside the sort's,
+// whose few workgroups wait on latency.
 
-constexpr int kSortThreads = 256;
+struct ClearParams {
+    void* table;
+    int64_t stride;
+    int32_t from, to;   // rows
+    int32_t width;
+    int32_t lanes;      // threads to a row
+    int32_t f32;
+};
+
 constexpr int kSortEach = kSortTile / kSortThreads;
 constexpr int kSortWaves = kSortThreads / 64;
 
@@ -70,12 +81,41 @@ struct SortParams {
     const uint32_t* rows_in;
     uint32_t* keys_out;
     uint32_t* rows_out;
-    uint32_t* counts;          // [tiles][kDigits]
+    uint32_t* counts;          // [tiles][kDigits] of this pass
+    uint32_t* counts_next;     // and of the next, or NULL
     int32_t n;
     int32_t vocab;
     int32_t tiles;
     int32_t shift;
+    int32_t passes;
+    ClearParams clear;         // by the workgroups behind the tiles
 };
+
+// Zeros: rows of the table, kClearRows a workgroup.
+template <typename L, int NT>
+__device__ __forceinline__ void clear_rows(const ClearParams& p, int group) {
+    using Elem = typename L::Elem;
+    constexpr int VEC = L::VEC;
+    const int lane = threadIdx.x & (p.lanes - 1), each = NT / p.lanes;
+    const int first = p.from + group * kClearRows;
+    const int end = first + kClearRows < p.to ? first + kClearRows : p.to;
+    const float v[VEC] = {};
+    for (int row = first + (int)(threadIdx.x / (uint32_t)p.lanes); row < end; row += each) {
+        Elem* to = static_cast<Elem*>(p.table) + (int64_t)row * p.stride;
+        for (int c = lane * VEC; c < p.width; c += p.lanes * VEC)
+            store_columns<L>(to, c, p.width, v);
+    }
+}
+
+__device__ __forceinline__ void clear_part(const ClearParams& p, int group) {
+    // (zeros are the same bits in FP16 and BF16)
+    if (p.f32) clear_rows<F32, kSortThreads>(p, group);
+    else clear_rows<BF16, kSortThreads>(p, group);
+}
+
+__global__ void __launch_bounds__(kSortThreads) clear_kernel(ClearParams p) {
+    clear_part(p, blockIdx.x);
+}
 
 __device__ __forceinline__ uint32_t key_of(const SortParams& p, int i) {
     if (p.shift > 0) return p.keys_in[i];
@@ -87,23 +127,31 @@ __device__ __forceinline__ uint32_t digit_of(uint32_t key, int shift) {
     return key >> shift & (kDigits - 1);
 }
 
+// The first pass's counts, and room for the others'.
 __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(SortParams p) {
+    if ((int)blockIdx.x >= p.tiles) {
+        clear_part(p.clear, blockIdx.x - p.tiles);
+        return;
+    }
     __shared__ uint32_t count[kDigits];
-    for (int d = threadIdx.x; d < kDigits; d += kSortThreads) count[d] = 0;
+    const int tid = threadIdx.x;
+    if (tid < kDigits) count[tid] = 0;
     __syncthreads();
-    const int from = blockIdx.x * kSortTile;
 #pragma unroll
     for (int i = 0; i < kSortEach; ++i) {
-        const int at = from + i * kSortThreads + (int)threadIdx.x;
-        if (at < p.n) atomicAdd(&count[digit_of(key_of(p, at), p.shift)], 1u);
+        const int at = (int)blockIdx.x * kSortTile + i * kSortThreads + tid;
+        if (at < p.n) atomicAdd(&count[digit_of(key_of(p, at), 0)], 1u);
     }
     __syncthreads();
-    for (int d = threadIdx.x; d < kDigits; d += kSortThreads)
-        p.counts[(int64_t)blockIdx.x * kDigits + d] = count[d];
+    if (tid < kDigits) {
+        uint32_t* at = p.counts + (int64_t)blockIdx.x * kDigits + tid;
+        *at = count[tid];
+        for (int pass = 1; pass < p.passes; ++pass) at[(int64_t)pass * p.tiles * kDigits] = 0;
+    }
 }
 
-// The exclusive sum across a workgroup of one value a thread.
-template <int NT>
+// The exclusive sum over the first kDigits threads of one value each, which the
+// others take part in with 0.
 __device__ __forceinline__ uint32_t sum_before(uint32_t v, uint32_t* waves) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     uint32_t upto = v;
@@ -112,21 +160,21 @@ __device__ __forceinline__ uint32_t sum_before(uint32_t v, uint32_t* waves) {
         const uint32_t other = __shfl_up(upto, d);
         if (lane >= d) upto += other;
     }
-    if (lane == 63) waves[wave] = upto;
+    if (lane == 63 && wave < kDigits / 64) waves[wave] = upto;
     __syncthreads();
     uint32_t before = upto - v;
 #pragma unroll
-    for (int i = 0; i < NT / 64; ++i) before += i < wave ? waves[i] : 0;
+    for (int i = 0; i < kDigits / 64; ++i) before += i < wave ? waves[i] : 0;
     return before;
 }
 
-// counts[tile][digit] becomes where the tile's tokens of that digit go: one
-// digit a thread.
+// Many tiles: counts[tile][digit] becomes where the tile's tokens of that digit
+// go, one digit a thread.
 __global__ void __launch_bounds__(kDigits) sort_scan_kernel(SortParams p) {
     __shared__ uint32_t waves[kDigits / 64];
     uint32_t total = 0;
     for (int t = 0; t < p.tiles; ++t) total += p.counts[(int64_t)t * kDigits + threadIdx.x];
-    uint32_t at = sum_before<kDigits>(total, waves);
+    uint32_t at = sum_before(total, waves);
     for (int t = 0; t < p.tiles; ++t) {
         uint32_t* c = p.counts + (int64_t)t * kDigits + threadIdx.x;
         const uint32_t n = *c;
@@ -135,53 +183,148 @@ __global__ void __launch_bounds__(kDigits) sort_scan_kernel(SortParams p) {
     }
 }
 
-__global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortParams p) {
-    __shared__ uint32_t next[kSortWaves][kDigits];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    for (int i = tid; i < kSortWaves * kDigits; i += kSortThreads) (&next[0][0])[i] = 0;
+struct SortTile {
+    uint32_t next[kSortWaves][kDigits];
+    uint32_t waves[kDigits / 64];
+};
+
+// Ranks of a tile's tokens among those of their digit in their wave, whose
+// counts are left in next[wave].  A wave has 64 * kSortEach neighbouring tokens,
+// 64 at a time: lanes of the same digit find each other bit by bit, so equal digits
+// keep their order.
+__device__ __forceinline__ void rank_tile(const uint32_t (&key)[kSortEach], int first, int n,
+                                          int shift, SortTile& t, uint32_t (&rank)[kSortEach]) {
+    const int tid = threadIdx.x, wave = tid >> 6;
+    for (int i = tid; i < kSortWaves * kDigits; i += kSortThreads) (&t.next[0][0])[i] = 0;
     __syncthreads();
-    // A wave takes 64 neighbouring tokens at a time: lanes of the same digit
-    // find each other bit by bit, so equal digits keep their order.
-    const int from = blockIdx.x * kSortTile + wave * (kSortTile / kSortWaves) + lane;
-    uint32_t key[kSortEach], rank[kSortEach];
 #pragma unroll
     for (int i = 0; i < kSortEach; ++i) {
-        const int at = from + i * 64;
-        key[i] = at < p.n ? key_of(p, at) : 0;
-    }
-#pragma unroll
-    for (int i = 0; i < kSortEach; ++i) {
-        const uint32_t d = digit_of(key[i], p.shift);
-        uint64_t same = __ballot(from + i * 64 < p.n);
+        const uint32_t d = digit_of(key[i], shift);
+        const bool there = first + i * 64 < n;
+        uint64_t same = __ballot(there);
 #pragma unroll
         for (int b = 0; b < kDigitBits; ++b) {
             const uint64_t set = __ballot(d >> b & 1u);
             same &= d >> b & 1u ? set : ~set;
         }
         const int before = lanes_below(same);
-        rank[i] = next[wave][d] + (uint32_t)before;
+        rank[i] = t.next[wave][d] + (uint32_t)before;
         wave_lds_sync();
-        if (from + i * 64 < p.n && before == 0) next[wave][d] += (uint32_t)__popcll(same);
+        if (there && before == 0) t.next[wave][d] += (uint32_t)__popcll(same);
         wave_lds_sync();
     }
     __syncthreads();
-    for (int d = tid; d < kDigits; d += kSortThreads) {
-        uint32_t at = p.counts[(int64_t)blockIdx.x * kDigits + d];
+}
+
+// next[wave][digit] from counts to places, the tile's tokens of a digit going to
+// `at` and behind: one digit a thread.
+__device__ __forceinline__ void place_tile(SortTile& t, uint32_t at) {
+    const int d = threadIdx.x;
+    if (d < kDigits) {
 #pragma unroll
         for (int w = 0; w < kSortWaves; ++w) {
-            const uint32_t n = next[w][d];
-            next[w][d] = at;
+            const uint32_t n = t.next[w][d];
+            t.next[w][d] = at;
             at += n;
         }
     }
     __syncthreads();
+}
+
+__global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortParams p) {
+    if ((int)blockIdx.x >= p.tiles) {
+        clear_part(p.clear, blockIdx.x - p.tiles);
+        return;
+    }
+    __shared__ SortTile tile;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int first = (int)blockIdx.x * kSortTile + wave * 64 * kSortEach + lane;
+    uint32_t key[kSortEach], row[kSortEach], rank[kSortEach];
 #pragma unroll
     for (int i = 0; i < kSortEach; ++i) {
-        const int at = from + i * 64;
-        if (at >= p.n) continue;
-        const uint32_t to = next[wave][digit_of(key[i], p.shift)] + rank[i];
+        const int at = first + i * 64 < p.n ? first + i * 64 : p.n - 1;
+        key[i] = key_of(p, at);
+        row[i] = p.shift > 0 ? p.rows_in[at] : (uint32_t)at;
+    }
+    // Where the tile's tokens of a digit go.
+    uint32_t at = 0;
+    const bool scanned = p.tiles > kScanTiles;
+    if (tid < kDigits) {
+        if (scanned) {
+            at = p.counts[(int64_t)blockIdx.x * kDigits + tid];
+        } else {
+            uint32_t total = 0;
+#pragma unroll 8
+            for (int t = 0; t < p.tiles; ++t) {
+                const uint32_t c = p.counts[t * kDigits + tid];
+                total += c;
+                at += t < (int)blockIdx.x ? c : 0;
+            }
+            rank[0] = total;
+        }
+    }
+    if (!scanned) at += sum_before(tid < kDigits ? rank[0] : 0, tile.waves);
+    rank_tile(key, first, p.n, p.shift, tile, rank);
+    place_tile(tile, at);
+#pragma unroll
+    for (int i = 0; i < kSortEach; ++i) {
+        if (first + i * 64 >= p.n) continue;
+        const uint32_t to = tile.next[wave][digit_of(key[i], p.shift)] + rank[i];
         p.keys_out[to] = key[i];
-        p.rows_out[to] = p.shift > 0 ? p.rows_in[at] : (uint32_t)at;
+        p.rows_out[to] = row[i];
+        if (p.counts_next)
+            atomicAdd(&p.counts_next[(int64_t)(to / kSortTile) * kDigits +
+                                     digit_of(key[i], p.shift + kDigitBits)], 1u);
+    }
+}
+
+// All passes over at most kSortTile tokens.
+__global__ void __launch_bounds__(kSortThreads) sort_few_kernel(SortParams p) {
+    if (blockIdx.x >= 1) {
+        clear_part(p.clear, blockIdx.x - 1);
+        return;
+    }
+    __shared__ SortTile tile;
+    __shared__ uint32_t keys[kSortTile], rows[kSortTile];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int first = wave * 64 * kSortEach + lane;
+    uint32_t key[kSortEach], row[kSortEach], rank[kSortEach];
+#pragma unroll
+    for (int i = 0; i < kSortEach; ++i) {
+        const int at = first + i * 64 < p.n ? first + i * 64 : p.n - 1;
+        row[i] = (uint32_t)at;
+        key[i] = key_of(p, at);
+    }
+    for (int pass = 0; pass < p.passes; ++pass) {
+        const int shift = pass * kDigitBits;
+        rank_tile(key, first, p.n, shift, tile, rank);
+        uint32_t total = 0;
+        if (tid < kDigits) {
+#pragma unroll
+            for (int w = 0; w < kSortWaves; ++w) total += tile.next[w][tid];
+        }
+        place_tile(tile, sum_before(total, tile.waves));
+#pragma unroll
+        for (int i = 0; i < kSortEach; ++i) {
+            if (first + i * 64 >= p.n) continue;
+            const uint32_t to = tile.next[wave][digit_of(key[i], shift)] + rank[i];
+            keys[to] = key[i];
+            rows[to] = row[i];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kSortEach; ++i) {
+            const int at = first + i * 64 < p.n ? first + i * 64 : p.n - 1;
+            key[i] = keys[at];
+            row[i] = rows[at];
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < kSortEach; ++i) {
+        if (first + i * 64 >= p.n) continue;
+        p.keys_out[first + i * 64] = key[i];
+        p.rows_out[first + i * 64] = row[i];
     }
 }
 
@@ -219,40 +362,60 @@ __device__ __forceinline__ void write_sum(const SumParams& p, uint32_t key, int 
     store_either<L>(at, p.grad_f32, c, p.width, sum);
 }
 
-// The rows of one block of the sorted tokens.
+// The rows of one block of the sorted tokens, kSumAhead at a time on their way.
+constexpr int kSumAhead = 8;
+
 template <typename L>
 __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(SumParams p) {
     using Elem = typename L::Elem;
-    constexpr int VEC = L::VEC;
+    constexpr int VEC = L::VEC, U = kSumAhead;
+    __shared__ uint32_t keys[kMostRows + 2], rows[kMostRows];
     const int tile = blockIdx.x % (uint32_t)p.columns;
     const int64_t block = blockIdx.x / (uint32_t)p.columns;
+    const int from = (int)block * p.block;
+    const int n = p.n - from < p.block ? p.n - from : p.block;
+    // The block's tokens, and the ones before and behind (none: no token's key).
+    for (int i = threadIdx.x; i < n + 2; i += kSumThreads) {
+        const int at = from + i - 1;
+        keys[i] = at >= 0 && at < p.n ? p.keys[at] : 0xffffffffu;
+        if (i < n) rows[i] = p.rows[from + i];
+    }
+    __syncthreads();
     const int c = (tile * kSumThreads + (int)threadIdx.x) * VEC;
     if (c >= p.width) return;
-    const int from = (int)block * p.block;
-    const int to = p.n - from < p.block ? p.n : from + p.block;
     float sum[VEC];
 #pragma unroll
     for (int j = 0; j < VEC; ++j) sum[j] = 0.0f;
-    bool began = from > 0 && p.keys[from - 1] == p.keys[from];   // in an earlier block
-    for (int i = from; i < to; ++i) {
-        const uint32_t key = p.keys[i];
-        if (key >= (uint32_t)p.vocab) return;   // no token: all behind are
-        float v[VEC];
-        const Elem* row = static_cast<const Elem*>(p.grad_out) + (int64_t)p.rows[i] * p.stride;
-        L::unpack(load_columns<L>(row, c, p.width), v);
+    bool began = keys[0] == keys[1];   // in an earlier block
+    const Elem* grad = static_cast<const Elem*>(p.grad_out);
+    for (int base = 0; base < n; base += U) {
+        uint4 w[U];
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) sum[j] += v[j];
-        const bool last = i + 1 == p.n || p.keys[i + 1] != key;
-        if (!last && i + 1 < to) continue;
-        if (last && !began) {
-            write_sum<L>(p, key, c, sum);
-        } else {
-            float* out = p.partial + (block * 2 + (began ? 0 : 1)) * p.partial_stride;
-            store_either<L>(out, true, c, p.width, sum);
+        for (int i = 0; i < U; ++i) {
+            const int at = base + i < n ? base + i : n - 1;
+            w[i] = load_columns<L>(grad + (int64_t)rows[at] * p.stride, c, p.width);
         }
-        began = false;
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) sum[j] = 0.0f;
+        for (int i = 0; i < U; ++i) {
+            if (base + i >= n) return;
+            const uint32_t key = __builtin_amdgcn_readfirstlane(keys[base + i + 1]);
+            if (key >= (uint32_t)p.vocab) return;   // no token: all behind are
+            float v[VEC];
+            L::unpack(w[i], v);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) sum[j] += v[j];
+            const bool last = __builtin_amdgcn_readfirstlane(keys[base + i + 2]) != key;
+            if (!last && base + i + 1 < n) continue;
+            if (last && !began) {
+                write_sum<L>(p, key, c, sum);
+            } else {
+                float* out = p.partial + (block * 2 + (began ? 0 : 1)) * p.partial_stride;
+                store_either<L>(out, true, c, p.width, sum);
+            }
+            began = false;
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) sum[j] = 0.0f;
+        }
     }
 }
 
@@ -272,37 +435,26 @@ __global__ void __launch_bounds__(kSumThreads) embed_join_kernel(SumParams p) {
     if (c >= p.width) return;
     float sum[VEC];
     load_either<L>(p.partial + (block * 2 + 1) * p.partial_stride, true, c, p.width, sum);
-    for (int64_t b = block + 1; b < p.blocks; ++b) {
-        const int first = (int)b * p.block;
-        if (p.keys[first] != key) break;
-        float v[VEC];
-        load_either<L>(p.partial + b * 2 * p.partial_stride, true, c, p.width, v);
+    constexpr int U = 4;
+    for (int64_t b = block + 1; b < p.blocks; b += U) {
+        uint32_t found[U];
+        float v[U][VEC];
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) sum[j] += v[j];
+        for (int i = 0; i < U; ++i) {
+            const int64_t at = b + i < p.blocks ? b + i : b;
+            found[i] = p.keys[at * p.block];
+            load_either<L>(p.partial + at * 2 * p.partial_stride, true, c, p.width, v[i]);
+        }
+        bool over = false;
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            over = over || b + i >= p.blocks || found[i] != key;
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) sum[j] += over ? 0.0f : v[i][j];
+        }
+        if (over) break;
     }
     write_sum<L>(p, key, c, sum);
-}
-
-struct ClearParams {
-    void* grad_table;
-    int64_t grad_stride;
-    int32_t vocab;
-    int32_t width;
-    int32_t lanes;
-};
-
-// Zeros, as embed_kernel lays its rows over a workgroup.
-template <typename L>
-__global__ void __launch_bounds__(kLookupThreads) clear_kernel(ClearParams p) {
-    using Elem = typename L::Elem;
-    constexpr int VEC = L::VEC;
-    const int lane = threadIdx.x & (p.lanes - 1);
-    const int64_t row =
-        (int64_t)blockIdx.x * (kLookupThreads / p.lanes) + threadIdx.x / (uint32_t)p.lanes;
-    if (row >= p.vocab) return;
-    Elem* to = static_cast<Elem*>(p.grad_table) + row * p.grad_stride;
-    const float v[VEC] = {};
-    for (int c = lane * VEC; c < p.width; c += p.lanes * VEC) store_columns<L>(to, c, p.width, v);
 }
 
 // ---------------------------------------------------------------------------
@@ -314,23 +466,25 @@ __global__ void __launch_bounds__(kLookupThreads) clear_kernel(ClearParams p) {
         else { CALL(BF16); }                                 \
     } while (0)
 
-int clear_table(const ws_states& t, const ws_embed_grad_args& a, hipStream_t s) {
+// Rows [from, to) of the table as a kernel clears them; `groups` workgroups.
+ClearParams clear_of(const ws_states& t, const ws_embed_grad_args& a, int from, int to,
+                     int64_t* groups) {
     ws_states rows = t;
-    rows.rows = a.vocab;
     rows.dtype = a.grad_dtype;
-    const EmbedPlan plan = plan_embed(rows);
     ClearParams p{};
-    p.grad_table = a.grad_table;
-    p.grad_stride = a.grad_stride;
-    p.vocab = a.vocab;
+    p.table = a.grad_table;
+    p.stride = a.grad_stride;
+    p.from = from;
+    p.to = to;
     p.width = t.width;
-    p.lanes = plan.lanes;
-#define CALL(L) return launch(clear_kernel<L>, plan.groups, kLookupThreads, p, s)
-    WS_BY_DTYPE(a.grad_dtype, CALL);
-#undef CALL
+    p.lanes = plan_embed(rows).lanes;
+    p.f32 = a.grad_dtype == WS_DTYPE_F32;
+    *groups = (to - from + kClearRows - 1) / kClearRows;
+    return p;
 }
 
-// Sorted keys and rows; returns which of the two buffers holds them.
+// Sorted keys and rows, and beside that zeros in the table; `where` becomes the
+// one of the two buffers that holds them.
 int sort_tokens(const ws_states& t, const ws_embed_grad_args& a, const EmbedGradPlan& plan,
                 hipStream_t s, int* where) {
     char* space = static_cast<char*>(a.workspace);
@@ -339,26 +493,42 @@ int sort_tokens(const ws_states& t, const ws_embed_grad_args& a, const EmbedGrad
         keys[i] = reinterpret_cast<uint32_t*>(space + plan.keys_at[i]);
         rows[i] = reinterpret_cast<uint32_t*>(space + plan.rows_at[i]);
     }
+    uint32_t* counts = reinterpret_cast<uint32_t*>(space + plan.counts_at);
     SortParams p{};
     p.ids = a.ids;
-    p.counts = reinterpret_cast<uint32_t*>(space + plan.counts_at);
+    p.keys_out = keys[0];
+    p.rows_out = rows[0];
+    p.counts = counts;
     p.n = t.rows;
     p.vocab = a.vocab;
     p.tiles = plan.tiles;
-    for (int pass = 0; pass < plan.passes; ++pass) {
+    p.passes = plan.passes;
+    const int64_t steps = plan.tiles == 1 ? 1 : 1 + plan.passes;
+    int64_t clears = 0;
+    const auto share = [&](int64_t step) {
+        if (!a.accumulate)
+            p.clear = clear_of(t, a, (int)(a.vocab * step / steps),
+                               (int)(a.vocab * (step + 1) / steps), &clears);
+    };
+    share(0);
+    *where = 0;
+    if (plan.tiles == 1) return launch(sort_few_kernel, 1 + clears, kSortThreads, p, s);
+    int v = launch(sort_count_kernel, plan.tiles + clears, kSortThreads, p, s);
+    for (int pass = 0; pass < plan.passes && v == WS_OK; ++pass) {
         const int to = pass & 1;
         p.keys_in = keys[to ^ 1];
         p.rows_in = rows[to ^ 1];
         p.keys_out = keys[to];
         p.rows_out = rows[to];
         p.shift = pass * kDigitBits;
-        int v = launch(sort_count_kernel, plan.tiles, kSortThreads, p, s);
-        if (v == WS_OK) v = launch(sort_scan_kernel, 1, kDigits, p, s);
-        if (v == WS_OK) v = launch(sort_place_kernel, plan.tiles, kSortThreads, p, s);
-        if (v != WS_OK) return v;
+        p.counts = counts + (int64_t)pass * plan.tiles * kDigits;
+        p.counts_next = pass + 1 < plan.passes ? p.counts + (int64_t)plan.tiles * kDigits : nullptr;
+        share(pass + 1);
+        if (plan.tiles > kScanTiles) v = launch(sort_scan_kernel, 1, kDigits, p, s);
+        if (v == WS_OK) v = launch(sort_place_kernel, plan.tiles + clears, kSortThreads, p, s);
         *where = to;
     }
-    return WS_OK;
+    return v;
 }
 
 template <typename L>
@@ -417,9 +587,10 @@ extern "C" int ws_embed_grad(const ws_states* states, const ws_embed_grad_args* 
     v = ws::device_ready(states->device);
     if (v != WS_OK) return v;
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    if (!args->accumulate) {
-        v = ws::clear_table(*states, *args, s);
-        if (v != WS_OK || states->rows == 0) return v;
+    if (states->rows == 0) {
+        int64_t groups = 0;
+        const ws::ClearParams p = ws::clear_of(*states, *args, 0, args->vocab, &groups);
+        return ws::launch(ws::clear_kernel, groups, ws::kSortThreads, p, s);
     }
     int where = 0;
     v = ws::sort_tokens(*states, *args, plan, s, &where);

@@ -20,14 +20,89 @@ struct NormParams {
     void* y;
     ws_norm_stats* stats;
     int64_t x_stride, y_stride;
+    int32_t rows;
     int32_t width;
     int32_t weight_f32;
     float inv_width;
     float eps;
 };
 
-// One row a workgroup, read again for each of its three passes: the mean, the
-// deviations from it, the result.
+// A row's mean and deviation from its slots in registers: the deviations' own
+// sum takes back the mean's rounding, which a row far from 0 would otherwise carry
+// into its variance and its result.
+//
+// Rows up to a few thousand elements: the next row is on its way while one is
+// worked on, weights stay in registers where there is room, and each element is
+// read and written once.
+template <typename L, int NT, int R>
+__global__ void __launch_bounds__(NT) norm_kernel(NormParams p) {
+    using Elem = typename L::Elem;
+    constexpr int VEC = L::VEC;
+    constexpr bool kHold = R * VEC <= 16;
+    __shared__ float first[NT / 64];
+    __shared__ float2 second[NT / 64];
+    const HeldSlots<L, NT, R> slots(p.width);
+    const Elem* x = static_cast<const Elem*>(p.x);
+    Elem* y = static_cast<Elem*>(p.y);
+    float g[kHold ? R : 1][VEC], b[kHold ? R : 1][VEC];
+    if constexpr (kHold) {
+        slots.weights(p.weight, p.weight_f32, 1.0f, g);
+        slots.weights(p.bias, p.weight_f32, 0.0f, b);
+    }
+    uint4 w[R];
+    slots.load(x + (int64_t)blockIdx.x * p.x_stride, w);
+    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+        float v[R][VEC];
+#pragma unroll
+        for (int i = 0; i < R; ++i) L::unpack(w[i], v[i]);
+        const int64_t next = row + gridDim.x;
+        slots.load(x + (next < p.rows ? next : row) * p.x_stride, w);
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) sum += slots.mine(i, j) ? v[i][j] : 0.0f;
+        const float mean = group_sum<NT>(sum, first) * p.inv_width;
+        float2 far = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                v[i][j] -= mean;
+                const float d = slots.mine(i, j) ? v[i][j] : 0.0f;
+                far.x += d;
+                far.y = fmaf(d, d, far.y);
+            }
+        far = group_sums<NT>(far, second);
+        const float shift = far.x * p.inv_width;
+        const float var = fmaxf(far.y * p.inv_width - shift * shift, 0.0f);
+        const float inverse = 1.0f / sqrtf(var + p.eps);
+        if (p.stats && threadIdx.x == 0) p.stats[row] = {mean + shift, inverse};
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            if (!slots.any(i)) continue;
+            if constexpr (kHold) {
+#pragma unroll
+                for (int j = 0; j < VEC; ++j)
+                    v[i][j] = fmaf((v[i][j] - shift) * inverse, g[i][j], b[i][j]);
+            } else {
+                float gi[VEC], bi[VEC];
+                if (p.weight) load_either<L>(p.weight, p.weight_f32, slots.at[i], p.width, gi);
+                if (p.bias) load_either<L>(p.bias, p.weight_f32, slots.at[i], p.width, bi);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    v[i][j] = (v[i][j] - shift) * inverse;
+                    if (p.weight) v[i][j] *= gi[j];
+                    if (p.bias) v[i][j] += bi[j];
+                }
+            }
+            store_loose<L>(y + row * p.y_stride + slots.at[i], L::pack(v[i]));
+        }
+    }
+}
+
+// Longer rows, and those of less than a slot: one a workgroup, read again for
+// each of its three passes.
 template <typename L, int NT>
 __global__ void __launch_bounds__(NT) norm_long_kernel(NormParams p) {
     using Elem = typename L::Elem;
@@ -46,8 +121,6 @@ __global__ void __launch_bounds__(NT) norm_long_kernel(NormParams p) {
         for (int j = 0; j < VEC; ++j) sum += v[j];
     }
     float mean = group_sum<NT>(sum, waves[0]) * p.inv_width;
-    // The deviations' own sum takes back the mean's rounding, which a row far
-    // from 0 would otherwise carry into its variance and its result.
     float left = 0.0f, square = 0.0f;
     for (int c = first; c < p.width; c += NT * VEC) {
         float v[VEC];
@@ -97,7 +170,84 @@ struct NormGradParams {
     float inv_width;
 };
 
-// The gradient of one row a workgroup, in two passes over it.
+// Rows held as norm_kernel's: grad_x, and in registers the workgroup's rows'
+// sums for the weight's and the bias's gradient, which it leaves in the workspace.
+// SUMS: with those.
+template <typename L, int NT, int R, bool SUMS>
+__global__ void __launch_bounds__(NT) norm_grad_kernel(NormGradParams p) {
+    using Elem = typename L::Elem;
+    constexpr int VEC = L::VEC;
+    __shared__ float2 waves[2][NT / 64];
+    const HeldSlots<L, NT, R> slots(p.width);
+    const Elem* x = static_cast<const Elem*>(p.x);
+    const Elem* gy = static_cast<const Elem*>(p.grad_y);
+    float g[R][VEC], gw[SUMS ? R : 1][VEC], gb[SUMS ? R : 1][VEC];
+    slots.weights(p.weight, p.weight_f32, 1.0f, g);
+    if constexpr (SUMS) {
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) gw[i][j] = gb[i][j] = 0.0f;
+    }
+    uint4 wx[R], wy[R];
+    slots.load(x + (int64_t)blockIdx.x * p.x_stride, wx);
+    slots.load(gy + (int64_t)blockIdx.x * p.y_stride, wy);
+    ws_norm_stats ahead = p.stats[blockIdx.x];
+    int turn = 0;
+    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+        float u[R][VEC], d[R][VEC];
+        const ws_norm_stats s = ahead;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            L::unpack(wx[i], u[i]);
+            L::unpack(wy[i], d[i]);
+        }
+        int64_t next = row + gridDim.x;
+        next = next < p.rows ? next : row;
+        slots.load(x + next * p.x_stride, wx);
+        slots.load(gy + next * p.y_stride, wy);
+        ahead = p.stats[next];
+        float2 sums = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                u[i][j] = (u[i][j] - s.mean) * s.inverse;
+                if constexpr (SUMS) {
+                    gw[i][j] = fmaf(d[i][j], u[i][j], gw[i][j]);
+                    gb[i][j] += d[i][j];
+                }
+                d[i][j] *= g[i][j];
+                const float m = slots.mine(i, j) ? d[i][j] : 0.0f;
+                sums.x += m;
+                sums.y += slots.mine(i, j) ? m * u[i][j] : 0.0f;
+            }
+        if (!p.grad_x) continue;
+        sums = group_sums<NT>(sums, waves[turn]);
+        turn ^= 1;
+        const float level = sums.x * p.inv_width, along = sums.y * p.inv_width;
+        Elem* gx = static_cast<Elem*>(p.grad_x) + row * p.grad_stride;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            if (!slots.any(i)) continue;
+#pragma unroll
+            for (int j = 0; j < VEC; ++j)
+                d[i][j] = s.inverse * (d[i][j] - level - u[i][j] * along);
+            store_loose<L>(gx + slots.at[i], L::pack(d[i]));
+        }
+    }
+    if constexpr (SUMS) {
+        float* out = p.partial + (int64_t)blockIdx.x * 2 * p.partial_stride;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            if (!slots.any(i)) continue;
+            store_either<L>(out, true, slots.at[i], p.width, gw[i]);
+            store_either<L>(out + p.partial_stride, true, slots.at[i], p.width, gb[i]);
+        }
+    }
+}
+
+// The gradient of one longer row a workgroup, in two passes over it.
 template <typename L, int NT>
 __global__ void __launch_bounds__(NT) norm_grad_long_kernel(NormGradParams p) {
     using Elem = typename L::Elem;
@@ -171,25 +321,60 @@ __global__ void __launch_bounds__(NT) norm_columns_kernel(NormGradParams p) {
     store_either<L>(out + p.partial_stride, true, c, p.width, gb);
 }
 
-// The groups' sums of a column, one column a thread.
+// The groups' sums of a column: 64 columns a workgroup, whose 64 shares of
+// sixteen lanes take the groups in turn, four columns a lane.
+constexpr int kJoinThreads = 1024, kJoinColumns = 64, kJoinShares = kJoinThreads / 16;
+
+__device__ __forceinline__ float4 add4(float4 a, float4 b) {
+    return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+}
+
+template <int J>
+__device__ __forceinline__ float4 xor_lane4(float4 v, int lane) {
+    return make_float4(xor_lane_f<J>(v.x, lane), xor_lane_f<J>(v.y, lane),
+                       xor_lane_f<J>(v.z, lane), xor_lane_f<J>(v.w, lane));
+}
+
 template <typename L>
-__global__ void __launch_bounds__(kNormThreads) norm_join_kernel(NormGradParams p) {
-    const int c = blockIdx.x * kNormThreads + (int)threadIdx.x;
-    if (c >= p.width) return;
-    float gw = 0.0f, gb = 0.0f;
-    for (int g = 0; g < p.groups; ++g) {
-        const float* in = p.partial + (int64_t)g * 2 * p.partial_stride + c;
-        gw += in[0];
-        gb += in[p.partial_stride];
+__global__ void __launch_bounds__(kJoinThreads) norm_join_kernel(NormGradParams p) {
+    constexpr int U = 8;   // loads in flight
+    __shared__ float4 part[kJoinThreads / 64][16];
+    const int lane = threadIdx.x % 16u, share = threadIdx.x / 16u;
+    const int tiles = (p.width + kJoinColumns - 1) / kJoinColumns;
+    const bool bias = (int)blockIdx.x >= tiles;
+    const int c = ((int)blockIdx.x - (bias ? tiles : 0)) * kJoinColumns + lane * 4;
+    const float* in = p.partial + (bias ? p.partial_stride : 0) + c;
+    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (c < p.width) {   // a row of the workspace is whole in fours
+        for (int from = share; from < p.groups; from += U * kJoinShares) {
+            float4 v[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int g = from + i * kJoinShares < p.groups ? from + i * kJoinShares : from;
+                v[i] = *reinterpret_cast<const float4*>(in + (int64_t)g * 2 * p.partial_stride);
+            }
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+                if (from + i * kJoinShares < p.groups) sum = add4(sum, v[i]);
+        }
     }
-    if (p.grad_weight) {
-        if (p.weight_f32) static_cast<float*>(p.grad_weight)[c] = gw;
-        else static_cast<typename L::Elem*>(p.grad_weight)[c] = L::down(gw);
-    }
-    if (p.grad_bias) {
-        if (p.weight_f32) static_cast<float*>(p.grad_bias)[c] = gb;
-        else static_cast<typename L::Elem*>(p.grad_bias)[c] = L::down(gb);
-    }
+    sum = add4(sum, xor_lane4<16>(sum, threadIdx.x & 63));
+    sum = add4(sum, xor_lane4<32>(sum, threadIdx.x & 63));
+    if ((threadIdx.x & 63) < 16) part[threadIdx.x >> 6][lane] = sum;
+    __syncthreads();
+    if (share != 0) return;
+    sum = part[0][lane];
+#pragma unroll
+    for (int i = 1; i < kJoinThreads / 64; ++i) sum = add4(sum, part[i][lane]);
+    void* out = bias ? p.grad_bias : p.grad_weight;
+    if (!out) return;
+    const float v[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (c + j < p.width) {
+            if (p.weight_f32) static_cast<float*>(out)[c + j] = v[j];
+            else static_cast<typename L::Elem*>(out)[c + j] = L::down(v[j]);
+        }
 }
 
 // ---------------------------------------------------------------------------
@@ -203,23 +388,52 @@ __global__ void __launch_bounds__(kNormThreads) norm_join_kernel(NormGradParams 
 
 template <typename L>
 int run_norm(const ws_states& t, const NormParams& p, hipStream_t s) {
+    const NormPlan plan = plan_layernorm(t);
+#define PICK(NT, R) \
+    if (plan.threads == NT && plan.held == R) return launch(norm_kernel<L, NT, R>, plan.groups, NT, p, s)
+    PICK(64, 1);
+    PICK(64, 2);
+    PICK(256, 1);
+    PICK(256, 2);
+    PICK(512, 2);
+    PICK(1024, 2);
+    PICK(1024, 4);
+#undef PICK
     return launch(norm_long_kernel<L, kNormThreads>, t.rows, kNormThreads, p, s);
+}
+
+template <typename L, bool SUMS>
+int run_norm_grad_held(const NormGradPlan& plan, const NormGradParams& p, hipStream_t s) {
+#define PICK(NT, R)                                  \
+    if (plan.threads == NT && plan.held == R)        \
+    return launch(norm_grad_kernel<L, NT, R, SUMS>, plan.groups, NT, p, s)
+    PICK(64, 1);
+    PICK(64, 2);
+    PICK(256, 1);
+    PICK(256, 2);
+    PICK(512, 2);
+#undef PICK
+    return launch(norm_grad_kernel<L, 1024, 2, SUMS>, plan.groups, 1024, p, s);
 }
 
 template <typename L>
 int run_norm_grad(const ws_states& t, const NormGradPlan& plan, const NormGradParams& p,
                   hipStream_t s) {
-    // The sums over rows first: grad_x may take the place of x or grad_y.
-    if (p.grad_weight || p.grad_bias) {
-        int v = launch(norm_columns_kernel<L, kNormThreads>, (int64_t)plan.columns * plan.groups,
+    const bool sums = p.grad_weight || p.grad_bias;
+    int v = WS_OK;
+    if (t.rows > 0 && plan.held > 0) {
+        v = sums ? run_norm_grad_held<L, true>(plan, p, s) : run_norm_grad_held<L, false>(plan, p, s);
+    } else if (t.rows > 0) {
+        // The sums over rows first: grad_x may take the place of x or grad_y.
+        if (sums)
+            v = launch(norm_columns_kernel<L, kNormThreads>, (int64_t)plan.columns * plan.groups,
                        kNormThreads, p, s);
-        if (v != WS_OK) return v;
-        v = launch(norm_join_kernel<L>, (p.width + kNormThreads - 1) / kNormThreads, kNormThreads,
-                   p, s);
-        if (v != WS_OK) return v;
+        if (v == WS_OK && p.grad_x)
+            v = launch(norm_grad_long_kernel<L, kNormThreads>, t.rows, kNormThreads, p, s);
     }
-    if (!p.grad_x || t.rows == 0) return WS_OK;
-    return launch(norm_grad_long_kernel<L, kNormThreads>, t.rows, kNormThreads, p, s);
+    if (v != WS_OK || !sums) return v;
+    return launch(norm_join_kernel<L>, 2 * ((p.width + kJoinColumns - 1) / kJoinColumns),
+                  kJoinThreads, p, s);
 }
 
 }  // namespace
@@ -240,6 +454,7 @@ extern "C" int ws_layernorm(const ws_states* states, const ws_layernorm_args* ar
     p.stats = args->stats;
     p.x_stride = states->row_stride;
     p.y_stride = args->y_stride;
+    p.rows = states->rows;
     p.width = states->width;
     p.weight_f32 = args->weight_dtype == WS_DTYPE_F32;
     p.inv_width = (float)(1.0 / states->width);

@@ -115,8 +115,26 @@ __device__ __forceinline__ void store_either(void* row, bool f32, int c, int wid
     }
 }
 
-// The sum over a workgroup, in every thread.  `waves` (LDS) must not be
-// written again before every thread has read it: two sums in turn take two.
+// The sums of two values over a workgroup, in every thread.  `waves` (LDS) must
+// not be written again before every thread has read it: two sums in turn take two.
+template <int NT>
+__device__ __forceinline__ float2 group_sums(float2 v, float2* waves) {
+    const int lane = threadIdx.x & 63;
+    v.x = wave_sum(v.x, lane);
+    v.y = wave_sum(v.y, lane);
+    if constexpr (NT > 64) {
+        if (lane == 0) waves[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < NT / 64; ++i) {
+            v.x += waves[i].x;
+            v.y += waves[i].y;
+        }
+    }
+    return v;
+}
+
 template <int NT>
 __device__ __forceinline__ float group_sum(float v, float* waves) {
     const int lane = threadIdx.x & 63;
@@ -130,5 +148,46 @@ __device__ __forceinline__ float group_sum(float v, float* waves) {
     }
     return v;
 }
+
+// Slots a thread holds of every row: i * NT + thread.  All are full, so that no
+// load hangs on a condition: a last slot that would end behind the row begins
+// earlier instead and has its first elements in common with the one before, and
+// threads without a slot hold the row's end too.  Needs rows of VEC elements.
+template <typename L, int NT, int R>
+struct HeldSlots {
+    static constexpr int VEC = L::VEC;
+    int at[R];      // first column
+    int own[R];     // the thread's own elements are own[i] and behind
+
+    __device__ __forceinline__ explicit HeldSlots(int width) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int c = (i * NT + (int)threadIdx.x) * VEC;
+            at[i] = c + VEC <= width ? c : width - VEC;
+            own[i] = c - at[i];
+        }
+    }
+    __device__ __forceinline__ bool mine(int i, int j) const { return j >= own[i]; }
+    // Whether the slot holds elements of its own, and so is written whole: what
+    // two threads write twice is the same.
+    __device__ __forceinline__ bool any(int i) const { return own[i] < VEC; }
+    __device__ __forceinline__ void load(const typename L::Elem* row, uint4 (&w)[R]) const {
+#pragma unroll
+        for (int i = 0; i < R; ++i) w[i] = load_loose<L>(row + at[i]);
+    }
+    // A weight's values for the slots, FP32 or L; `none` without one.
+    __device__ __forceinline__ void weights(const void* row, bool f32, float none,
+                                            float (&v)[R][VEC]) const {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            if (row) {
+                load_either<L>(row, f32, at[i], at[i] + VEC, v[i]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) v[i][j] = none;
+            }
+        }
+    }
+};
 
 }  // namespace ws

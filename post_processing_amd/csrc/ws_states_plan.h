@@ -127,9 +127,13 @@ inline EmbedPlan plan_embed(const ws_states& t) {
 }
 
 // Gradient: tokens sorted in tiles of kSortTile, one digit of kDigitBits a pass;
-// the sorted rows are added in blocks of `block` rows.
-constexpr int kSortTile = 2048, kDigitBits = 9, kDigits = 1 << kDigitBits;
-constexpr int kMostBlocks = 8192, kBlockRows = 32, kSumThreads = 256;
+// the sorted rows are added in blocks of `block` rows.  Blocks are small while
+// workgroups are few (the rows of a block come one after the other).
+constexpr int kSortThreads = 1024, kSortTile = 2048, kDigitBits = 9, kDigits = 1 << kDigitBits;
+constexpr int kScanTiles = 64;     // up to here every tile sums the counts for itself
+constexpr int kMostBlocks = 8192, kLeastRows = 8, kBlockRows = 32, kSumGroups = 512;
+constexpr int kSumThreads = 256, kMostRows = WS_MAX_ROWS / kMostBlocks;
+constexpr int kClearRows = 16;     // of the table, by one workgroup
 
 struct EmbedGradPlan {
     int32_t tiles = 0;
@@ -152,9 +156,12 @@ inline EmbedGradPlan plan_embed_grad(const ws_states& t, int32_t vocab) {
     int bits = 1;
     while ((vocab >> bits) != 0) ++bits;
     p.passes = (bits + kDigitBits - 1) / kDigitBits;
-    if (n > (int64_t)p.block * kMostBlocks) p.block = (int32_t)((n + kMostBlocks - 1) / kMostBlocks);
-    p.blocks = (int32_t)((n + p.block - 1) / p.block);
     p.columns = (int32_t)((slots_in(t.width, t.dtype) + kSumThreads - 1) / kSumThreads);
+    int64_t block = n * p.columns / kSumGroups;
+    block = block < kLeastRows ? kLeastRows : block > kBlockRows ? kBlockRows : block;
+    if (n > block * kMostBlocks) block = (n + kMostBlocks - 1) / kMostBlocks;
+    p.block = (int32_t)block;
+    p.blocks = (int32_t)((n + block - 1) / block);
     const size_t each = round16((size_t)n * 4);
     size_t at = 0;
     for (int i = 0; i < 2; ++i) {
@@ -163,7 +170,7 @@ inline EmbedGradPlan plan_embed_grad(const ws_states& t, int32_t vocab) {
         at += 2 * each;
     }
     p.counts_at = at;
-    at += (size_t)p.tiles * kDigits * 4;
+    if (p.tiles > 1) at += (size_t)p.passes * p.tiles * kDigits * 4;
     // Two rows of FP32 sums a block: of the token that began before it, and of
     // the one that goes on behind it.
     p.partial_at = at;
@@ -232,24 +239,59 @@ inline int validate_layernorm_grad(const ws_states* t, const ws_layernorm_grad_a
 
 constexpr int kNormThreads = 256;
 
+// Rows held in registers: `held` slots by each of `threads` threads, `groups`
+// workgroups that take rows in turn.  0: rows that do not fit, or have no slot.
+struct NormPlan {
+    int32_t threads = kNormThreads;
+    int32_t held = 0;
+    int32_t groups = 0;
+};
+
+// Waves a CU has at work at a time, four or more to a SIMD.
+constexpr int64_t kNormWaves = 256 * 16;
+
+inline NormPlan plan_held(const ws_states& t, int64_t most) {
+    NormPlan p;
+    const int64_t slots = slots_in(t.width, t.dtype);
+    if (slots > most || t.width < 16 / logit_bytes(t.dtype)) return p;
+    p.threads = slots <= 128 ? 64 : slots <= 512 ? 256 : slots <= 1024 ? 512 : 1024;
+    p.held = slots <= p.threads ? 1 : slots <= 2 * p.threads ? 2 : 4;
+    if (p.threads >= 512 && p.held < 2) p.held = 2;
+    const int64_t groups = kNormWaves / (p.threads / 64);
+    p.groups = (int32_t)(t.rows < groups ? t.rows : groups);
+    return p;
+}
+
+inline NormPlan plan_layernorm(const ws_states& t) { return plan_held(t, 4096); }
+
 // Sums over the rows: `groups` workgroups' sums of every column, then their sum.
 constexpr int64_t kColumnGroups = 512;
 
 struct NormGradPlan {
-    int32_t columns = 1;   // workgroups over the columns
+    int32_t threads = kNormThreads;
+    int32_t held = 0;
+    int32_t columns = 1;   // of rows that are not held: workgroups over the columns
     int32_t groups = 1;    // over the rows
     size_t workspace = 0;
 };
 
 inline NormGradPlan plan_layernorm_grad(const ws_states& t) {
     NormGradPlan p;
-    p.columns = (int32_t)((slots_in(t.width, t.dtype) + kNormThreads - 1) / kNormThreads);
-    int64_t groups = kColumnGroups / p.columns;
-    const int64_t most = (t.rows + 7) / 8;
-    if (groups > most) groups = most;
-    if (groups < 1) groups = 1;
-    p.groups = (int32_t)groups;
-    p.workspace = (size_t)groups * 2 * round16((size_t)t.width * 4);
+    const NormPlan held = plan_held(t, 2048);
+    p.threads = held.threads;
+    p.held = held.held;
+    if (t.rows == 0) {
+        p.groups = 0;
+    } else if (p.held > 0) {
+        p.groups = held.groups < kColumnGroups ? held.groups : (int32_t)kColumnGroups;
+    } else {
+        p.columns = (int32_t)((slots_in(t.width, t.dtype) + kNormThreads - 1) / kNormThreads);
+        int64_t groups = kColumnGroups / p.columns;
+        const int64_t most = (t.rows + 7) / 8;
+        if (groups > most) groups = most;
+        p.groups = (int32_t)(groups < 1 ? 1 : groups);
+    }
+    p.workspace = (size_t)p.groups * 2 * round16((size_t)t.width * 4);
     return p;
 }
 
