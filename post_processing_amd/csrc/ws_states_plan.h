@@ -170,7 +170,7 @@ inline EmbedGradPlan plan_embed_grad(const ws_states& t, int32_t vocab) {
         at += 2 * each;
     }
     p.counts_at = at;
-    if (p.tiles > 1) at += (size_t)p.passes * p.tiles * kDigits * 4;
+    if (p.tiles > 1) at += (size_t)p.tiles * kDigits * 4;
     // Two rows of FP32 sums a block: of the token that began before it, and of
     // the one that goes on behind it.
     p.partial_at = at;
