@@ -144,14 +144,15 @@ typedef struct ws_layernorm_grad_args {
     void                *grad_weight;     /* [width] of weight_dtype, or NULL */
     void                *grad_bias;       /* [width] of weight_dtype, or NULL */
     void                *workspace;       /* ws_layernorm_grad_workspace
-                                             bytes, 16-byte aligned           */
+                                             bytes, 16-byte aligned; NULL
+                                             without both                     */
     size_t               workspace_bytes;
     int32_t              weight_dtype;    /* states->dtype or WS_DTYPE_F32    */
     int32_t              reserved;        /* must be 0                        */
 } ws_layernorm_grad_args;
 
-/* Workspace bytes of ws_layernorm_grad for these rows (0 when neither the
- * weight's nor the bias's gradient is asked for). */
+/* Workspace bytes of ws_layernorm_grad for these rows, with the weight's or the
+ * bias's gradient (without both it needs none). */
 int ws_layernorm_grad_workspace(const ws_states *states, size_t *bytes);
 
 int ws_layernorm_grad(const ws_states *states, const ws_layernorm_grad_args *args, void *stream);

@@ -331,6 +331,8 @@ inline DistillPlan plan_distill(const ws_rows& r, int32_t mode, bool gradient, b
 // workspace, and drawn from by a second kernel.
 constexpr int kMaxSampleParts = 32;
 constexpr int64_t kSampleSlots = 1024;   // of a part, at least
+constexpr int64_t kSampleShort = 1024;   // slots of a row up to which 256 threads do
+constexpr int kSampleGroups = 256;       // workgroups of 1,024 threads at work at a time
 constexpr int kStretchBytes = 24 + 64 * 4;
 
 struct SamplePlan {
@@ -345,7 +347,9 @@ inline SamplePlan plan_sample(const ws_rows& r) {
     SamplePlan p;
     if (r.rows == 0) return p;
     const int64_t slots = slots_of(r);
-    p.threads = slots <= 1024 ? 256 : r.rows > 256 ? 512 : 1024;
+    p.threads = slots <= kSampleShort                                           ? 256
+                : r.rows > kSampleGroups && r.rows <= 2 * kSampleGroups ? 512
+                                                                        : 1024;
     if (slots > kSplitSlots) {
         int64_t parts = kSplitGroups / r.rows;
         if (parts > slots / kSampleSlots) parts = slots / kSampleSlots;

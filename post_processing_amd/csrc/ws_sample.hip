@@ -44,6 +44,7 @@ struct SampleParams {
     int32_t* token;
     float* logprob;
     char* space;        // of split rows: [rows] of kStretchBytes * stretches
+    int32_t rows;
     int32_t vocab;
     int32_t chunk;      // slots of a part
     int32_t parts;
@@ -91,16 +92,16 @@ __device__ __forceinline__ void fill_table(double* table, int threads) {
         table[i] = small_exp((double)i * (0.6931471805599453 / kTable));
 }
 
-// e^x for x between -700 and 100 to 2e-13 relative: x = (n + r) log 2 / 256, 2 to
-// the n / 256 from a table (LDS) and a shift of its exponent, and the series of
-// what is left (at most 1.4e-3) to the third power.  Eighteen instructions with
+constexpr double kScale = 369.3299304675746;     // 256 / log 2
+
+// e^(t / kScale) for t between -700 and 100 times kScale, to 2e-13 relative: t = n +
+// r, 2 to the n / 256 from a table (LDS) and a shift of its exponent, and the series
+// of what is left (at most 1.4e-3) to the third power.  Sixteen instructions with
 // the sum, half of the exponential the library has in FP64; the draw's borders
 // between tokens lie 1e-6 apart and more.
-__device__ __forceinline__ double table_exp(double x, const double* table) {
-    constexpr double kScale = 369.3299304675746;     // 256 / log 2
+__device__ __forceinline__ double table_exp_scaled(double t, const double* table) {
     constexpr double kMagic = 6755399441055744.0;    // 1.5 x 2^52: adds to an integer
     constexpr double a1 = 0.0027076061740622863;     // log 2 / 256
-    const double t = x * kScale;
     const double y = t + kMagic;
     const int n = (int)(uint32_t)__builtin_bit_cast(uint64_t, y);
     const double r = t - (y - kMagic);
@@ -109,6 +110,10 @@ __device__ __forceinline__ double table_exp(double x, const double* table) {
     const uint32_t hi = (uint32_t)(w >> 32) + ((uint32_t)(n & ~(kTable - 1)) << 12);
     const double s = __builtin_bit_cast(double, ((uint64_t)hi << 32) | (uint32_t)w);
     return fma(s, q, s);
+}
+
+__device__ __forceinline__ double table_exp(double x, const double* table) {
+    return table_exp_scaled(x * kScale, table);
 }
 
 // ---- stretches -----------------------------------------------------------------
@@ -244,6 +249,7 @@ __device__ __forceinline__ Stretch scan_stretch(const Part<L>& row, int from, in
     s.ref = -INFINITY;
     float top = -INFINITY;
     double ref = 0.0;
+    const double steepness = inv_tau * kScale;
     // A logit 60 exponents above the reference makes it the new one.
     float limit = -INFINITY;
     const float reach = (float)(60.0 / inv_tau);
@@ -268,7 +274,8 @@ __device__ __forceinline__ Stretch scan_stretch(const Part<L>& row, int from, in
             for (int i = 0; i < kBatchSlots; ++i)
 #pragma unroll
                 for (int j = 0; j < VEC; ++j)
-                    sum[i] += table_exp(fmax(((double)v[i][j] - ref) * inv_tau, -700.0), table);
+                    sum[i] += table_exp_scaled(
+                        fmax(((double)v[i][j] - ref) * steepness, -700.0 * kScale), table);
 #pragma unroll
             for (int i = 0; i < kBatchSlots; ++i) s.sum += sum[i];
         }
@@ -642,16 +649,23 @@ struct Sampler {
         }
         __syncthreads();
         if (wave < waves && key != 0) {
-            int rank = lane;
-            for (int w = 0; w < waves; ++w) {
-                if (w == wave) continue;
-                // Keys above this one in a list sorted in descending order.
-                const uint64_t* list = lists + w * 64;
-                int above = 0;
+            // Keys above this one in the waves' lists, each sorted in descending
+            // order: four searches at a time, each a chain of reads.
+            constexpr int U = kWaves < 4 ? kWaves : 4;
+            int rank = 0;
+            for (int w = 0; w < waves; w += U) {
+                const uint64_t* list[U];
+                int above[U] = {};
+#pragma unroll
+                for (int i = 0; i < U; ++i) list[i] = lists + (w + i < waves ? w + i : wave) * 64;
 #pragma unroll
                 for (int step = 32; step > 0; step /= 2)
-                    if (list[above + step - 1] > key) above += step;
-                rank += above + (list[above] > key);
+#pragma unroll
+                    for (int i = 0; i < U; ++i)
+                        above[i] += list[i][above[i] + step - 1] > key ? step : 0;
+#pragma unroll
+                for (int i = 0; i < U; ++i)
+                    if (w + i < waves) rank += above[i] + (list[i][above[i]] > key);
             }
             to[rank] = key;
         }
@@ -724,7 +738,7 @@ struct Sampler {
 
     template <int N>
     __device__ __forceinline__ void push(const float (&v)[N], int e, float steps, float limit) {
-        if (!among(slot_maximum<N>(v), steps, limit)) return;
+        if (!among(slot_maximum<N>(v), steps, limit) || sh->count > kList) return;
 #pragma unroll
         for (int j = 0; j < N; ++j)
             if (among(v[j], steps, limit)) {
@@ -1023,17 +1037,28 @@ struct Sampler {
         if (tid == 0) sh->count = 0;
         __syncthreads();
         const float low = (float)sh->first, high = (float)(sh->last + 1);
-        if (sh->last == kBins) return false;
+        __syncthreads();   // everyone has read them before they change
+        if (high > (float)kBins) return false;
         int from = wave * each;
         if (from > row.n) from = row.n;
         double sum = 0.0;
+        const double steepness = set.inv_tau * kScale;
         lane_slots<L, 64>(row, from, from + each < row.n ? from + each : row.n, lane,
                           [&](const float (&v)[VEC], int e) {
+            bool some = false;
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
                 const float b = fminf(top32 - v[j], FLT_MAX) * steps;
-                const double w = weight(v[j]);
+                // (what lies above the cut is far from weight 0)
+                const double w = table_exp_scaled(
+                    fmax(((double)v[j] - top) * steepness, -700.0 * kScale), sh->table);
                 sum += b < low ? w : 0.0;
+                some = some || (b >= low && b < high);
+            }
+            if (!some) return;   // one branch a slot
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                const float b = fminf(top32 - v[j], FLT_MAX) * steps;
                 if (b >= low && b < high) {
                     const int i = atomicAdd(&sh->count, 1);
                     if (i < kList) sh->list.keys[i] = value_key(v[j], (uint32_t)(e + j));
@@ -1227,7 +1252,7 @@ struct Sampler {
             const double light = log2(2.0 * (double)vocab / ((1.0 - set.p) * mass));
             const float reach = (float)fmin(fmax(light, 1.0), 64.0) * octave;
             if (nucleus(set.p * mass, reach, each, cut, all)) {
-                if (set.least == -INFINITY) {
+                if (exponent(cut.z) >= set.least) {   // none of them under min-p
                     const int token = locate_stretch(set.uniform * all, each, kept);
                     logprob = log_share(all);
                     return token;
@@ -1253,13 +1278,60 @@ struct Sampler {
     }
 };
 
+// Where there are more rows than workgroups at work at a time, those whose whole
+// mass is needed go first, among kOrdered neighbouring rows: a flat row's nucleus
+// takes a workgroup ten times as long as a best-50, and one that began last would
+// be waited for alone (1,024 rows of 131,072 BF16 with mixed settings 163 us in
+// their own order).  Every workgroup finds its row from the settings.
+constexpr int kOrdered = 1024;
+
+template <int NT>
+__device__ __forceinline__ int64_t ordered_row(const SampleParams& p, uint32_t* counts) {
+    constexpr int kEach = kOrdered / NT;   // neighbouring rows of a thread
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int64_t base = (int64_t)(blockIdx.x / kOrdered) * kOrdered;
+    const int n = p.rows - base < kOrdered ? (int)(p.rows - base) : kOrdered;
+    const uint32_t want = blockIdx.x % kOrdered;
+    uint32_t heavy[kEach], mine = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const int64_t r = base + (tid * kEach + i < n ? tid * kEach + i : 0);
+        const float t = p.temperature ? p.temperature[r] : p.tau;
+        const int32_t k = p.top_k ? p.top_k[r] : 0;
+        const float top_p = p.top_p ? p.top_p[r] : 1.0f, q = p.min_p ? p.min_p[r] : 0.0f;
+        heavy[i] = tid * kEach + i < n && t != 0.0f && (k <= 0 || k >= p.vocab) &&
+                   (top_p < 1.0f || !(q > 0.0f));
+        mine += heavy[i];
+    }
+    const uint32_t upto = wave_upto(mine);
+    if (lane == 63) counts[wave] = upto;
+    __syncthreads();
+    uint32_t before = upto - mine, all = 0;
+#pragma unroll
+    for (int i = 0; i < NT / 64; ++i) {
+        before += i < wave ? counts[i] : 0;
+        all += counts[i];
+    }
+    // The row that lands on this workgroup's place.
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const uint32_t r = tid * kEach + i;
+        const uint32_t place = heavy[i] ? before : all + r - before;
+        if ((int)r < n && place == want) counts[NT / 64] = r;
+        before += heavy[i];
+    }
+    __syncthreads();
+    return base + counts[NT / 64];
+}
+
 // A row a workgroup.
 template <typename L, int NT>
 __global__ void __launch_bounds__(NT) sample_kernel(SampleParams p) {
     using S = Sampler<L, NT, 1>;
     __shared__ typename S::Shared shared;
+    __shared__ uint32_t counts[NT / 64 + 1];
     const int tid = threadIdx.x, wave = tid >> 6;
-    const int64_t r = blockIdx.x;
+    const int64_t r = p.rows > kSampleGroups * (1024 / NT) ? ordered_row<NT>(p, counts) : blockIdx.x;
     S s(p, &shared);
     s.set.read(p, r);
     s.row.init(p.logits, r * p.stride, p.vocab, p.chunk, 1, 0);
@@ -1374,6 +1446,7 @@ extern "C" int ws_sample(const ws_rows* rows, const ws_sample_args* args, void* 
     p.token = args->token;
     p.logprob = args->logprob;
     p.space = static_cast<char*>(args->workspace);
+    p.rows = r.rows;
     p.vocab = r.vocab;
     p.chunk = plan.chunk;
     p.parts = plan.parts;
