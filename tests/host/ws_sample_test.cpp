@@ -88,6 +88,29 @@ static void test_arguments() {
     YES(r.rows = 0; std::memset(&a, 0, sizeof a));
 }
 
+static void test_plans() {
+    for (int32_t dtype : {WS_DTYPE_F32, WS_DTYPE_F16, WS_DTYPE_BF16})
+        for (int64_t count : {1ll, 2ll, 15ll, 16ll, 17ll, 64ll, 256ll, 257ll, 512ll, 513ll, 1ll << 22})
+            for (int32_t vocab : {1, 7, 8, 9, 8192, 8193, 24576, 49152, 49160, 131072, 200003, 1 << 30}) {
+                ws_rows r = rows();
+                r.dtype = dtype;
+                r.rows = (int32_t)count;
+                r.vocab = vocab;
+                r.row_stride = vocab;
+                const ws::SamplePlan p = ws::plan_sample(r);
+                CHECK(p.threads == 256 || p.threads == 512 || p.threads == 1024);
+                CHECK(p.parts >= 1 && p.parts <= ws::kMaxSampleParts);
+                CHECK(count * p.parts < (1ll << 31));
+                CHECK((int64_t)p.chunk * p.parts <= ws::slots_of(r));
+                CHECK(ws::slots_of(r) - (int64_t)p.chunk * p.parts < p.parts);
+                CHECK(p.parts == 1 || p.chunk >= ws::kSampleSlots);
+                CHECK(p.workspace == (p.parts > 1 ? (size_t)count * p.parts * 4 * ws::kStretchBytes : 0));
+                // The sum of a row's weights in fixed point fits 63 bits.
+                CHECK(p.unit >= 32 && p.unit <= 62 && ((int64_t)vocab << p.unit) > 0);
+                CHECK(((int64_t)vocab << p.unit) <= (1ll << 62));
+            }
+}
+
 static void layout() {
 #define FIELD(f) std::printf("ws_sample_args " #f " %zu\n", offsetof(ws_sample_args, f))
     std::printf("ws_sample_args sizeof %zu\n", sizeof(ws_sample_args));
@@ -101,6 +124,7 @@ int main(int argc, char** argv) {
         return 0;
     }
     test_arguments();
+    test_plans();
     std::printf("%d failures\n", failures);
     return failures != 0;
 }

@@ -252,6 +252,39 @@ def test_sample_batches(gpu_lib, rows, V):
               min_p=rng.choice([0, 0, 0.05, 0.1], rows))
 
 
+@pytest.mark.parametrize("rows", [257, 512, 513, 1023, 1024, 1025, 2600])
+def test_sample_rows_in_any_order(gpu_lib, rows):
+    """More rows than workgroups at work at a time, which take them in an order of
+    their own: every row is drawn, with its own settings."""
+    rng = np.random.default_rng(rows)
+    V = 9001
+    z = logits(rng, rows, V)
+    kinds = rng.integers(0, 5, rows)
+    given = dict(temperature=np.where(kinds == 0, 0.0, 0.9),
+                 top_k=np.choose(kinds, [0, 0, 20, 0, 0]),
+                 top_p=np.choose(kinds, [1.0, 0.8, 0.9, 1.0, 1.0]),
+                 min_p=np.choose(kinds, [0.0, 0.0, 0.0, 0.05, 0.0]))
+    check(z, rng.random(rows), "bf16", **given)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("V", [9001, 60001])
+def test_sample_wide_nuclei(gpu_lib, dtype, V):
+    """Undecided rows, whose nucleus is thousands of tokens: from a histogram, cut
+    in a bin of few logits, of many, and among equal ones."""
+    rng = np.random.default_rng(V)
+    rows = [rng.normal(size=V) * s for s in (0.01, 0.3, 1.0, 2.0)]
+    rows += [np.round(rng.normal(size=V) * 4) / 4, np.round(rng.normal(size=V)),
+             np.where(rng.random(V) < 0.3, -np.inf, rng.normal(size=V)),
+             rng.normal(size=V) * 1e-4 + 50.0]
+    z = np.stack(rows * 3)
+    p = np.repeat([0.3, 0.8, 0.995], len(rows))
+    check(z, rng.random(len(z)), dtype, top_p=p)
+    check(z, rng.random(len(z)), dtype, top_p=p, min_p=np.tile([0.0, 0.2, 0.01, 1e-4], 6))
+    check(z, rng.random(len(z)), dtype, top_p=p, top_k=np.tile([600, 2000, 5000, 8000], 6),
+          temperature=rng.choice([0.3, 1.0, 20.0], len(z)))
+
+
 def test_sample_without_logprob_and_without_rows(gpu_lib):
     import torch
     rng = np.random.default_rng(13)
