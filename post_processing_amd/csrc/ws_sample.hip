@@ -354,21 +354,30 @@ struct Image {
 // outside the row are -inf.
 template <typename L, typename F>
 __device__ __forceinline__ void walk(const Part<L>& row, int from, int to, F f) {
+    const bool whole = row.full_to > row.full_from;
+    uint4 next = L::none();
+    if (whole) next = row.load_near(from);
     for (int s = from; s < to; ++s) {
         float v[L::VEC];
-        if (row.whole(s)) L::unpack(row.load(s), v);
-        else row.load_edge(s, v);
+        L::unpack(next, v);
+        if (whole) next = row.load_near(s + 1);   // on its way while f runs
+        if (!row.whole(s)) row.load_edge(s, v);
         f(v, row.e0 + s * L::VEC);
     }
 }
 
 constexpr int kBins = 2048, kBounds = 1024;
+// A lane sums 16 neighbouring bounds: one word more for every 16, so that the lanes
+// read from different banks.
+constexpr int kBoundsRoom = kBounds + kBounds / 16;
+__device__ __forceinline__ int bound_at(int b) { return b + (b >> 4); }
 
-// The prefix of the order that is kept: tokens above z, and those at it up to
-// element `last`.
+
+// A prefix of the order: tokens above z, and those at it up to element `last`.
 struct Cut {
     float z;
     int last;
+    double ties;   // above 0: `last` is not known yet, but this many at z belong
     double mass;   // of the prefix, if it was asked for
 };
 
@@ -382,7 +391,7 @@ struct Sampler {
         double table[kTable];
         Stretch stretch[kMostStretches > kWaves ? kMostStretches : kWaves];
         union {
-            uint32_t bounds[kBounds];
+            uint32_t bounds[kBoundsRoom];
             struct {
                 unsigned long long mass[kBins];
                 uint32_t count[kBins];
@@ -412,6 +421,7 @@ struct Sampler {
     float group[GROUPS];   // largest logits of groups of slots: this thread's
     float top32;
     double top, scale;
+    Cut cut;               // what is kept, but for min-p
 
     __device__ __forceinline__ Sampler(const SampleParams& params, Shared* shared)
         : p(params), sh(shared) {}
@@ -423,8 +433,19 @@ struct Sampler {
         const double x = exponent(z);
         return x < kNone ? 0.0 : table_exp(x, sh->table);
     }
+    __device__ __forceinline__ double kept(float v, int e) const {   // its weight, or 0
+        const double x = exponent(v);
+        const bool in = (v > cut.z || (v == cut.z && e <= cut.last)) && x >= set.least && x >= kNone;
+        return in ? table_exp(fmax(x, kNone), sh->table) : 0.0;
+    }
     __device__ __forceinline__ unsigned long long fixed(double w) const {
         return (unsigned long long)fma(w, scale, 0.5);
+    }
+
+    // Keeps what a loop derives from the row's place out of the registers of all
+    // that comes before the loop.
+    __device__ __forceinline__ void recompute() {
+        asm volatile("" : "+v"(row.row), "+v"(row.base), "+v"(row.vocab), "+v"(row.e0));
     }
 
     // The log of the drawn token's share, in thread 0.
@@ -480,111 +501,127 @@ struct Sampler {
         return found;
     }
 
-    // The element at which the amounts f(value, element) >= 0 of slots [from, to)
-    // sum to more than `left` in the order of the vocabulary, and its amount in
-    // sh->left.  Every sum's order is fixed.
-    template <typename F>
-    __device__ __forceinline__ int locate_in(int from, int to, double left, F f) {
+    // The kept token at which the weights of slots [from, to) sum to more than
+    // `left` in the order of the vocabulary, and its weight in sh->left.  Every sum's
+    // order is fixed.
+    __device__ __forceinline__ int locate(int from, int to, double left) {
         const int tid = threadIdx.x;
-        while (to - from > NT) {
+        for (;;) {
+            recompute();
             const int each = (to - from + NT - 1) / NT;
             int mine = from + tid * each;
             if (mine > to) mine = to;
             const int end = mine + each < to ? mine + each : to;
-            double sum = 0.0, at;
-            walk(row, mine, end, [&](const float (&v)[VEC], int e) {
+            double w[VEC], sum = 0.0, at;   // w: of the last slot
+            int element = 0;
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) sum += f(v[j], e + j);
+            for (int j = 0; j < VEC; ++j) w[j] = 0.0;
+            walk(row, mine, end, [&](const float (&v)[VEC], int e) {
+                element = e;
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    w[j] = kept(v[j], e + j);
+                    sum += w[j];
+                }
             });
             const int found = find_thread(sum, left, at);
             if (found < 0) return -1;
-            if (tid == found) sh->total = at;
+            if (tid == found) {
+                sh->total = at;
+                bool done = false;
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    if (!done && w[j] > 0.0) {
+                        sh->token = element + j;
+                        sh->left = w[j];
+                    }
+                    at += w[j];
+                    done = done || (w[j] > 0.0 && at > left);
+                }
+            }
+            __syncthreads();
+            const double skipped = sh->total;
+            const int token = sh->token;
+            __syncthreads();   // everyone has read them before they change
+            if (each == 1) return token;
             from += found * each;
             to = from + each < to ? from + each : to;
-            __syncthreads();
-            left -= sh->total;
-            __syncthreads();
+            left -= skipped;
         }
-        // A slot a thread, its amounts kept.
-        double w[VEC], sum = 0.0, at;
-        int e = 0;
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) w[j] = 0.0;
-        if (from + tid < to) {
-            const int s = from + tid;
-            float v[VEC];
-            if (row.whole(s)) L::unpack(row.load(s), v);
-            else row.load_edge(s, v);
-            e = row.e0 + s * VEC;
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                w[j] = f(v[j], e + j);
-                sum += w[j];
-            }
-        }
-        const int found = find_thread(sum, left, at);
-        if (tid == found) {
-            int token = -1;
-            double amount = 0.0;
-            bool done = false;
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                if (!done && w[j] > 0.0) {
-                    token = e + j;
-                    amount = w[j];
-                }
-                at += w[j];
-                done = done || (w[j] > 0.0 && at > left);
-            }
-            sh->token = token;
-            sh->left = amount;
-        }
-        __syncthreads();
-        const int token = found < 0 ? -1 : sh->token;
-        __syncthreads();   // everyone has read it before it changes
-        return token;
     }
 
-    // The same over the whole row, for a target that depends on the total.
-    template <typename F, typename T>
-    __device__ __forceinline__ int locate(F f, T target, double& total) {
-        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-        const int each = (row.n + kWaves - 1) / kWaves;
+    __device__ __forceinline__ int row_stretch() const { return (row.n + kWaves - 1) / kWaves; }
+
+    // The kept weights of the row's stretches, one a wave, in sh->waves; returns
+    // their sum.
+    __device__ __forceinline__ double sum_row() {
+        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, each = row_stretch();
         int from = wave * each;
         if (from > row.n) from = row.n;
-        const int to = from + each < row.n ? from + each : row.n;
         double sum = 0.0;
-        lane_slots<L, 64>(row, from, to, lane, [&](const float (&v)[VEC], int e) {
+        lane_slots<L, 64>(row, from, from + each < row.n ? from + each : row.n, lane,
+                          [&](const float (&v)[VEC], int e) {
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) sum += f(v[j], e + j);
+            for (int j = 0; j < VEC; ++j) sum += kept(v[j], e + j);
         });
         sum = wave_sum_d(sum, lane);
         if (lane == 0) sh->waves[wave] = sum;
         __syncthreads();
-        total = 0.0;
+        double total = 0.0;
 #pragma unroll
         for (int i = 0; i < kWaves; ++i) total += sh->waves[i];
-        return locate_stretch(target(total), each, f);
+        return total;
     }
 
-    // The same once the stretches' sums are in sh->waves.
-    template <typename F>
-    __device__ __forceinline__ int locate_stretch(double target, int each, F f) {
-        double rest = target, left = 0.0;
-        int chosen = -1;
+    // The stretch of sh->waves that holds the target, and what is left to go in it.
+    __device__ __forceinline__ void find_stretch(double target, int& from, int& to, double& left) {
+        int chosen = 0;
+        left = 0.0;
 #pragma unroll
         for (int i = 0; i < kWaves; ++i) {
             const double w = sh->waves[i];
-            if (w > 0.0 && rest >= 0.0) {
+            if (w > 0.0 && target >= 0.0) {
                 chosen = i;
-                left = rest;
+                left = target;
             }
-            rest -= w;
+            target -= w;
         }
         __syncthreads();
-        if (chosen < 0) return -1;
-        const int from = chosen * each;
-        return locate_in(from, from + each < row.n ? from + each : row.n, left, f);
+        const int each = row_stretch();
+        from = chosen * each;
+        to = from + each < row.n ? from + each : row.n;
+    }
+
+    // The element that is the n-th at z, by index: slots NT at a time.
+    __device__ __forceinline__ int find_tie(float z, uint32_t n) {
+        const int tid = threadIdx.x;
+        uint32_t passed = 0;
+        for (int base = 0; base < row.n; base += NT) {
+            recompute();
+            uint32_t hits = 0, total;   // a bit an element
+            int e = 0;
+            walk(row, base + tid, base + tid < row.n ? base + tid + 1 : 0,
+                 [&](const float (&v)[VEC], int element) {
+                e = element;
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) hits |= v[j] == z ? 1u << j : 0u;
+            });
+            const uint32_t mine = __popc(hits);
+            uint32_t at = passed + before(mine, sh->waves_count, total);
+            if (at < n && at + mine >= n) {
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    at += hits >> j & 1u;
+                    if ((hits >> j & 1u) && at == n) sh->token = e + j;
+                }
+            }
+            __syncthreads();
+            passed += total;
+            if (passed >= n) break;
+        }
+        const int token = sh->token;
+        __syncthreads();   // everyone has read it before it changes
+        return token;
     }
 
     // The largest logit of the row.
@@ -680,7 +717,6 @@ struct Sampler {
     // returns how many (more than kList: they are not all there).  The groups that
     // reach so far are listed, and their slots shared out over the threads.
     __device__ __forceinline__ int collect(float steps, float limit) {
-        constexpr int U = kBatchSlots;
         const int tid = threadIdx.x, lane = tid & 63;
         uint32_t* active = reinterpret_cast<uint32_t*>(sh->list.sorted);
 #pragma unroll
@@ -701,36 +737,35 @@ struct Sampler {
         int each = (row.n - (p.parts - 1) * p.chunk + stretch_waves - 1) / stretch_waves;
         each = (each + 63) / 64;   // slots of a group at most
         const int items = row.full_to > row.full_from ? groups * each : 0;
-        for (int base = 0; base < items; base += U * NT) {
-            uint4 w[U];
-            int s[U];
-#pragma unroll
-            for (int i = 0; i < U; ++i) {
-                const int item = base + i * NT + tid;
-                const int a = item < items ? item / each : 0;
-                const int at = (int)active[a];
-                stretch_slots(row, p, stretch_waves, at >> 6, from, to);
-                from = from > row.full_from ? from : row.full_from;
-                to = to < row.full_to ? to : row.full_to;
-                s[i] = from + (at & 63) + (item - a * each) * 64;
-                if (item >= items || s[i] >= to) s[i] = -1;
-                w[i] = row.load_near(s[i] < 0 ? row.full_from : s[i]);
-            }
-#pragma unroll
-            for (int i = 0; i < U; ++i) {
-                float v[VEC];
-                L::unpack(w[i], v);
-                if (s[i] >= 0) push<VEC>(v, row.e0 + s[i] * VEC, steps, limit);
-            }
+        const auto slot = [&](int item) {   // -1: none
+            const int a = item < items ? item / each : 0;
+            const int at = (int)active[a];
+            stretch_slots(row, p, stretch_waves, at >> 6, from, to);
+            from = from > row.full_from ? from : row.full_from;
+            to = to < row.full_to ? to : row.full_to;
+            const int s = from + (at & 63) + (item - a * each) * 64;
+            return item < items && s < to ? s : -1;
+        };
+        const int tail = row.full_to > row.full_from ? row.full_to : row.full_from;
+        const int rounds = (items + NT - 1) / NT;
+        int next = -1;
+        uint4 ahead = L::none();
+        if (rounds > 0) {
+            next = slot(tid);
+            ahead = row.load_near(next < 0 ? row.full_from : next);
         }
-        if (tid < 2) {   // what sticks out of the row's ends
-            const int tail = row.full_to > row.full_from ? row.full_to : row.full_from;
-            const int s = tid == 0 ? 0 : tail;
-            if (tid == 0 ? row.full_from > 0 : tail < row.n) {
-                float v[VEC];
-                row.load_edge(s, v);
-                push<VEC>(v, row.e0 + s * VEC, steps, limit);
+        for (int r = 0; r <= rounds; ++r) {
+            int s = next;
+            float v[VEC];
+            L::unpack(ahead, v);
+            if (r + 1 < rounds) {
+                next = slot((r + 1) * NT + tid);
+                ahead = row.load_near(next < 0 ? row.full_from : next);
+            } else if (r == rounds) {   // what sticks out of the row's ends
+                s = tid == 0 && row.full_from > 0 ? 0 : tid == 1 && tail < row.n ? tail : -1;
+                if (s >= 0) row.load_edge(s, v);
             }
+            if (s >= 0) push<VEC>(v, row.e0 + s * VEC, steps, limit);
         }
         __syncthreads();
         return sh->count;
@@ -761,20 +796,20 @@ struct Sampler {
             const float b = fminf(d * steps, (float)(kBounds - 1));
             const uint32_t amount =
                 mass ? (uint32_t)(__builtin_amdgcn_exp2f(-d * c) * 262144.0f) : 1u;
-            if (amount) atomicAdd(&sh->bounds[(int)b], amount);
+            if (amount) atomicAdd(&sh->bounds[bound_at((int)b)], amount);
         }
         __syncthreads();
         if (tid < 64) {
             constexpr int kEach = kBounds / 64;
             uint32_t sum = 0;
 #pragma unroll
-            for (int i = 0; i < kEach; ++i) sum += sh->bounds[lane * kEach + i];
+            for (int i = 0; i < kEach; ++i) sum += sh->bounds[bound_at(lane * kEach + i)];
             const uint32_t upto = wave_upto(sum);
             uint32_t at = upto - sum;
             if (lane == 63 && upto < target) sh->limit = INFINITY;
 #pragma unroll
             for (int i = 0; i < kEach; ++i) {
-                const uint32_t next = at + sh->bounds[lane * kEach + i];
+                const uint32_t next = at + sh->bounds[bound_at(lane * kEach + i)];
                 if (at < target && next >= target) sh->limit = (float)(lane * kEach + i + 1);
                 at = next;
             }
@@ -860,18 +895,18 @@ struct Sampler {
         return sh->token;
     }
 
-    // The shortest prefix of the order whose count (MASS: mass) reaches `target`:
+    // The shortest prefix of the order whose count (or mass) reaches `target`:
     // the bin of a histogram over the values in which it ends, and that bin's
     // logits sorted, or, if they are many, bins of them again down to one value,
     // whose ties are counted.  reach: how far below the largest logit the bins
     // go; the last one holds what lies beyond.  Bins sum in fixed point, whose
     // order does not matter; inside a bin sums are FP64.
-    template <bool MASS>
-    __device__ __forceinline__ Cut select(double target, bool masses, float reach) {
+    __device__ __forceinline__ Cut select(bool by_mass, double target, bool masses, float reach) {
         const int tid = threadIdx.x, lane = tid & 63;
-        const Cut everything{-INFINITY, 0x7fffffff, 0.0};
+        const Cut everything{-INFINITY, 0x7fffffff, 0.0, 0.0};
         const double unit = 1.0 / scale;
-        const uint64_t goal = MASS ? (uint64_t)fmax(ceil(target * scale), 1.0) : (uint64_t)target;
+        const uint64_t goal =
+            by_mass ? (uint64_t)fmax(ceil(target * scale), 1.0) : (uint64_t)target;
         const float steps = fminf((float)(kBins - 1) / reach, 1e30f);
         const auto bin_of = [&](float v) {
             return (int)fminf(fminf(top32 - v, FLT_MAX) * steps, (float)(kBins - 1));
@@ -883,13 +918,13 @@ struct Sampler {
                 if (!(v[j] > -INFINITY)) continue;
                 const int b = bin_of(v[j]);
                 atomicAdd(&sh->bins.count[b], 1u);
-                if (masses && (!MASS || b < kBins - 1))
+                if (masses && (!by_mass || b < kBins - 1))
                     atomicAdd(&sh->bins.mass[b], fixed(weight(v[j])));
             }
         });
         uint32_t count = 0, here = 0;
         uint64_t mass = 0, here_mass = 0;
-        int bin = find_bin<MASS>(goal, count, mass, here, here_mass);
+        int bin = find_bin(by_mass, goal, count, mass, here, here_mass);
         if (bin == kBins) return everything;
         if (here <= (uint32_t)kList) {
             if (tid == 0) sh->count = 0;
@@ -909,7 +944,7 @@ struct Sampler {
             const double w = masses && tid < (int)here ? weight(z) : 0.0;
             double all;
             const double m = (double)mass * unit + before(w, sh->waves, all);
-            const bool reached = MASS ? m + w >= target : (double)count + tid + 1.0 >= target;
+            const bool reached = by_mass ? m + w >= target : (double)count + tid + 1.0 >= target;
             if (tid == 0) sh->first = (int)here - 1;
             __syncthreads();
             note_first(tid < (int)here && reached);
@@ -920,9 +955,9 @@ struct Sampler {
                 sh->total = m + w;
             }
             __syncthreads();
-            const Cut cut{sh->limit, sh->last, sh->total};
+            const Cut found{sh->limit, sh->last, 0.0, sh->total};
             __syncthreads();
-            return cut;
+            return found;
         }
         // The images of the bin's logits, from smallest to largest.
         uint32_t lo = 0xffffffffu, hi = 0;
@@ -950,6 +985,7 @@ struct Sampler {
         lo = sh->low;
         hi = sh->high;
         for (;;) {
+            recompute();
             int shift = 0;
             while ((hi - lo) >> shift >= (uint32_t)kBins) ++shift;
             clear_bins();
@@ -964,7 +1000,7 @@ struct Sampler {
                         atomicAdd(&sh->bins.mass[b], fixed(weight(v[j])));
                 }
             });
-            bin = find_bin<MASS>(goal, count, mass, here, here_mass);
+            bin = find_bin(by_mass, goal, count, mass, here, here_mass);
             if (bin == kBins) return everything;
             const uint32_t last = hi - ((uint32_t)bin << shift);
             const uint32_t first = last - ((1u << shift) - 1);
@@ -973,18 +1009,11 @@ struct Sampler {
             if (shift == 0) break;
         }
         // One value: as many of its tokens as the target wants, by index.
-        Cut cut{Image<L>::value(hi), 0x7fffffff, 0.0};
-        const double w = masses ? weight(cut.z) : 0.0, light = (double)mass * unit;
-        double ties = MASS ? ceil((target - light) / w) : target - (double)count;
+        const float z = Image<L>::value(hi);
+        const double w = masses ? weight(z) : 0.0, light = (double)mass * unit;
+        double ties = by_mass ? ceil((target - light) / w) : target - (double)count;
         ties = fmin(fmax(ties, 1.0), (double)here);
-        if (ties < (double)here) {
-            const float z = cut.z;
-            double all;
-            cut.last = locate([&](float v, int) { return v == z ? 1.0 : 0.0; },
-                              [&](double) { return ties - 0.5; }, all);
-        }
-        cut.mass = light + w * ties;
-        return cut;
+        return {z, 0x7fffffff, ties < (double)here ? ties : 0.0, light + w * ties};
     }
 
     // The shortest prefix of the order that holds `target` of the mass, as select
@@ -992,9 +1021,8 @@ struct Sampler {
     // of the cut up to a few bins, then those bins' logits, sorted, on top of an
     // exact sum of what lies above them, by stretches of a wave each, which stays
     // in sh->waves with the kept ones added.  False if those logits are too many.
-    __device__ __forceinline__ bool nucleus(double target, float reach, int each, Cut& cut,
-                                            double& total) {
-        const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    __device__ __forceinline__ bool nucleus(double target, float reach, double& total) {
+        const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, each = row_stretch();
         constexpr float kUnit = 2147483648.0f;
         const float steps = fminf((float)(kBins - 1) / reach, 1e30f);
         const float c = (float)(set.inv_tau * 1.4426950408889634);
@@ -1099,6 +1127,7 @@ struct Sampler {
         __syncthreads();
         cut.z = sh->limit;
         cut.last = sh->last;
+        cut.ties = 0.0;
         total = 0.0;
 #pragma unroll
         for (int i = 0; i < kWaves; ++i) total += sh->waves[i];
@@ -1114,10 +1143,9 @@ struct Sampler {
         __syncthreads();
     }
 
-    // The first bin at whose end count (MASS: mass) reaches the target; count and
+    // The first bin at whose end the count (or mass) reaches the target; count and
     // mass become what lies before it, here and here_mass its own.
-    template <bool MASS>
-    __device__ __forceinline__ int find_bin(uint64_t target, uint32_t& count, uint64_t& mass,
+    __device__ __forceinline__ int find_bin(bool by_mass, uint64_t target, uint32_t& count, uint64_t& mass,
                                             uint32_t& here, uint64_t& here_mass) {
         constexpr int kEach = kBins / NT;
         const int tid = threadIdx.x;
@@ -1136,7 +1164,7 @@ struct Sampler {
             const int b = tid * kEach + i;
             const uint32_t c1 = c + sh->bins.count[b];
             const uint64_t m1 = m + sh->bins.mass[b];
-            const uint64_t was = MASS ? m : c, is = MASS ? m1 : c1;
+            const uint64_t was = by_mass ? m : c, is = by_mass ? m1 : c1;
             if (was < target && is >= target) {   // one bin of all
                 sh->bin = b;
                 sh->before_count = c;
@@ -1188,83 +1216,77 @@ struct Sampler {
             logprob = 0.0f;
             return sh->first;
         }
-        double mass = 0.0;
+        cut = {-INFINITY, 0x7fffffff, 0.0, 0.0};
+        double mass = 0.0, left = 0.0;
+        int from = 0, to = -1;   // the stretch to draw in, once it is known
         if (set.needs_mass(vocab)) {
             sum_stretches();
             mass = sh->total;
             if (!by_p) {
-                int from, to;
                 stretch_slots(row, p, stretch_waves, sh->chosen, from, to);
-                const int token =
-                    locate_in(from, to, sh->left, [&](float v, int) { return weight(v); });
-                logprob = log_share(mass);
-                return token;
+                left = sh->left;
             }
         }
-        // A bound, and the few logits at or above it.
-        float low = INFINITY;
-        for (int i = tid & 63; i < stretches; i += 64) low = fminf(low, sh->stretch[i].low);
-        low = wave_minimum(low, tid & 63);
-        const float steps = fminf((float)(kBounds - 1) / fminf(top32 - low, FLT_MAX), 1e30f);
-        float limit = INFINITY;
-        bool bounded = by_k && set.k <= kList / 2;
-        if (bounded) {
-            limit = bound((uint32_t)set.k, false, steps);
-        } else if (by_p && !by_k) {
+        if (to < 0) {
+            // A bound, and the few logits at or above it.
+            float low = INFINITY;
+            for (int i = tid & 63; i < stretches; i += 64) low = fminf(low, sh->stretch[i].low);
+            low = wave_minimum(low, tid & 63);
+            const float steps = fminf((float)(kBounds - 1) / fminf(top32 - low, FLT_MAX), 1e30f);
+            float limit = INFINITY;
+            bool bounded = by_k && set.k <= kList / 2;
             // (the weights in FP32 are off by less than 1e-5)
-            const double want = set.p * mass * (262144.0 * (1.0 + 1e-5)) + 1.0;
-            if (want < 2e9) limit = bound((uint32_t)want + 1, true, steps);
-        }
-        // Tokens under min-p matter to the mass of the first k alone.
-        if (set.least > -INFINITY && !(by_k && by_p))
-            limit = fminf(limit, fmaxf((float)(-set.least / set.inv_tau * (1.0 + 2e-5)) * steps,
-                                       FLT_MIN));
-        bounded = bounded || limit < INFINITY;
-        if (tid == 0) sh->count = sh->active = 0;
-        __syncthreads();
-        if (bounded) {
-            const int n = collect(steps, limit);
-            if (n <= 64) return draw_few(n, by_k, mass, logprob);
-            if (n <= kList) return draw_list(n, by_k, mass, logprob);
+            const double want = by_k ? (double)set.k : set.p * mass * (262144.0 * (1.0 + 1e-5)) + 2.0;
+            if (bounded || (by_p && !by_k && want < 2e9))
+                limit = bound((uint32_t)want, !by_k, steps);
+            // Tokens under min-p matter to the mass of the first k alone.
+            if (set.least > -INFINITY && !(by_k && by_p))
+                limit = fminf(limit, fmaxf((float)(-set.least / set.inv_tau * (1.0 + 2e-5)) * steps,
+                                           FLT_MIN));
+            bounded = bounded || limit < INFINITY;
+            if (tid == 0) sh->count = sh->active = 0;
             __syncthreads();
-        }
-        // Many: by a histogram of the row.
-        Cut cut{-INFINITY, 0x7fffffff, 0.0};
-        const float octave = (float)(0.6931471805599453 / set.inv_tau);
-        if (by_k) {
-            cut = select<false>((double)set.k, by_p, 64.0f * octave);
-            mass = cut.mass;
-            // Fewer finite logits than k: all of them.
-            if (by_p && cut.z == -INFINITY)
-                locate([&](float v, int) { return v > -INFINITY ? weight(v) : 0.0; },
-                       [](double) { return 0.0; }, mass);
-        }
-        const int each = (row.n + kWaves - 1) / kWaves;
-        const auto kept = [&](float v, int e) {
-            if (!(v > cut.z || (v == cut.z && e <= cut.last)) || v == -INFINITY) return 0.0;
-            const double x = exponent(v);
-            return x >= set.least && x >= kNone ? table_exp(x, sh->table) : 0.0;
-        };
-        double all;
-        if (by_p) {
-            // Tokens too light to make up 1 - p of the mass all together are not
-            // in the shortest prefix.
-            const double light = log2(2.0 * (double)vocab / ((1.0 - set.p) * mass));
-            const float reach = (float)fmin(fmax(light, 1.0), 64.0) * octave;
-            if (nucleus(set.p * mass, reach, each, cut, all)) {
-                if (exponent(cut.z) >= set.least) {   // none of them under min-p
-                    const int token = locate_stretch(set.uniform * all, each, kept);
-                    logprob = log_share(all);
-                    return token;
-                }
-            } else {
-                // The finest steps in which a row of this mass stays below 2^62.
-                if (!by_k) scale = ldexp(1.0, 61 - ilogb(mass));
-                cut = select<true>(set.p * mass, true, reach);
+            if (bounded) {
+                const int n = collect(steps, limit);
+                if (n <= 64) return draw_few(n, by_k, mass, logprob);
+                if (n <= kList) return draw_list(n, by_k, mass, logprob);
+                __syncthreads();
             }
+            // Many: by a histogram of the row, by k and then by p.
+            const float octave = (float)(0.6931471805599453 / set.inv_tau);
+            bool summed = false;   // the stretches of what is kept
+            double all = 0.0;
+            if (by_k) {
+                cut = select(false, (double)set.k, by_p, 64.0f * octave);
+                mass = cut.mass;
+                if (by_p && cut.z == -INFINITY) {
+                    // Fewer finite logits than k: all of them, min-p or not.
+                    const double least = set.least;
+                    set.least = -INFINITY;
+                    mass = sum_row();
+                    set.least = least;
+                    __syncthreads();
+                }
+            }
+            if (by_p) {
+                // Tokens too light to make up 1 - p of the mass all together are
+                // not in the shortest prefix.
+                const float light = log2f((float)(3.0 * (double)vocab / ((1.0 - set.p) * mass)));
+                const float reach = fminf(fmaxf(light, 1.0f), 64.0f) * octave;
+                summed = nucleus(set.p * mass, reach, all);
+                if (!summed) {
+                    // The finest steps in which a row of this mass stays below 2^62.
+                    if (!by_k) scale = ldexp(1.0, 61 - ilogb(mass));
+                    cut = select(true, set.p * mass, true, reach);
+                }
+            }
+            if (cut.ties > 0.0) cut.last = find_tie(cut.z, (uint32_t)cut.ties);
+            if (!summed || exponent(cut.z) < set.least) all = sum_row();
+            mass = all;
+            find_stretch(set.uniform * all, from, to, left);
         }
-        const int token = locate(kept, [&](double w) { return set.uniform * w; }, all);
-        logprob = log_share(all);
+        const int token = locate(from, to, left);
+        logprob = log_share(mass);
         return token;
     }
 
@@ -1326,7 +1348,8 @@ __device__ __forceinline__ int64_t ordered_row(const SampleParams& p, uint32_t* 
 
 // A row a workgroup.
 template <typename L, int NT>
-__global__ void __launch_bounds__(NT) sample_kernel(SampleParams p) {
+__global__ void __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4)))
+sample_kernel(SampleParams p) {
     using S = Sampler<L, NT, 1>;
     __shared__ typename S::Shared shared;
     __shared__ uint32_t counts[NT / 64 + 1];
@@ -1338,7 +1361,7 @@ __global__ void __launch_bounds__(NT) sample_kernel(SampleParams p) {
     s.scale = ldexp(1.0, p.unit);
     s.stretches = s.stretch_waves = NT / 64;
     fill_table(shared.table, NT);
-    for (int i = tid; i < kBounds; i += NT) shared.bounds[i] = 0;
+    for (int i = tid; i < kBoundsRoom; i += NT) shared.bounds[i] = 0;
     __syncthreads();
     int from, to;
     stretch_slots(s.row, p, NT / 64, wave, from, to);
@@ -1396,7 +1419,7 @@ __global__ void __launch_bounds__(kDrawThreads) sample_draw_kernel(SampleParams 
     s.row.init(p.logits, r * p.stride, p.vocab, p.chunk, 1, 0);
     s.scale = ldexp(1.0, p.unit);
     fill_table(shared.table, NT);
-    for (int i = tid; i < kBounds; i += NT) shared.bounds[i] = 0;
+    for (int i = tid; i < kBoundsRoom; i += NT) shared.bounds[i] = 0;
     __syncthreads();
     s.finish(r);
 }
