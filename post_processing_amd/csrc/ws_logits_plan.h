@@ -328,12 +328,28 @@ inline DistillPlan plan_distill(const ws_rows& r, int32_t mode, bool gradient, b
 
 // ws_sample: a workgroup a row; few long rows are read by `parts` workgroups
 // each, whose waves leave 24 bytes and their lanes' largest logits in the
-// workspace, and drawn from by a second kernel.
+// workspace, and drawn from by a second kernel (as row_parts splits rows: more
+// parts for more rows brought nothing, 300 x 50,001 FP32 33 us whole and 36 in
+// three).
+//
+// A CU has 1,024 threads of the kernel at work.  One row of them while rows are
+// few, or long (the longest row's nucleus is then waited for: 1,024 x 131,072 BF16
+// with mixed settings 131 us, 166 with two rows of 512 threads); two of 512 where
+// rows come in more than one round and are shorter (2,000 x 32,768 FP16 mixed 77 us
+// and 115 with one of 1,024; 600 x 50,001 BF16 with the best 50 30 and 38), and up to
+// 512 rows of any length (300 x 50,001 FP32 31 and 38); 256 threads for rows that
+// give more no whole slot.
 constexpr int kMaxSampleParts = 32;
 constexpr int64_t kSampleSlots = 1024;   // of a part, at least
-constexpr int64_t kSampleShort = 1024;   // slots of a row up to which 256 threads do
+constexpr int64_t kSampleShort = 1024, kSampleLong = 8192;   // slots of a row
 constexpr int kSampleGroups = 256;       // workgroups of 1,024 threads at work at a time
 constexpr int kStretchBytes = 24 + 64 * 4;
+
+inline int32_t sample_threads(int64_t rows, int64_t slots) {
+    if (slots <= kSampleShort) return 256;
+    if (rows <= kSampleGroups) return 1024;
+    return rows <= 2 * kSampleGroups || slots <= kSampleLong ? 512 : 1024;
+}
 
 struct SamplePlan {
     int32_t threads = 1024;
@@ -347,9 +363,7 @@ inline SamplePlan plan_sample(const ws_rows& r) {
     SamplePlan p;
     if (r.rows == 0) return p;
     const int64_t slots = slots_of(r);
-    p.threads = slots <= kSampleShort                                           ? 256
-                : r.rows > kSampleGroups && r.rows <= 2 * kSampleGroups ? 512
-                                                                        : 1024;
+    p.threads = sample_threads(r.rows, slots);
     if (slots > kSplitSlots) {
         int64_t parts = kSplitGroups / r.rows;
         if (parts > slots / kSampleSlots) parts = slots / kSampleSlots;
