@@ -25,8 +25,10 @@ struct EmbedParams {
     float scale;
 };
 
-// A copy: bound by HBM, or for few rows by the index's and the row's latency
-// one after the other.
+// A copy: bound by HBM and the caches, or for few rows by the index's and the row's
+// latency one after the other (64 x 4,096 BF16 3.2 us; 16,384 x 4,096 from 32,768
+// rows 42 us: 134.2 MB written and 78.6 read, tokens that repeat come from the
+// caches).
 template <typename L>
 __global__ void __launch_bounds__(kLookupThreads) embed_kernel(EmbedParams p) {
     using Elem = typename L::Elem;
@@ -63,6 +65,13 @@ __global__ void __launch_bounds__(kLookupThreads) embed_kernel(EmbedParams p) {
 // depends on timing, and one token that half the rows name is as many blocks' work
 // as half the rows.  The table's zeros are written by workgroups beside the sort's,
 // whose few workgroups wait on latency.
+//
+// Bytes bound it: 16,384 rows into 32,768 x 4,096 BF16, 112 us for 268 MB of zeros,
+// 134 read and 47 of sums written (4.0 TB/s): the sort with the zeros 46, the sums 57
+// (while the zeros still drain), the join 9.  Leaving out the zeros of rows that are
+// named would save 45 MB but cost as much: every clearing workgroup would read all
+// tokens first (129 us).  777 rows take 17 us: three launches, each a chain of
+// latencies (sort 7.8, sums 5.7, join 3.6).
 
 struct ClearParams {
     void* table;

