@@ -105,7 +105,7 @@ __device__ __forceinline__ void fill_table(double* table, int threads) {
 
 constexpr double kScale = 369.3299304675746;     // 256 / log 2
 
-// e^(t / kScale) for t between -700 and 100 times kScale, to 2e-13 relative: t = n +
+// e^(t / kScale) for t between -700 and 130 times kScale, to 2e-13 relative: t = n +
 // r, 2 to the n / 256 from a table (LDS) and a shift of its exponent, and the series
 // of what is left (at most 1.4e-3) to the third power.  Sixteen instructions with
 // the sum, half of the exponential the library has in FP64; the draw's borders
