@@ -39,13 +39,19 @@ struct NormParams {
 // BF16).  HBM bounds it: 52.5 us for that, 5.1 TB/s, the rate of a large copy; three
 // passes over the row in a workgroup a row took 75.7.  64 rows take 3.9 us: a
 // launch, one row's latency and two sums over four waves.
+// NT threads to a row; rows of less than a wave's slots lie side by side in one,
+// whose lanes would else be idle (200,000 x 256 BF16 68 us with a wave a row, 40 with
+// two rows a wave).
+constexpr int group_threads(int nt) { return nt < 64 ? 64 : nt; }
+
 template <typename L, int NT, int R>
-__global__ void __launch_bounds__(NT) norm_kernel(NormParams p) {
+__global__ void __launch_bounds__(group_threads(NT)) norm_kernel(NormParams p) {
     using Elem = typename L::Elem;
     constexpr int VEC = L::VEC;
     constexpr bool kHold = R * VEC <= 16;
-    __shared__ float first[NT / 64];
-    __shared__ float2 second[NT / 64];
+    constexpr int kRows = group_threads(NT) / NT;   // side by side
+    __shared__ float first[kRows > 1 ? 1 : NT / 64];
+    __shared__ float2 second[kRows > 1 ? 1 : NT / 64];
     const HeldSlots<L, NT, R> slots(p.width);
     const Elem* x = static_cast<const Elem*>(p.x);
     Elem* y = static_cast<Elem*>(p.y);
@@ -55,13 +61,16 @@ __global__ void __launch_bounds__(NT) norm_kernel(NormParams p) {
         slots.weights(p.bias, p.weight_f32, 0.0f, b);
     }
     uint4 w[R];
-    slots.load(x + (int64_t)blockIdx.x * p.x_stride, w);
-    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    const int64_t step = (int64_t)gridDim.x * kRows;
+    int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / NT;
+    slots.load(x + (row < p.rows ? row : p.rows - 1) * p.x_stride, w);
+    // (a row side by side with the last one may lie behind it)
+    for (int64_t base = (int64_t)blockIdx.x * kRows; base < p.rows; base += step, row += step) {
         float v[R][VEC];
 #pragma unroll
         for (int i = 0; i < R; ++i) L::unpack(w[i], v[i]);
-        const int64_t next = row + gridDim.x;
-        slots.load(x + (next < p.rows ? next : row) * p.x_stride, w);
+        const int64_t next = row + step;
+        slots.load(x + (next < p.rows ? next : p.rows - 1) * p.x_stride, w);
         float sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < R; ++i)
@@ -82,7 +91,8 @@ __global__ void __launch_bounds__(NT) norm_kernel(NormParams p) {
         const float shift = far.x * p.inv_width;
         const float var = fmaxf(far.y * p.inv_width - shift * shift, 0.0f);
         const float inverse = 1.0f / sqrtf(var + p.eps);
-        if (p.stats && threadIdx.x == 0) p.stats[row] = {mean + shift, inverse};
+        if (kRows > 1 && row >= p.rows) continue;
+        if (p.stats && threadIdx.x % NT == 0) p.stats[row] = {mean + shift, inverse};
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             if (!slots.any(i)) continue;
@@ -175,16 +185,26 @@ struct NormGradParams {
     float inv_width;
 };
 
+// The sum over a wave's lanes NT apart, in each of them.
+template <int NT>
+__device__ __forceinline__ float apart_sum(float v) {
+    const int lane = threadIdx.x & 63;
+    if constexpr (NT <= 8) v += xor_lane_f<8>(v, lane);
+    if constexpr (NT <= 16) v += xor_lane_f<16>(v, lane);
+    return v + xor_lane_f<32>(v, lane);
+}
+
 // Rows held as norm_kernel's: grad_x, and in registers the workgroup's rows'
 // sums for the weight's and the bias's gradient, which it leaves in the workspace.
 // SUMS: with those.  One pass over x and grad_y serves both: 16,384 x 4,096 BF16
 // 75 us (5.4 TB/s; 269.7 MB read, 151.0 written, 16.8 of them the workgroups' sums)
 // and 5 for joining the sums; with a kernel for each, 219 in all.
 template <typename L, int NT, int R, bool SUMS>
-__global__ void __launch_bounds__(NT) norm_grad_kernel(NormGradParams p) {
+__global__ void __launch_bounds__(group_threads(NT)) norm_grad_kernel(NormGradParams p) {
     using Elem = typename L::Elem;
     constexpr int VEC = L::VEC;
-    __shared__ float2 waves[2][NT / 64];
+    constexpr int kRows = group_threads(NT) / NT;
+    __shared__ float2 waves[2][kRows > 1 ? 1 : NT / 64];
     const HeldSlots<L, NT, R> slots(p.width);
     const Elem* x = static_cast<const Elem*>(p.x);
     const Elem* gy = static_cast<const Elem*>(p.grad_y);
@@ -197,11 +217,14 @@ __global__ void __launch_bounds__(NT) norm_grad_kernel(NormGradParams p) {
             for (int j = 0; j < VEC; ++j) gw[i][j] = gb[i][j] = 0.0f;
     }
     uint4 wx[R], wy[R];
-    slots.load(x + (int64_t)blockIdx.x * p.x_stride, wx);
-    slots.load(gy + (int64_t)blockIdx.x * p.y_stride, wy);
-    ws_norm_stats ahead = p.stats[blockIdx.x];
+    const int64_t step = (int64_t)gridDim.x * kRows;
+    int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / NT;
+    int64_t next = row < p.rows ? row : p.rows - 1;
+    slots.load(x + next * p.x_stride, wx);
+    slots.load(gy + next * p.y_stride, wy);
+    ws_norm_stats ahead = p.stats[next];
     int turn = 0;
-    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    for (int64_t base = (int64_t)blockIdx.x * kRows; base < p.rows; base += step, row += step) {
         float u[R][VEC], d[R][VEC];
         const ws_norm_stats s = ahead;
 #pragma unroll
@@ -209,8 +232,7 @@ __global__ void __launch_bounds__(NT) norm_grad_kernel(NormGradParams p) {
             L::unpack(wx[i], u[i]);
             L::unpack(wy[i], d[i]);
         }
-        int64_t next = row + gridDim.x;
-        next = next < p.rows ? next : row;
+        next = row + step < p.rows ? row + step : p.rows - 1;
         slots.load(x + next * p.x_stride, wx);
         slots.load(gy + next * p.y_stride, wy);
         ahead = p.stats[next];
@@ -221,6 +243,7 @@ __global__ void __launch_bounds__(NT) norm_grad_kernel(NormGradParams p) {
             for (int j = 0; j < VEC; ++j) {
                 u[i][j] = (u[i][j] - s.mean) * s.inverse;
                 if constexpr (SUMS) {
+                    if (kRows > 1 && row >= p.rows) continue;
                     gw[i][j] = fmaf(d[i][j], u[i][j], gw[i][j]);
                     gb[i][j] += d[i][j];
                 }
@@ -232,6 +255,7 @@ __global__ void __launch_bounds__(NT) norm_grad_kernel(NormGradParams p) {
         if (!p.grad_x) continue;
         sums = group_sums<NT>(sums, waves[turn]);
         turn ^= 1;
+        if (kRows > 1 && row >= p.rows) continue;
         const float level = sums.x * p.inv_width, along = sums.y * p.inv_width;
         Elem* gx = static_cast<Elem*>(p.grad_x) + row * p.grad_stride;
 #pragma unroll
@@ -245,6 +269,16 @@ __global__ void __launch_bounds__(NT) norm_grad_kernel(NormGradParams p) {
     }
     if constexpr (SUMS) {
         float* out = p.partial + (int64_t)blockIdx.x * 2 * p.partial_stride;
+        if constexpr (kRows > 1) {   // the rows side by side
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    gw[i][j] = apart_sum<NT>(gw[i][j]);
+                    gb[i][j] = apart_sum<NT>(gb[i][j]);
+                }
+            if (threadIdx.x >= NT) return;
+        }
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             if (!slots.any(i)) continue;
@@ -396,8 +430,12 @@ __global__ void __launch_bounds__(kJoinThreads) norm_join_kernel(NormGradParams 
 template <typename L>
 int run_norm(const ws_states& t, const NormParams& p, hipStream_t s) {
     const NormPlan plan = plan_layernorm(t);
-#define PICK(NT, R) \
-    if (plan.threads == NT && plan.held == R) return launch(norm_kernel<L, NT, R>, plan.groups, NT, p, s)
+#define PICK(NT, R)                           \
+    if (plan.threads == NT && plan.held == R) \
+    return launch(norm_kernel<L, NT, R>, plan.groups, group_threads(NT), p, s)
+    PICK(8, 1);
+    PICK(16, 1);
+    PICK(32, 1);
     PICK(64, 1);
     PICK(64, 2);
     PICK(256, 1);
@@ -406,14 +444,17 @@ int run_norm(const ws_states& t, const NormParams& p, hipStream_t s) {
     PICK(1024, 2);
     PICK(1024, 4);
 #undef PICK
-    return launch(norm_long_kernel<L, kNormThreads>, t.rows, kNormThreads, p, s);
+    return launch(norm_long_kernel<L, kLongThreads>, t.rows, kLongThreads, p, s);
 }
 
 template <typename L, bool SUMS>
 int run_norm_grad_held(const NormGradPlan& plan, const NormGradParams& p, hipStream_t s) {
 #define PICK(NT, R)                                  \
     if (plan.threads == NT && plan.held == R)        \
-    return launch(norm_grad_kernel<L, NT, R, SUMS>, plan.groups, NT, p, s)
+    return launch(norm_grad_kernel<L, NT, R, SUMS>, plan.groups, group_threads(NT), p, s)
+    PICK(8, 1);
+    PICK(16, 1);
+    PICK(32, 1);
     PICK(64, 1);
     PICK(64, 2);
     PICK(256, 1);
@@ -436,7 +477,7 @@ int run_norm_grad(const ws_states& t, const NormGradPlan& plan, const NormGradPa
             v = launch(norm_columns_kernel<L, kNormThreads>, (int64_t)plan.columns * plan.groups,
                        kNormThreads, p, s);
         if (v == WS_OK && p.grad_x)
-            v = launch(norm_grad_long_kernel<L, kNormThreads>, t.rows, kNormThreads, p, s);
+            v = launch(norm_grad_long_kernel<L, kLongThreads>, t.rows, kLongThreads, p, s);
     }
     if (v != WS_OK || !sums) return v;
     return launch(norm_join_kernel<L>, 2 * ((p.width + kJoinColumns - 1) / kJoinColumns),

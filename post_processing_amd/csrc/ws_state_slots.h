@@ -115,13 +115,26 @@ __device__ __forceinline__ void store_either(void* row, bool f32, int c, int wid
     }
 }
 
-// The sums of two values over a workgroup, in every thread.  `waves` (LDS) must
-// not be written again before every thread has read it: two sums in turn take two.
+// The sum over the LANES neighbouring lanes (a power of two) one's own is among,
+// in each of them.
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float v, int lane) {
+    if constexpr (LANES > 32) v += xor_lane_f<32>(v, lane);
+    if constexpr (LANES > 16) v += xor_lane_f<16>(v, lane);
+    if constexpr (LANES > 8) v += xor_lane_f<8>(v, lane);
+    v += xor_lane_f<4>(v, lane);
+    v += xor_lane_f<2>(v, lane);
+    return v + xor_lane_f<1>(v, lane);
+}
+
+// The sums of two values over NT threads, in each of them: neighbouring lanes of a
+// wave, or the workgroup.  `waves` (LDS) must not be written again before every
+// thread has read it: two sums in turn take two.
 template <int NT>
 __device__ __forceinline__ float2 group_sums(float2 v, float2* waves) {
     const int lane = threadIdx.x & 63;
-    v.x = wave_sum(v.x, lane);
-    v.y = wave_sum(v.y, lane);
+    v.x = lanes_sum<NT < 64 ? NT : 64>(v.x, lane);
+    v.y = lanes_sum<NT < 64 ? NT : 64>(v.y, lane);
     if constexpr (NT > 64) {
         if (lane == 0) waves[threadIdx.x >> 6] = v;
         __syncthreads();
@@ -138,7 +151,7 @@ __device__ __forceinline__ float2 group_sums(float2 v, float2* waves) {
 template <int NT>
 __device__ __forceinline__ float group_sum(float v, float* waves) {
     const int lane = threadIdx.x & 63;
-    v = wave_sum(v, lane);
+    v = lanes_sum<NT < 64 ? NT : 64>(v, lane);
     if constexpr (NT > 64) {
         if (lane == 0) waves[threadIdx.x >> 6] = v;
         __syncthreads();
@@ -149,7 +162,7 @@ __device__ __forceinline__ float group_sum(float v, float* waves) {
     return v;
 }
 
-// Slots a thread holds of every row: i * NT + thread.  All are full, so that no
+// Slots a thread holds of every row of its NT threads: i * NT + thread.  All are full, so that no
 // load hangs on a condition: a last slot that would end behind the row begins
 // earlier instead and has its first elements in common with the one before, and
 // threads without a slot hold the row's end too.  Needs rows of VEC elements.
@@ -162,7 +175,7 @@ struct HeldSlots {
     __device__ __forceinline__ explicit HeldSlots(int width) {
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            const int c = (i * NT + (int)threadIdx.x) * VEC;
+            const int c = (i * NT + (int)threadIdx.x % NT) * VEC;
             at[i] = c + VEC <= width ? c : width - VEC;
             own[i] = c - at[i];
         }

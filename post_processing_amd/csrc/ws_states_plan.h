@@ -237,10 +237,11 @@ inline int validate_layernorm_grad(const ws_states* t, const ws_layernorm_grad_a
     return WS_OK;
 }
 
-constexpr int kNormThreads = 256;
+constexpr int kNormThreads = 256, kLongThreads = 1024;
 
-// Rows held in registers: `held` slots by each of `threads` threads, `groups`
-// workgroups that take rows in turn.  0: rows that do not fit, or have no slot.
+// Rows held in registers: `held` slots by each of `threads` threads (less than a
+// wave: rows side by side in one), `groups` workgroups that take rows in turn.  0:
+// rows that do not fit, or have no slot.
 struct NormPlan {
     int32_t threads = kNormThreads;
     int32_t held = 0;
@@ -254,17 +255,27 @@ inline NormPlan plan_held(const ws_states& t, int64_t most) {
     NormPlan p;
     const int64_t slots = slots_in(t.width, t.dtype);
     if (slots > most || t.width < 16 / logit_bytes(t.dtype)) return p;
-    p.threads = slots <= 128 ? 64 : slots <= 512 ? 256 : slots <= 1024 ? 512 : 1024;
+    p.threads = slots <= 8      ? 8
+                : slots <= 16   ? 16
+                : slots <= 32   ? 32
+                : slots <= 128  ? 64
+                : slots <= 512  ? 256
+                : slots <= 1024 ? 512
+                                : 1024;
     p.held = slots <= p.threads ? 1 : slots <= 2 * p.threads ? 2 : 4;
     if (p.threads >= 512 && p.held < 2) p.held = 2;
-    const int64_t groups = kNormWaves / (p.threads / 64);
-    p.groups = (int32_t)(t.rows < groups ? t.rows : groups);
+    const int64_t beside = p.threads < 64 ? 64 / p.threads : 1;
+    const int64_t most_groups = kNormWaves / (p.threads < 64 ? 1 : p.threads / 64);
+    const int64_t groups = (t.rows + beside - 1) / beside;
+    p.groups = (int32_t)(groups < most_groups ? groups : most_groups);
     return p;
 }
 
 inline NormPlan plan_layernorm(const ws_states& t) { return plan_held(t, 4096); }
 
 // Sums over the rows: `groups` workgroups' sums of every column, then their sum.
+// Workgroups of one wave are four times as many: 65,536 x 1,024 BF16 takes 116 us
+// with 512 of them, 88 with 2,048.
 constexpr int64_t kColumnGroups = 512;
 
 struct NormGradPlan {
@@ -283,7 +294,8 @@ inline NormGradPlan plan_layernorm_grad(const ws_states& t) {
     if (t.rows == 0) {
         p.groups = 0;
     } else if (p.held > 0) {
-        p.groups = held.groups < kColumnGroups ? held.groups : (int32_t)kColumnGroups;
+        const int64_t most = p.threads <= 64 ? 4 * kColumnGroups : kColumnGroups;
+        p.groups = (int32_t)(held.groups < most ? held.groups : most);
     } else {
         p.columns = (int32_t)((slots_in(t.width, t.dtype) + kNormThreads - 1) / kNormThreads);
         int64_t groups = kColumnGroups / p.columns;

@@ -376,6 +376,17 @@ def test_norm_in_place(gpu_lib, width):
     check_norm(rng.normal(size=(9, width)), "f16", in_place=True, pad=2)
 
 
+NARROW = [(1, 8), (3, 16), (7, 31), (8, 64), (9, 33), (15, 9), (17, 64), (2, 65), (3, 128), (4, 129),
+          (5, 256), (31, 200), (1001, 40), (40000, 33), (20000, 130)]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,width", NARROW)
+def test_norm_narrow_rows(gpu_lib, dtype, rows, width):
+    rng = np.random.default_rng(rows + width)
+    check_norm(rng.normal(size=(rows, width)) * 2 - 1, dtype, weight=dtype, pad=rows % 4)
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("width", [30, 900, 40000])
 def test_norm_rows_far_from_zero(gpu_lib, dtype, width):
@@ -451,6 +462,14 @@ def test_norm_grad_widths(gpu_lib, dtype, width):
 def test_norm_grad_rows(gpu_lib, dtype, rows):
     rng = np.random.default_rng(rows)
     check_norm_grad(rng.normal(size=(rows, 129)), rng.normal(size=(rows, 129)), dtype, weight=dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,width", NARROW)
+def test_norm_grad_narrow_rows(gpu_lib, dtype, rows, width):
+    rng = np.random.default_rng(rows + width)
+    check_norm_grad(rng.normal(size=(rows, width)) * 2 - 1, rng.normal(size=(rows, width)), dtype,
+                    weight=dtype, pad=rows % 4)
 
 
 @pytest.mark.parametrize("dtype", TYPES)
