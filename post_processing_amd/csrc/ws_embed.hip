@@ -63,7 +63,10 @@ __global__ void __launch_bounds__(kLookupThreads) embed_kernel(EmbedParams p) {
 // written at once; of a token that goes over a border each block leaves a partial
 // sum, and the block where the token begins has them added in order.  So no sum
 // depends on timing, and one token that half the rows name is as many blocks' work
-// as half the rows.  The table's zeros are written by workgroups beside the sort's,
+// as half the rows.  Rows of few slots have their blocks side by side in a workgroup
+// (200,000 x 64 BF16 into 50,000 rows 178 us with a block a workgroup and one
+// workgroup that sums the tiles' counts, 59 with this and a wave a digit; 1,000,000
+// rows 552 and 134).  The table's zeros are written by workgroups beside the sort's,
 // whose few workgroups wait on latency.
 //
 // Bytes bound it: 16,384 rows into 32,768 x 4,096 BF16, 112 us for 268 MB of zeros,
@@ -172,17 +175,28 @@ __device__ __forceinline__ uint32_t sum_before(uint32_t v, uint32_t* waves) {
     return before;
 }
 
-// Many tiles: counts[tile][digit] becomes where the tile's tokens of that digit
-// go, one digit a thread.
-__global__ void __launch_bounds__(kDigits) sort_scan_kernel(SortParams p) {
-    __shared__ uint32_t waves[kDigits / 64];
+// Many tiles: counts[tile][digit] becomes how many tokens of the digit are in the
+// tiles before, and counts[tiles][digit] how many there are: a digit a wave, whose
+// lanes take neighbouring tiles.
+__global__ void __launch_bounds__(kScanDigits * 64) sort_scan_kernel(SortParams p) {
+    const int lane = threadIdx.x & 63;
+    uint32_t* c = p.counts + blockIdx.x * kScanDigits + (threadIdx.x >> 6);
+    const int each = (p.tiles + 63) / 64;
+    const int first = lane * each, end = first + each < p.tiles ? first + each : p.tiles;
     uint32_t total = 0;
-    for (int t = 0; t < p.tiles; ++t) total += p.counts[(int64_t)t * kDigits + threadIdx.x];
-    uint32_t at = sum_before(total, waves);
-    for (int t = 0; t < p.tiles; ++t) {
-        uint32_t* c = p.counts + (int64_t)t * kDigits + threadIdx.x;
-        const uint32_t n = *c;
-        *c = at;
+#pragma unroll 4
+    for (int t = first; t < end; ++t) total += c[(int64_t)t * kDigits];
+    uint32_t upto = total;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const uint32_t other = __shfl_up(upto, d);
+        if (lane >= d) upto += other;
+    }
+    if (lane == 63) c[(int64_t)p.tiles * kDigits] = upto;
+    uint32_t at = upto - total;
+    for (int t = first; t < end; ++t) {
+        const uint32_t n = c[(int64_t)t * kDigits];
+        c[(int64_t)t * kDigits] = at;
         at += n;
     }
 }
@@ -251,23 +265,19 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortParams p) 
         row[i] = p.shift > 0 ? p.rows_in[at] : (uint32_t)at;
     }
     // Where the tile's tokens of a digit go.
-    uint32_t at = 0;
-    const bool scanned = p.tiles > kScanTiles;
-    if (tid < kDigits) {
-        if (scanned) {
-            at = p.counts[(int64_t)blockIdx.x * kDigits + tid];
-        } else {
-            uint32_t total = 0;
+    uint32_t at = 0, total = 0;
+    if (tid < kDigits && p.tiles > kScanTiles) {
+        at = p.counts[(int64_t)blockIdx.x * kDigits + tid];
+        total = p.counts[(int64_t)p.tiles * kDigits + tid];
+    } else if (tid < kDigits) {
 #pragma unroll 8
-            for (int t = 0; t < p.tiles; ++t) {
-                const uint32_t c = p.counts[t * kDigits + tid];
-                total += c;
-                at += t < (int)blockIdx.x ? c : 0;
-            }
-            rank[0] = total;
+        for (int t = 0; t < p.tiles; ++t) {
+            const uint32_t c = p.counts[t * kDigits + tid];
+            total += c;
+            at += t < (int)blockIdx.x ? c : 0;
         }
     }
-    if (!scanned) at += sum_before(tid < kDigits ? rank[0] : 0, tile.waves);
+    at += sum_before(total, tile.waves);
     rank_tile(key, first, p.n, p.shift, tile, rank);
     place_tile(tile, at);
 #pragma unroll
@@ -341,6 +351,7 @@ struct SumParams {
     int32_t vocab;
     int32_t block, blocks;
     int32_t columns;
+    int32_t lanes;          // threads to a block
     int32_t grad_f32;
     int32_t accumulate;
     float scale;
@@ -404,27 +415,40 @@ __device__ __forceinline__ void write_sum(const SumParams& p, uint32_t key, cons
     }
 }
 
-// The rows of one block of the sorted tokens, kSumAhead at a time on their way.
+// A value that WAVES says is the same in a whole wave.
+template <bool WAVES>
+__device__ __forceinline__ uint32_t same(uint32_t v) {
+    return WAVES ? __builtin_amdgcn_readfirstlane(v) : v;
+}
+
+// The rows of blocks of the sorted tokens, kSumAhead at a time on their way; rows of
+// few slots have several blocks side by side, WAVES: each of whole waves.
 constexpr int kSumAhead = 8;
 
-template <typename L>
+template <typename L, bool WAVES>
 __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(SumParams p) {
     using Elem = typename L::Elem;
     constexpr int VEC = L::VEC, U = kSumAhead;
-    __shared__ uint32_t keys[kMostRows + 2], rows[kMostRows];
+    __shared__ uint32_t all_keys[kMostRows + 2], all_rows[kMostRows];
     const int tile = blockIdx.x % (uint32_t)p.columns;
-    const int64_t block = blockIdx.x / (uint32_t)p.columns;
-    const int from = (int)block * p.block;
-    const int n = p.n - from < p.block ? p.n - from : p.block;
-    // The block's tokens, and the ones before and behind (none: no token's key).
-    for (int i = threadIdx.x; i < n + 2; i += kSumThreads) {
+    const int side = threadIdx.x / (uint32_t)p.lanes, beside = kSumThreads / p.lanes;
+    const int64_t first = blockIdx.x / (uint32_t)p.columns * (int64_t)beside;
+    const int from = (int)first * p.block;
+    const int n_all = p.n - from < beside * p.block ? p.n - from : beside * p.block;
+    // The blocks' tokens, and the ones before and behind (none: no token's key).
+    for (int i = threadIdx.x; i < n_all + 2; i += kSumThreads) {
         const int at = from + i - 1;
-        keys[i] = at >= 0 && at < p.n ? p.keys[at] : 0xffffffffu;
-        if (i < n) rows[i] = p.rows[from + i];
+        all_keys[i] = at >= 0 && at < p.n ? p.keys[at] : 0xffffffffu;
+        if (i < n_all) all_rows[i] = p.rows[from + i];
     }
     __syncthreads();
-    if ((tile * kSumThreads + (int)threadIdx.x) * VEC >= p.width) return;
-    const Columns<L> c((tile * kSumThreads + (int)threadIdx.x) * VEC, p.width);
+    const int64_t block = first + side;
+    const uint32_t* keys = all_keys + side * p.block;
+    const uint32_t* rows = all_rows + side * p.block;
+    const int left = n_all - side * p.block, n = left < p.block ? left : p.block;
+    const int column = (tile * p.lanes + (int)threadIdx.x % p.lanes) * VEC;
+    if (n <= 0 || column >= p.width) return;
+    const Columns<L> c(column, p.width);
     float sum[VEC];
 #pragma unroll
     for (int j = 0; j < VEC; ++j) sum[j] = 0.0f;
@@ -440,21 +464,20 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(SumParams p) {
         } else {
 #pragma unroll
             for (int i = 0; i < U; ++i) {
-                const uint32_t row =
-                    __builtin_amdgcn_readfirstlane(rows[base + i < n ? base + i : n - 1]);
+                const uint32_t row = same<WAVES>(rows[base + i < n ? base + i : n - 1]);
                 w[i] = c.load(grad + (int64_t)row * p.stride);
             }
         }
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             if (base + i >= n) return;
-            const uint32_t key = __builtin_amdgcn_readfirstlane(keys[base + i + 1]);
+            const uint32_t key = same<WAVES>(keys[base + i + 1]);
             if (key >= (uint32_t)p.vocab) return;   // no token: all behind are
             float v[VEC];
             L::unpack(w[i], v);
 #pragma unroll
             for (int j = 0; j < VEC; ++j) sum[j] += v[j];
-            const bool last = __builtin_amdgcn_readfirstlane(keys[base + i + 2]) != key;
+            const bool last = same<WAVES>(keys[base + i + 2]) != key;
             if (!last && base + i + 1 < n) continue;
             if (last && !began) {
                 write_sum<L>(p, key, c, sum);
@@ -469,24 +492,17 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(SumParams p) {
     }
 }
 
-// A token that begins in this block and goes on: its partial sums in order.
+// The sum of the token's partial sums of blocks from `b` on, kJoinAhead of them at a
+// time and `step` from one time to the next, until the token ends (true) or the
+// block `until`.
+constexpr int kJoinAhead = 8;
+
 template <typename L>
-__global__ void __launch_bounds__(kSumThreads) embed_join_kernel(SumParams p) {
-    constexpr int VEC = L::VEC;
-    const int tile = blockIdx.x % (uint32_t)p.columns;
-    const int64_t block = blockIdx.x / (uint32_t)p.columns;
-    const int from = (int)block * p.block;
-    if (p.n - from <= p.block) return;   // the last block
-    const int end = from + p.block;      // behind it
-    const uint32_t key = p.keys[end];
-    if (key >= (uint32_t)p.vocab || p.keys[end - 1] != key) return;
-    if (from > 0 && p.keys[from - 1] == key) return;   // began earlier
-    if ((tile * kSumThreads + (int)threadIdx.x) * VEC >= p.width) return;
-    const Columns<L> c((tile * kSumThreads + (int)threadIdx.x) * VEC, p.width);
-    float sum[VEC];
-    c.load_sum(p.partial + (block * 2 + 1) * p.partial_stride, sum);
-    constexpr int U = 8;
-    for (int64_t b = block + 1; b < p.blocks; b += U) {
+__device__ __forceinline__ bool add_partials(const SumParams& p, uint32_t key, int64_t b,
+                                             int64_t step, int64_t until, const Columns<L>& c,
+                                             float (&sum)[L::VEC]) {
+    constexpr int VEC = L::VEC, U = kJoinAhead;
+    for (; b < until; b += step) {
         uint32_t found[U];
         float v[U][VEC];
 #pragma unroll
@@ -502,9 +518,79 @@ __global__ void __launch_bounds__(kSumThreads) embed_join_kernel(SumParams p) {
 #pragma unroll
             for (int j = 0; j < VEC; ++j) sum[j] += over ? 0.0f : v[i][j];
         }
-        if (over) break;
+        if (over) return true;
     }
-    write_sum<L>(p, key, c, sum);
+    return until >= p.blocks;
+}
+
+// Tokens that begin in one of the workgroup's blocks and go on: their partial sums
+// in order.  Of a token that goes on for more than kJoinShort blocks the rest is
+// added by all threads, the sums of blocks side by side taking turns, and theirs
+// joined in order.
+constexpr int kJoinShort = 4 * kJoinAhead;
+
+template <typename L>
+__global__ void __launch_bounds__(kSumThreads) embed_join_kernel(SumParams p) {
+    constexpr int VEC = L::VEC;
+    __shared__ uint32_t goes_on;
+    __shared__ float sums[kSumThreads][VEC];
+    const int tile = blockIdx.x % (uint32_t)p.columns;
+    const int side = threadIdx.x / (uint32_t)p.lanes, beside = kSumThreads / p.lanes;
+    const int64_t first = blockIdx.x / (uint32_t)p.columns * (int64_t)beside;
+    const int column = (tile * p.lanes + (int)threadIdx.x % p.lanes) * VEC;
+    const Columns<L> c(column < p.width ? column : 0, p.width);
+    if (threadIdx.x == 0) goes_on = 0;
+    __syncthreads();
+
+    const auto begins = [&](int64_t block, uint32_t* key) {
+        const int64_t from = block * p.block, end = from + p.block;
+        if (end >= p.n) return false;   // the last block
+        *key = p.keys[end];
+        return *key < (uint32_t)p.vocab && p.keys[end - 1] == *key &&
+               !(from > 0 && p.keys[from - 1] == *key);   // began earlier
+    };
+    const int64_t block = first + side;
+    uint32_t key;
+    float sum[VEC];
+    if (begins(block, &key) && column < p.width) {
+        c.load_sum(p.partial + (block * 2 + 1) * p.partial_stride, sum);
+        const int64_t until = block + 1 + kJoinShort;
+        if (add_partials<L>(p, key, block + 1, kJoinAhead, until < p.blocks ? until : p.blocks, c, sum))
+            write_sum<L>(p, key, c, sum);
+        else if (threadIdx.x % p.lanes == 0)
+            atomicOr(&goes_on, 1u << side);
+    }
+    __syncthreads();
+    uint32_t rest = goes_on;   // bits in ascending order, the same in every thread
+    while (rest != 0) {
+        const int at = __ffs(rest) - 1;
+        rest &= rest - 1;
+        const int64_t from = first + at;
+        begins(from, &key);
+        float more[VEC];
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) more[j] = 0.0f;
+        if (column < p.width)
+            add_partials<L>(p, key, from + 1 + kJoinShort + side * kJoinAhead, beside * kJoinAhead,
+                            p.blocks, c, more);
+        if (beside > 1) {
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) sums[threadIdx.x][j] = more[j];
+            __syncthreads();
+        }
+        if (side == at && column < p.width) {
+            if (beside > 1)
+                for (int i = 0; i < beside; ++i)
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j)
+                        sum[j] += sums[i * p.lanes + threadIdx.x % p.lanes][j];
+            else
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) sum[j] += more[j];
+            write_sum<L>(p, key, c, sum);
+        }
+        __syncthreads();
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -575,7 +661,8 @@ int sort_tokens(const ws_states& t, const ws_embed_grad_args& a, const EmbedGrad
         p.shift = pass * kDigitBits;
         share();
         v = launch(sort_count_kernel, plan.tiles + clears, kSortThreads, p, s);
-        if (v == WS_OK && plan.tiles > kScanTiles) v = launch(sort_scan_kernel, 1, kDigits, p, s);
+        if (v == WS_OK && plan.tiles > kScanTiles)
+            v = launch(sort_scan_kernel, kDigits / kScanDigits, kScanDigits * 64, p, s);
         share();
         if (v == WS_OK) v = launch(sort_place_kernel, plan.tiles + clears, kSortThreads, p, s);
         *where = to;
@@ -585,8 +672,10 @@ int sort_tokens(const ws_states& t, const ws_embed_grad_args& a, const EmbedGrad
 
 template <typename L>
 int run_sum(const EmbedGradPlan& plan, const SumParams& p, hipStream_t s) {
-    const int64_t groups = (int64_t)plan.blocks * plan.columns;
-    const int v = launch(embed_sum_kernel<L>, groups, kSumThreads, p, s);
+    const int64_t beside = kSumThreads / plan.lanes;
+    const int64_t groups = (plan.blocks + beside - 1) / beside * plan.columns;
+    const int v = plan.lanes >= 64 ? launch(embed_sum_kernel<L, true>, groups, kSumThreads, p, s)
+                                   : launch(embed_sum_kernel<L, false>, groups, kSumThreads, p, s);
     if (v != WS_OK || plan.blocks == 1) return v;
     return launch(embed_join_kernel<L>, groups, kSumThreads, p, s);
 }
@@ -663,6 +752,7 @@ extern "C" int ws_embed_grad(const ws_states* states, const ws_embed_grad_args* 
     p.block = plan.block;
     p.blocks = plan.blocks;
     p.columns = plan.columns;
+    p.lanes = plan.lanes;
     p.grad_f32 = args->grad_dtype == WS_DTYPE_F32;
     p.accumulate = args->accumulate;
     p.scale = args->scale;

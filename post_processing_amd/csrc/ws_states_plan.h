@@ -131,15 +131,20 @@ inline EmbedPlan plan_embed(const ws_states& t) {
 // workgroups are few (the rows of a block come one after the other).
 constexpr int kSortThreads = 1024, kSortTile = 2048, kDigitBits = 9, kDigits = 1 << kDigitBits;
 constexpr int kScanTiles = 64;     // up to here every tile sums the counts for itself
-constexpr int kMostBlocks = 8192, kLeastRows = 8, kBlockRows = 32, kSumGroups = 512;
-constexpr int kSumThreads = 256, kMostRows = WS_MAX_ROWS / kMostBlocks;
+constexpr int kScanDigits = 16;    // a cache line of them
+constexpr int kMostGroups = 8192, kLeastRows = 8, kBlockRows = 32, kSumGroups = 512;
+constexpr int kSumThreads = 256, kLeastLanes = 8;
+constexpr int kMostRows = kBlockRows * kSumThreads / kLeastLanes;   // of a workgroup
+static_assert(kMostRows >= WS_MAX_ROWS / kMostGroups, "a workgroup's rows");
 constexpr int kClearRows = 16;     // of the table, by one workgroup
 
 struct EmbedGradPlan {
     int32_t tiles = 0;
     int32_t passes = 0;
-    int32_t block = kBlockRows;    // sorted rows added by one workgroup
+    int32_t block = kBlockRows;    // sorted rows added one after the other
     int32_t blocks = 0;
+    int32_t lanes = kLeastLanes;   // threads to a block; the blocks of a workgroup lie
+                                   // side by side
     int32_t columns = 0;           // workgroups over a row's slots
     size_t keys_at[2] = {0, 0}, rows_at[2] = {0, 0}, counts_at = 0, partial_at = 0;
     size_t workspace = 0;
@@ -156,10 +161,13 @@ inline EmbedGradPlan plan_embed_grad(const ws_states& t, int32_t vocab) {
     int bits = 1;
     while ((vocab >> bits) != 0) ++bits;
     p.passes = (bits + kDigitBits - 1) / kDigitBits;
-    p.columns = (int32_t)((slots_in(t.width, t.dtype) + kSumThreads - 1) / kSumThreads);
-    int64_t block = n * p.columns / kSumGroups;
+    const int64_t slots = slots_in(t.width, t.dtype);
+    while (p.lanes < slots && p.lanes < kSumThreads) p.lanes *= 2;
+    p.columns = (int32_t)((slots + kSumThreads - 1) / kSumThreads);
+    const int64_t beside = kSumThreads / p.lanes, most = kMostGroups * beside;
+    int64_t block = n * p.columns / (kSumGroups * beside);
     block = block < kLeastRows ? kLeastRows : block > kBlockRows ? kBlockRows : block;
-    if (n > block * kMostBlocks) block = (n + kMostBlocks - 1) / kMostBlocks;
+    if (n > block * most) block = (n + most - 1) / most;
     p.block = (int32_t)block;
     p.blocks = (int32_t)((n + block - 1) / block);
     const size_t each = round16((size_t)n * 4);
@@ -170,7 +178,7 @@ inline EmbedGradPlan plan_embed_grad(const ws_states& t, int32_t vocab) {
         at += 2 * each;
     }
     p.counts_at = at;
-    if (p.tiles > 1) at += (size_t)p.tiles * kDigits * 4;
+    if (p.tiles > 1) at += (size_t)(p.tiles + 1) * kDigits * 4;   // and the tiles' sums
     // Two rows of FP32 sums a block: of the token that began before it, and of
     // the one that goes on behind it.
     p.partial_at = at;

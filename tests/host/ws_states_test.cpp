@@ -281,6 +281,9 @@ static void test_plans() {
                     CHECK((int64_t)g.tiles * ws::kSortTile >= rows);
                     CHECK((int64_t)g.blocks * g.block >= rows && (int64_t)(g.blocks - 1) * g.block < rows);
                     CHECK((int64_t)g.blocks * g.columns < (1ll << 31));
+                    CHECK(g.lanes >= ws::kLeastLanes && ws::kSumThreads % g.lanes == 0);
+                    CHECK(g.block * (ws::kSumThreads / g.lanes) <= ws::kMostRows);
+                    CHECK((int64_t)g.lanes * g.columns >= ws::slots_in(t.width, t.dtype));
                     CHECK(g.keys_at[1] % 16 == 0 && g.rows_at[1] % 16 == 0 && g.counts_at % 16 == 0 &&
                           g.partial_at % 16 == 0);
                 }

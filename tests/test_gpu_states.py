@@ -245,6 +245,26 @@ def test_embed_grad_runs(gpu_lib, ids):
         check_embed_grad("f32", ids, 20, 8, accumulate=accumulate)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,width", [(4000, 1), (3000, 9), (3000, 65), (2000, 130), (1500, 300),
+                                        (1200, 700), (700, 2100)])
+def test_embed_grad_long_runs(gpu_lib, dtype, rows, width):
+    """Tokens that go on for many blocks of rows, from blocks side by side or apart."""
+    rng = np.random.default_rng(rows)
+    ids = np.sort(rng.integers(0, 30, rows))
+    ids[rows // 8:] = np.where(np.arange(rows - rows // 8) < rows // 2, 31, 33)
+    check_embed_grad(dtype, rng.permutation(ids), width, 40, scale=0.3, seed=width)
+
+
+@pytest.mark.parametrize("rows,width,vocab", [(131072, 2, 700), (131073, 3, 5), (140000, 33, 50000),
+                                              (300000, 8, 2)])
+def test_embed_grad_many_rows(gpu_lib, rows, width, vocab):
+    rng = np.random.default_rng(rows)
+    ids = rng.integers(-1, vocab, rows)
+    ids[rng.random(rows) < 0.4] = vocab // 2
+    check_embed_grad("bf16", ids, width, vocab, grad_dtype="f32")
+
+
 def test_embed_grad_without_rows(gpu_lib):
     import torch
     held = torch.full((5, 6), 3.0, device=_dev())
@@ -354,6 +374,17 @@ def test_norm_rows(gpu_lib, dtype, rows):
     check_norm(rng.normal(size=(rows, 129)), dtype, weight=dtype)
 
 
+NARROW = [(1, 8), (3, 16), (7, 31), (8, 64), (9, 33), (15, 9), (17, 64), (2, 65), (3, 128), (4, 129),
+          (5, 256), (31, 200), (1001, 40), (40000, 33), (20000, 130)]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,width", NARROW)
+def test_norm_narrow_rows(gpu_lib, dtype, rows, width):
+    rng = np.random.default_rng(rows + width)
+    check_norm(rng.normal(size=(rows, width)) * 2 - 1, dtype, weight=dtype, pad=rows % 4)
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("pad,shift", [(1, 0), (3, 5), (0, 1), (8, 8), (7, 3)])
 @pytest.mark.parametrize("width", [5, 203, 2050])
@@ -374,17 +405,6 @@ def test_norm_weights(gpu_lib, weight, bias, width):
 def test_norm_in_place(gpu_lib, width):
     rng = np.random.default_rng(4)
     check_norm(rng.normal(size=(9, width)), "f16", in_place=True, pad=2)
-
-
-NARROW = [(1, 8), (3, 16), (7, 31), (8, 64), (9, 33), (15, 9), (17, 64), (2, 65), (3, 128), (4, 129),
-          (5, 256), (31, 200), (1001, 40), (40000, 33), (20000, 130)]
-
-
-@pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("rows,width", NARROW)
-def test_norm_narrow_rows(gpu_lib, dtype, rows, width):
-    rng = np.random.default_rng(rows + width)
-    check_norm(rng.normal(size=(rows, width)) * 2 - 1, dtype, weight=dtype, pad=rows % 4)
 
 
 @pytest.mark.parametrize("dtype", TYPES)
