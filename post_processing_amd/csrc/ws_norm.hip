@@ -44,6 +44,22 @@ struct NormParams {
 // two rows a wave).
 constexpr int group_threads(int nt) { return nt < 64 ? 64 : nt; }
 
+// A product that its uses all see rounded: fused into a subtraction here and not
+// there, the mean would be two numbers, and the deviations' sum that of one of them.
+__device__ __forceinline__ float rounded(float v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
+// Has the compiler unpack the slots again instead of keeping twice the registers
+// (4,096 x 32,768 BF16 142 us, 154 unpacked; 4,096 x 20,000 98 and 117).
+template <int R>
+__device__ __forceinline__ void stay_packed(uint4 (&w)[R]) {
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+        asm volatile("" : "+v"(w[i].x), "+v"(w[i].y), "+v"(w[i].z), "+v"(w[i].w));
+}
+
 template <typename L, int NT, int R>
 __global__ void __launch_bounds__(group_threads(NT)) norm_kernel(NormParams p) {
     using Elem = typename L::Elem;
@@ -66,28 +82,35 @@ __global__ void __launch_bounds__(group_threads(NT)) norm_kernel(NormParams p) {
     slots.load(x + (row < p.rows ? row : p.rows - 1) * p.x_stride, w);
     // (a row side by side with the last one may lie behind it)
     for (int64_t base = (int64_t)blockIdx.x * kRows; base < p.rows; base += step, row += step) {
-        float v[R][VEC];
+        uint4 own[R];
 #pragma unroll
-        for (int i = 0; i < R; ++i) L::unpack(w[i], v[i]);
+        for (int i = 0; i < R; ++i) own[i] = w[i];
         const int64_t next = row + step;
         slots.load(x + (next < p.rows ? next : p.rows - 1) * p.x_stride, w);
         float sum = 0.0f;
 #pragma unroll
-        for (int i = 0; i < R; ++i)
+        for (int i = 0; i < R; ++i) {
+            float v[VEC];
+            L::unpack(own[i], v);
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) sum += slots.mine(i, j) ? v[i][j] : 0.0f;
-        const float mean = group_sum<NT>(sum, first) * p.inv_width;
+            for (int j = 0; j < VEC; ++j) sum += slots.mine(i, j) ? v[j] : 0.0f;
+        }
+        const float mean = rounded(group_sum<NT>(sum, first) * p.inv_width);
+        if constexpr (!kHold) stay_packed(own);
         float2 far = make_float2(0.0f, 0.0f);
 #pragma unroll
-        for (int i = 0; i < R; ++i)
+        for (int i = 0; i < R; ++i) {
+            float v[VEC];
+            L::unpack(own[i], v);
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
-                v[i][j] -= mean;
-                const float d = slots.mine(i, j) ? v[i][j] : 0.0f;
+                const float d = slots.mine(i, j) ? v[j] - mean : 0.0f;
                 far.x += d;
                 far.y = fmaf(d, d, far.y);
             }
+        }
         far = group_sums<NT>(far, second);
+        if constexpr (!kHold) stay_packed(own);
         const float shift = far.x * p.inv_width;
         const float var = fmaxf(far.y * p.inv_width - shift * shift, 0.0f);
         const float inverse = 1.0f / sqrtf(var + p.eps);
@@ -96,22 +119,23 @@ __global__ void __launch_bounds__(group_threads(NT)) norm_kernel(NormParams p) {
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             if (!slots.any(i)) continue;
-            if constexpr (kHold) {
+            float v[VEC], g_own[VEC], b_own[VEC];
+            L::unpack(own[i], v);
+            if constexpr (!kHold) {
+                if (p.weight) load_either<L>(p.weight, p.weight_f32, slots.at[i], p.width, g_own);
+                if (p.bias) load_either<L>(p.bias, p.weight_f32, slots.at[i], p.width, b_own);
+            }
 #pragma unroll
-                for (int j = 0; j < VEC; ++j)
-                    v[i][j] = fmaf((v[i][j] - shift) * inverse, g[i][j], b[i][j]);
-            } else {
-                float gi[VEC], bi[VEC];
-                if (p.weight) load_either<L>(p.weight, p.weight_f32, slots.at[i], p.width, gi);
-                if (p.bias) load_either<L>(p.bias, p.weight_f32, slots.at[i], p.width, bi);
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    v[i][j] = (v[i][j] - shift) * inverse;
-                    if (p.weight) v[i][j] *= gi[j];
-                    if (p.bias) v[i][j] += bi[j];
+            for (int j = 0; j < VEC; ++j) {
+                v[j] = (v[j] - mean - shift) * inverse;
+                if constexpr (kHold) {
+                    v[j] = fmaf(v[j], g[i][j], b[i][j]);
+                } else {
+                    if (p.weight) v[j] *= g_own[j];
+                    if (p.bias) v[j] += b_own[j];
                 }
             }
-            store_loose<L>(y + row * p.y_stride + slots.at[i], L::pack(v[i]));
+            store_loose<L>(y + row * p.y_stride + slots.at[i], L::pack(v));
         }
     }
 }
@@ -136,7 +160,7 @@ __global__ void __launch_bounds__(NT) norm_long_kernel(NormParams p) {
 #pragma unroll
         for (int j = 0; j < VEC; ++j) sum += v[j];
     }
-    float mean = group_sum<NT>(sum, waves[0]) * p.inv_width;
+    const float mean = rounded(group_sum<NT>(sum, waves[0]) * p.inv_width);
     float left = 0.0f, square = 0.0f;
     for (int c = first; c < p.width; c += NT * VEC) {
         float v[VEC];
