@@ -73,8 +73,9 @@ __global__ void __launch_bounds__(kLookupThreads) embed_kernel(EmbedParams p) {
 // 134 read and 47 of sums written (4.0 TB/s): the sort with the zeros 46, the sums 57
 // (while the zeros still drain), the join 9.  Leaving out the zeros of rows that are
 // named would save 45 MB but cost as much: every clearing workgroup would read all
-// tokens first (129 us).  777 rows take 17 us: three launches, each a chain of
-// latencies (sort 7.8, sums 5.7, join 3.6).
+// tokens first (129 us).  Sorted, 777 x 1,000 FP32 rows take 18 us: three launches, each
+// a chain of latencies (sort 7.8, sums 5.7, join 3.6); few rows go without
+// (embed_few_kernel).
 
 struct ClearParams {
     void* table;
@@ -593,6 +594,147 @@ __global__ void __launch_bounds__(kSumThreads) embed_join_kernel(SumParams p) {
     }
 }
 
+// Few rows, without a sort, in one launch.  A workgroup a row (and a tile of the
+// columns) reads all tokens and lists the rows of its own row's; if its row is the
+// first of them, it adds them: p.lanes threads a row, and the shares of the rows that
+// lie side by side joined in order.  Further workgroups write zeros into the rows that
+// no token names, and read all tokens for that.  Two latencies one after the other
+// (tokens, rows) and the workgroups' turns bound it (777 x 1,000 FP32 into 5,003 rows
+// 9.7 us; with 1,024 threads a workgroup 8.8, but 13.2 instead of 7.6 for 1,000 x 64
+// into 50,000, whose many clearing workgroups then wait for room).
+struct FewParams {
+    SumParams sum;
+    const int32_t* ids;
+    ClearParams clear;
+    int32_t groups;   // of sums
+};
+
+constexpr int kFewEach = kFewRows / kSumThreads;   // tokens a thread reads
+
+template <typename L>
+__device__ __forceinline__ void clear_unnamed(const FewParams& few, int group) {
+    using Elem = typename L::Elem;
+    constexpr int VEC = L::VEC;
+    const ClearParams& p = few.clear;
+    __shared__ uint32_t named;
+    const int first = p.from + group * kClearRows;
+    if (threadIdx.x == 0) named = 0;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kFewEach; ++k) {
+        const int i = k * kSumThreads + (int)threadIdx.x;
+        const uint32_t at = i < few.sum.n ? (uint32_t)few.ids[i] - (uint32_t)first : ~0u;
+        if (at < (uint32_t)kClearRows) atomicOr(&named, 1u << at);
+    }
+    __syncthreads();
+    const uint32_t skip = named;
+    const int lane = threadIdx.x & (p.lanes - 1), each = kSumThreads / p.lanes;
+    const int end = first + kClearRows < p.to ? first + kClearRows : p.to;
+    const float v[VEC] = {};
+    for (int row = first + (int)(threadIdx.x / (uint32_t)p.lanes); row < end; row += each) {
+        if (skip >> (row - first) & 1u) continue;
+        Elem* to = static_cast<Elem*>(p.table) + (int64_t)row * p.stride;
+        for (int c = lane * VEC; c < p.width; c += p.lanes * VEC)
+            store_columns<L>(to, c, p.width, v);
+    }
+}
+
+template <typename L>
+__global__ void __launch_bounds__(kSumThreads) embed_few_kernel(FewParams few) {
+    using Elem = typename L::Elem;
+    constexpr int VEC = L::VEC, U = 8;
+    if ((int)blockIdx.x >= few.groups) {
+        if (few.clear.f32) clear_unnamed<F32>(few, blockIdx.x - few.groups);
+        else clear_unnamed<BF16>(few, blockIdx.x - few.groups);
+        return;
+    }
+    const SumParams& p = few.sum;
+    __shared__ uint64_t found[kFewRows / 64];   // bit by bit, the rows of the token
+    __shared__ uint32_t rows[kFewRows];
+    __shared__ float sums[kSumThreads][VEC];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tile = blockIdx.x % (uint32_t)p.columns;
+    const int own = blockIdx.x / (uint32_t)p.columns;
+    const uint32_t key = (uint32_t)few.ids[own];
+    if (key >= (uint32_t)p.vocab) return;
+#pragma unroll
+    for (int k = 0; k < kFewEach; ++k) {
+        const int i = k * kSumThreads + tid;
+        const uint64_t set = __ballot(i < p.n && (uint32_t)few.ids[i < p.n ? i : own] == key);
+        if (lane == 0) found[i >> 6] = set;
+    }
+    __syncthreads();
+    int n = 0, before[kFewEach];
+    bool earlier = false;
+#pragma unroll
+    for (int w = 0; w < kFewRows / 64; ++w) {
+        const uint64_t set = found[w];
+#pragma unroll
+        for (int k = 0; k < kFewEach; ++k)
+            if (w == k * (kSumThreads / 64) + wave) before[k] = n + lanes_below(set);
+        n += __popcll(set);
+        const int upto = own - w * 64;   // bits of rows before its own
+        earlier |= upto >= 64 ? set != 0 : upto > 0 && (set & ((1ull << upto) - 1)) != 0;
+    }
+    if (earlier) return;   // another row's
+    if (n == 1) {
+        if (tid == 0) rows[0] = (uint32_t)own;
+    } else {
+#pragma unroll
+        for (int k = 0; k < kFewEach; ++k) {
+            const int w = k * (kSumThreads / 64) + wave;
+            if (found[w] >> lane & 1u) rows[before[k]] = (uint32_t)(w * 64 + lane);
+        }
+    }
+    __syncthreads();
+
+    const int side = tid / (uint32_t)p.lanes, beside = kSumThreads / p.lanes;
+    const int column = (tile * p.lanes + tid % p.lanes) * VEC;
+    const Columns<L> c(column < p.width ? column : 0, p.width);
+    const Elem* grad = static_cast<const Elem*>(p.grad_out);
+    float sum[VEC];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) sum[j] = 0.0f;
+    if (column < p.width) {
+        for (int base = side; base < n; base += U * beside) {
+            uint4 w[U];
+            uint32_t r[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+                r[i] = rows[base + i * beside < n ? base + i * beside : base];
+            if (c.short_row()) {
+#pragma unroll
+                for (int i = 0; i < U; ++i)
+                    w[i] = load_columns<L>(grad + (int64_t)r[i] * p.stride, 0, p.width);
+            } else {
+#pragma unroll
+                for (int i = 0; i < U; ++i) w[i] = c.load(grad + (int64_t)r[i] * p.stride);
+            }
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                if (base + i * beside >= n) break;
+                float v[VEC];
+                L::unpack(w[i], v);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) sum[j] += v[j];
+            }
+        }
+    }
+    const int shares = n < beside ? n : beside;
+    if (shares > 1) {
+        if (side < shares) {
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) sums[tid][j] = sum[j];
+        }
+        __syncthreads();
+        if (side == 0)
+            for (int i = 1; i < shares; ++i)
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) sum[j] += sums[i * p.lanes + tid][j];
+    }
+    if (side == 0 && column < p.width) write_sum<L>(p, key, c, sum);
+}
+
 // ---------------------------------------------------------------------------
 
 #define WS_BY_DTYPE(dtype, CALL)                             \
@@ -671,6 +813,17 @@ int sort_tokens(const ws_states& t, const ws_embed_grad_args& a, const EmbedGrad
 }
 
 template <typename L>
+int run_few(const ws_states& t, const ws_embed_grad_args& a, const SumParams& sum, hipStream_t s) {
+    FewParams p{};
+    p.sum = sum;
+    p.ids = a.ids;
+    p.groups = t.rows * sum.columns;
+    int64_t clears = 0;
+    if (!a.accumulate) p.clear = clear_of(t, a, 0, a.vocab, &clears);
+    return launch(embed_few_kernel<L>, p.groups + clears, kSumThreads, p, s);
+}
+
+template <typename L>
 int run_sum(const EmbedGradPlan& plan, const SumParams& p, hipStream_t s) {
     const int64_t beside = kSumThreads / plan.lanes;
     const int64_t groups = (plan.blocks + beside - 1) / beside * plan.columns;
@@ -733,14 +886,9 @@ extern "C" int ws_embed_grad(const ws_states* states, const ws_embed_grad_args* 
         const ws::ClearParams p = ws::clear_of(*states, *args, 0, args->vocab, &groups);
         return ws::launch(ws::clear_kernel, groups, ws::kSortThreads, p, s);
     }
-    int where = 0;
-    v = ws::sort_tokens(*states, *args, plan, s, &where);
-    if (v != WS_OK) return v;
     char* space = static_cast<char*>(args->workspace);
     ws::SumParams p{};
     p.grad_out = args->grad_out;
-    p.keys = reinterpret_cast<const uint32_t*>(space + plan.keys_at[where]);
-    p.rows = reinterpret_cast<const uint32_t*>(space + plan.rows_at[where]);
     p.grad_table = args->grad_table;
     p.partial = reinterpret_cast<float*>(space + plan.partial_at);
     p.stride = states->row_stride;
@@ -756,6 +904,16 @@ extern "C" int ws_embed_grad(const ws_states* states, const ws_embed_grad_args* 
     p.grad_f32 = args->grad_dtype == WS_DTYPE_F32;
     p.accumulate = args->accumulate;
     p.scale = args->scale;
+    if (plan.few) {
+#define CALL(L) return run_few<L>(*states, *args, p, s)
+        WS_BY_DTYPE(states->dtype, CALL);
+#undef CALL
+    }
+    int where = 0;
+    v = ws::sort_tokens(*states, *args, plan, s, &where);
+    if (v != WS_OK) return v;
+    p.keys = reinterpret_cast<const uint32_t*>(space + plan.keys_at[where]);
+    p.rows = reinterpret_cast<const uint32_t*>(space + plan.rows_at[where]);
 #define CALL(L) return run_sum<L>(plan, p, s)
     WS_BY_DTYPE(states->dtype, CALL);
 #undef CALL

@@ -137,8 +137,17 @@ constexpr int kSumThreads = 256, kLeastLanes = 8;
 constexpr int kMostRows = kBlockRows * kSumThreads / kLeastLanes;   // of a workgroup
 static_assert(kMostRows >= WS_MAX_ROWS / kMostGroups, "a workgroup's rows");
 constexpr int kClearRows = 16;     // of the table, by one workgroup
+// Few rows go without a sort, a workgroup a row and kSumThreads slots at most: 777 x
+// 1,000 FP32 into 5,003 rows 9.7 us, sorted 17.8; 64 x 4,096 BF16 9.7 and 18.5.  Not
+// where that makes more than kFewGroups workgroups, each of which reads all tokens
+// (512 x 16,384 BF16 27 us, sorted 23), nor where one token's rows could be more than
+// kFewBytes for one workgroup to add (1,024 x 4,096 BF16 of one token 98 us, sorted 32;
+// 777 x 1,000 FP32 34 and 25; 512 x 4,096 BF16 23 and 22).
+constexpr int kFewRows = 1024, kFewGroups = 2048;
+constexpr int64_t kFewBytes = 2 << 20;
 
 struct EmbedGradPlan {
+    bool few = false;              // one launch without a sort
     int32_t tiles = 0;
     int32_t passes = 0;
     int32_t block = kBlockRows;    // sorted rows added one after the other
@@ -164,6 +173,16 @@ inline EmbedGradPlan plan_embed_grad(const ws_states& t, int32_t vocab) {
     const int64_t slots = slots_in(t.width, t.dtype);
     while (p.lanes < slots && p.lanes < kSumThreads) p.lanes *= 2;
     p.columns = (int32_t)((slots + kSumThreads - 1) / kSumThreads);
+    if (n <= kFewRows) {
+        int32_t lanes = p.lanes;   // few, for a token of many rows is one workgroup's work
+        while (lanes > 64 && n * ((slots + lanes / 2 - 1) / (lanes / 2)) <= kFewGroups) lanes /= 2;
+        const int64_t columns = (slots + lanes - 1) / lanes;
+        p.few = n * columns <= kFewGroups && n * lanes * 16 <= kFewBytes;
+        if (p.few) {
+            p.lanes = lanes;
+            p.columns = (int32_t)columns;
+        }
+    }
     const int64_t beside = kSumThreads / p.lanes, most = kMostGroups * beside;
     int64_t block = n * p.columns / (kSumGroups * beside);
     block = block < kLeastRows ? kLeastRows : block > kBlockRows ? kBlockRows : block;

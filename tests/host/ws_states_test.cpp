@@ -284,6 +284,7 @@ static void test_plans() {
                     CHECK(g.lanes >= ws::kLeastLanes && ws::kSumThreads % g.lanes == 0);
                     CHECK(g.block * (ws::kSumThreads / g.lanes) <= ws::kMostRows);
                     CHECK((int64_t)g.lanes * g.columns >= ws::slots_in(t.width, t.dtype));
+                    CHECK(!g.few || (rows <= ws::kFewRows && rows * g.columns <= ws::kFewGroups));
                     CHECK(g.keys_at[1] % 16 == 0 && g.rows_at[1] % 16 == 0 && g.counts_at % 16 == 0 &&
                           g.partial_at % 16 == 0);
                 }

@@ -245,6 +245,19 @@ def test_embed_grad_runs(gpu_lib, ids):
         check_embed_grad("f32", ids, 20, 8, accumulate=accumulate)
 
 
+@pytest.mark.parametrize("dtype,grad_dtype", [("bf16", "bf16"), ("f16", "f32"), ("f32", "f32")])
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("rows,width", [(1, 1), (5, 3), (64, 64), (65, 9), (130, 70), (640, 20), (200, 700),
+                                        (100, 2100), (1023, 33), (1024, 260), (1025, 33)])
+def test_embed_grad_few_rows(gpu_lib, dtype, grad_dtype, accumulate, rows, width):
+    """One token of many rows, tokens of one, of some, and rows that name none."""
+    rng = np.random.default_rng(rows + width)
+    ids = rng.integers(-2, 50, rows)
+    ids[rng.random(rows) < 0.3] = 17
+    check_embed_grad(dtype, ids, width, 47, scale=1.3, grad_dtype=grad_dtype, accumulate=accumulate,
+                     pad=rows % 3, seed=rows)
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("rows,width", [(4000, 1), (3000, 9), (3000, 65), (2000, 130), (1500, 300),
                                         (1200, 700), (700, 2100)])
@@ -258,7 +271,7 @@ def test_embed_grad_long_runs(gpu_lib, dtype, rows, width):
 
 @pytest.mark.parametrize("rows,width,vocab", [(131072, 2, 700), (131073, 3, 5), (140000, 33, 50000),
                                               (300000, 8, 2)])
-def test_embed_grad_many_rows(gpu_lib, rows, width, vocab):
+def test_embed_grad_many_tiles(gpu_lib, rows, width, vocab):
     rng = np.random.default_rng(rows)
     ids = rng.integers(-1, vocab, rows)
     ids[rng.random(rows) < 0.4] = vocab // 2
