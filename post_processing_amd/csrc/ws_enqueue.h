@@ -21,14 +21,19 @@ inline int device_ready(int32_t device) {
 
 // Enqueues one kernel; its parameters are one struct, copied by the call.
 template <typename P>
-int launch(void (*kernel)(P), int64_t groups, int threads, const P& params, hipStream_t s,
-           size_t lds = 0) {
+int launch_grid(void (*kernel)(P), dim3 groups, int threads, const P& params, hipStream_t s,
+                size_t lds = 0) {
     P copy = params;
     void* args[] = {&copy};
-    const hipError_t e =
-        hipLaunchKernel(reinterpret_cast<const void*>(kernel), dim3((uint32_t)groups),
-                        dim3((uint32_t)threads), args, lds, s);
+    const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(kernel), groups,
+                                         dim3((uint32_t)threads), args, lds, s);
     return e == hipSuccess ? WS_OK : WS_E_HIP;
+}
+
+template <typename P>
+int launch(void (*kernel)(P), int64_t groups, int threads, const P& params, hipStream_t s,
+           size_t lds = 0) {
+    return launch_grid(kernel, dim3((uint32_t)groups), threads, params, s, lds);
 }
 
 }  // namespace ws

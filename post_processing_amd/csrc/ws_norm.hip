@@ -148,7 +148,8 @@ __global__ void __launch_bounds__(NT) norm_long_kernel(NormParams p) {
     using Elem = typename L::Elem;
     constexpr int VEC = L::VEC;
     __shared__ float waves[3][NT / 64];
-    const int64_t row = blockIdx.x;
+    const int64_t row = (int64_t)blockIdx.y * kLongGroups + blockIdx.x;
+    if (row >= p.rows) return;
     const Elem* x = static_cast<const Elem*>(p.x) + row * p.x_stride;
     Elem* y = static_cast<Elem*>(p.y) + row * p.y_stride;
     const int first = threadIdx.x * VEC;
@@ -319,7 +320,8 @@ __global__ void __launch_bounds__(NT) norm_grad_long_kernel(NormGradParams p) {
     using Elem = typename L::Elem;
     constexpr int VEC = L::VEC;
     __shared__ float waves[2][NT / 64];
-    const int64_t row = blockIdx.x;
+    const int64_t row = (int64_t)blockIdx.y * kLongGroups + blockIdx.x;
+    if (row >= p.rows) return;
     const Elem* x = static_cast<const Elem*>(p.x) + row * p.x_stride;
     const Elem* gy = static_cast<const Elem*>(p.grad_y) + row * p.y_stride;
     Elem* gx = static_cast<Elem*>(p.grad_x) + row * p.grad_stride;
@@ -465,6 +467,13 @@ __global__ void __launch_bounds__(kJoinThreads) norm_join_kernel(NormGradParams 
         else { CALL(BF16); }                                 \
     } while (0)
 
+// A workgroup a row.  A side of a grid has less than 2^32 threads, which 2^22 rows
+// of 1,024 would not be.
+dim3 long_grid(int64_t rows) {
+    return rows <= kLongGroups ? dim3((uint32_t)rows)
+                               : dim3(kLongGroups, (uint32_t)((rows + kLongGroups - 1) / kLongGroups));
+}
+
 template <typename L>
 int run_norm(const ws_states& t, const NormParams& p, hipStream_t s) {
     const NormPlan plan = plan_layernorm(t);
@@ -482,8 +491,9 @@ int run_norm(const ws_states& t, const NormParams& p, hipStream_t s) {
     PICK(1024, 2);
     PICK(1024, 4);
 #undef PICK
-    if (t.width < L::VEC) return launch(norm_long_kernel<L, 64>, t.rows, 64, p, s);
-    return launch(norm_long_kernel<L, kLongThreads>, t.rows, kLongThreads, p, s);
+    const dim3 grid = long_grid(t.rows);
+    if (t.width < L::VEC) return launch_grid(norm_long_kernel<L, 64>, grid, 64, p, s);
+    return launch_grid(norm_long_kernel<L, kLongThreads>, grid, kLongThreads, p, s);
 }
 
 template <typename L, bool SUMS>
@@ -515,10 +525,11 @@ int run_norm_grad(const ws_states& t, const NormGradPlan& plan, const NormGradPa
         if (sums)
             v = launch(norm_columns_kernel<L, kNormThreads>, (int64_t)plan.columns * plan.groups,
                        kNormThreads, p, s);
+        const dim3 grid = long_grid(t.rows);
         if (v == WS_OK && p.grad_x)
             v = t.width < L::VEC
-                    ? launch(norm_grad_long_kernel<L, 64>, t.rows, 64, p, s)
-                    : launch(norm_grad_long_kernel<L, kLongThreads>, t.rows, kLongThreads, p, s);
+                    ? launch_grid(norm_grad_long_kernel<L, 64>, grid, 64, p, s)
+                    : launch_grid(norm_grad_long_kernel<L, kLongThreads>, grid, kLongThreads, p, s);
     }
     if (v != WS_OK || !sums) return v;
     return launch(norm_join_kernel<L>, 2 * ((p.width + kJoinColumns - 1) / kJoinColumns),

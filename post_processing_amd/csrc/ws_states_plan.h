@@ -264,7 +264,7 @@ inline int validate_layernorm_grad(const ws_states* t, const ws_layernorm_grad_a
     return WS_OK;
 }
 
-constexpr int kNormThreads = 256, kLongThreads = 1024;
+constexpr int kNormThreads = 256, kLongThreads = 1024, kLongGroups = 1 << 20;
 
 // Rows held in registers: `held` slots by each of `threads` threads (less than a
 // wave: rows side by side in one), `groups` workgroups that take rows in turn.  0:

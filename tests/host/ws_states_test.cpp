@@ -288,6 +288,8 @@ static void test_plans() {
                     CHECK(g.keys_at[1] % 16 == 0 && g.rows_at[1] % 16 == 0 && g.counts_at % 16 == 0 &&
                           g.partial_at % 16 == 0);
                 }
+                const ws::NormPlan f = ws::plan_layernorm(t);
+                CHECK(f.held == 0 || (f.groups >= 1 && f.groups <= rows));
                 const ws::NormGradPlan n = ws::plan_layernorm_grad(t);
                 CHECK(n.groups >= 1 && n.groups <= rows);
                 CHECK(n.workspace >= (size_t)n.groups * 2 * 4 * (size_t)width);

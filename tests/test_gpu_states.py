@@ -532,6 +532,14 @@ def test_norm_grad_in_place(gpu_lib, in_place, width):
                     in_place=in_place)
 
 
+def test_norm_more_rows_than_workgroups(gpu_lib):
+    """Rows of less than a slot, some of which share a workgroup."""
+    rng = np.random.default_rng(1)
+    x, grad = rng.normal(size=(2, (1 << 20) + 3, 3))
+    check_norm(x, "bf16", weight="bf16")
+    check_norm_grad(x, grad, "bf16", weight="bf16")
+
+
 def test_norm_grad_without_rows(gpu_lib):
     import torch
     gw, gb = torch.full((70,), 3.0, device=_dev()), torch.full((70,), 3.0, device=_dev())
