@@ -32,9 +32,11 @@ struct NormParams {
 // deviations' own sum takes back the mean's rounding, which a row far from 0 would
 // otherwise carry into its variance and its result.
 //
-// Rows up to a few thousand elements: the next row is on its way while one is
-// worked on, weights stay in registers where there is room (read again for every
-// row, FP32 weights are four times a BF16 row's own bytes), and each element is
+// Rows up to 65,536 bytes: the next row is on its way while one is worked on,
+// weights stay in registers but for 1,024 threads' four 16-bit slots (8,200 BF16
+// elements: 80 us for 8,183 rows with them read again, 57 with 512 threads' three
+// slots and theirs; 32,768 elements: 105 us for 2,048 with 512 threads, 74), and each
+// element is
 // read and written once (counted: 134.5 MB read, 134.8 written for 16,384 x 4,096
 // BF16).  HBM bounds it: 52.5 us for that, 5.1 TB/s, the rate of a large copy; three
 // passes over the row in a workgroup a row took 75.7.  64 rows take 3.9 us: a
@@ -64,7 +66,7 @@ template <typename L, int NT, int R>
 __global__ void __launch_bounds__(group_threads(NT)) norm_kernel(NormParams p) {
     using Elem = typename L::Elem;
     constexpr int VEC = L::VEC;
-    constexpr bool kHold = R * VEC <= 16;
+    constexpr bool kHold = NT <= 512 || R * VEC <= 16;   // the weights too
     constexpr int kRows = group_threads(NT) / NT;   // side by side
     __shared__ float first[kRows > 1 ? 1 : NT / 64];
     __shared__ float2 second[kRows > 1 ? 1 : NT / 64];
@@ -485,9 +487,13 @@ int run_norm(const ws_states& t, const NormParams& p, hipStream_t s) {
     PICK(32, 1);
     PICK(64, 1);
     PICK(64, 2);
+    PICK(192, 1);
     PICK(256, 1);
     PICK(256, 2);
+    PICK(256, 3);
     PICK(512, 2);
+    PICK(512, 3);
+    PICK(512, 6);
     PICK(1024, 2);
     PICK(1024, 4);
 #undef PICK
@@ -508,9 +514,16 @@ int run_norm_grad_held(const NormGradPlan& plan, const NormGradParams& p, hipStr
     PICK(64, 2);
     PICK(256, 1);
     PICK(256, 2);
+    PICK(256, 3);
     PICK(512, 2);
+    PICK(512, 3);
+    if constexpr (L::VEC == 4) {   // of 16 bits they would not fit the registers
+        PICK(512, 5);
+        PICK(512, 6);
+        PICK(512, 8);
+    }
 #undef PICK
-    return launch(norm_grad_kernel<L, 1024, 2, SUMS>, plan.groups, 1024, p, s);
+    return launch(norm_grad_kernel<L, 512, 4, SUMS>, plan.groups, 512, p, s);
 }
 
 template <typename L>

@@ -275,22 +275,25 @@ struct NormPlan {
     int32_t groups = 0;
 };
 
-// Waves a CU has at work at a time, four or more to a SIMD.
-constexpr int64_t kNormWaves = 256 * 16;
+// Waves at work at a time, four to a SIMD.
+constexpr int32_t kNormCus = 256;
+constexpr int64_t kNormWaves = kNormCus * 16;
 
 inline NormPlan plan_held(const ws_states& t, int64_t most) {
     NormPlan p;
     const int64_t slots = slots_in(t.width, t.dtype);
     if (slots > most || t.width < 16 / logit_bytes(t.dtype)) return p;
-    p.threads = slots <= 8      ? 8
-                : slots <= 16   ? 16
-                : slots <= 32   ? 32
-                : slots <= 128  ? 64
-                : slots <= 512  ? 256
-                : slots <= 1024 ? 512
-                                : 1024;
-    p.held = slots <= p.threads ? 1 : slots <= 2 * p.threads ? 2 : 4;
-    if (p.threads >= 512 && p.held < 2) p.held = 2;
+    // (Thread counts between powers of two leave waves' room unused past 192: 384 and
+    // 768 threads with two slots each took 67 and 78 us for 5,120 and 12,288 BF16
+    // elements, 56 and 56 with three of 256 and 512.)
+    struct Shape { int16_t threads, held; };
+    constexpr Shape kShapes[] = {{8, 1},   {16, 1},  {32, 1},  {64, 1},  {64, 2},   {192, 1}, {256, 1},
+                                 {256, 2}, {256, 3}, {512, 2}, {512, 3}, {1024, 2}, {512, 6}, {1024, 4}};
+    for (const Shape& shape : kShapes) {
+        p.threads = shape.threads;
+        p.held = shape.held;
+        if (p.threads * p.held >= slots) break;
+    }
     const int64_t beside = p.threads < 64 ? 64 / p.threads : 1;
     const int64_t most_groups = kNormWaves / (p.threads < 64 ? 1 : p.threads / 64);
     const int64_t groups = (t.rows + beside - 1) / beside;
@@ -315,7 +318,16 @@ struct NormGradPlan {
 
 inline NormGradPlan plan_layernorm_grad(const ws_states& t) {
     NormGradPlan p;
-    const NormPlan held = plan_held(t, 2048);
+    NormPlan held = plan_held(t, t.dtype == WS_DTYPE_F32 ? 4096 : 2048);
+    // The sums fill the registers of 1,024 threads with two slots each: 12,288 BF16
+    // elements 122 us for 5,461 rows, 89 with three of 512 threads.
+    if (held.threads == 192) held.threads = 256;
+    if (held.threads > 256) {
+        held.threads = 512;
+        held.held = (int32_t)((slots_in(t.width, t.dtype) + 511) / 512);
+        if (held.held == 7) held.held = 8;
+        if (held.held > 2 && held.groups > kNormCus) held.groups = kNormCus;
+    }
     p.threads = held.threads;
     p.held = held.held;
     if (t.rows == 0) {
