@@ -36,9 +36,8 @@ struct NormParams {
 // weights stay in registers but for 1,024 threads' four 16-bit slots (8,200 BF16
 // elements: 80 us for 8,183 rows with them read again, 57 with 512 threads' three
 // slots and theirs; 32,768 elements: 105 us for 2,048 with 512 threads, 74), and each
-// element is
-// read and written once (counted: 134.5 MB read, 134.8 written for 16,384 x 4,096
-// BF16).  HBM bounds it: 52.5 us for that, 5.1 TB/s, the rate of a large copy; three
+// element is read and written once (counted: 134.5 MB read, 134.8 written for 16,384
+// x 4,096 BF16).  HBM bounds it: 52.5 us for that, 5.1 TB/s, the rate of a large copy; three
 // passes over the row in a workgroup a row took 75.7.  64 rows take 3.9 us: a
 // launch, one row's latency and two sums over four waves.
 // NT threads to a row; rows of less than a wave's slots lie side by side in one,
@@ -54,7 +53,7 @@ __device__ __forceinline__ float rounded(float v) {
 }
 
 // Has the compiler unpack the slots again instead of keeping twice the registers
-// (4,096 x 32,768 BF16 142 us, 154 unpacked; 4,096 x 20,000 98 and 117).
+// (4,096 x 32,768 BF16 142 us, 154 unpacked).
 template <int R>
 __device__ __forceinline__ void stay_packed(uint4 (&w)[R]) {
 #pragma unroll

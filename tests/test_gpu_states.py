@@ -532,6 +532,17 @@ def test_norm_grad_in_place(gpu_lib, in_place, width):
                     in_place=in_place)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,width", [(3, 1500), (3, 6001), (3, 10300), (2, 12288), (2, 14000), (2, 20000),
+                                        (2, 24600), (1500, 1100), (1100, 4200), (600, 8203), (300, 10300)])
+def test_norm_threads_and_slots(gpu_lib, dtype, rows, width):
+    """Rows of every number of slots a thread, and more rows than workgroups."""
+    rng = np.random.default_rng(rows + width)
+    x, grad = rng.normal(size=(2, rows, width))
+    check_norm(x + 0.5, dtype, weight=dtype)
+    check_norm_grad(x + 0.5, grad, dtype, weight=dtype)
+
+
 def test_norm_more_rows_than_workgroups(gpu_lib):
     """Rows of less than a slot, some of which share a workgroup."""
     rng = np.random.default_rng(1)
