@@ -164,4 +164,4 @@ def sample(z, u, tau, k=0, p=1.0, q=0.0):
     kept, w = kept_tokens(z, tau, k, p, q)
     upto = np.cumsum(w)
     at = min(int((upto <= u * upto[-1]).sum()), len(kept) - 1)
-    return int(kept[at]), float(np.log(w[at] / upto[-1]))
+    return int(kept[at]), float(np.log(w[at] / w.sum()))   # (summed in pairs)
