@@ -503,9 +503,10 @@ int run_norm(const ws_states& t, const NormParams& p, hipStream_t s) {
 
 template <typename L, bool SUMS>
 int run_norm_grad_held(const NormGradPlan& plan, const NormGradParams& p, hipStream_t s) {
+    const int64_t groups = SUMS ? plan.groups : plan.row_groups;
 #define PICK(NT, R)                                  \
     if (plan.threads == NT && plan.held == R)        \
-    return launch(norm_grad_kernel<L, NT, R, SUMS>, plan.groups, group_threads(NT), p, s)
+    return launch(norm_grad_kernel<L, NT, R, SUMS>, groups, group_threads(NT), p, s)
     PICK(8, 1);
     PICK(16, 1);
     PICK(32, 1);
@@ -522,7 +523,7 @@ int run_norm_grad_held(const NormGradPlan& plan, const NormGradParams& p, hipStr
         PICK(512, 8);
     }
 #undef PICK
-    return launch(norm_grad_kernel<L, 512, 4, SUMS>, plan.groups, 512, p, s);
+    return launch(norm_grad_kernel<L, 512, 4, SUMS>, groups, 512, p, s);
 }
 
 template <typename L>

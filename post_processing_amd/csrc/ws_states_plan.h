@@ -305,14 +305,17 @@ inline NormPlan plan_layernorm(const ws_states& t) { return plan_held(t, 4096); 
 
 // Sums over the rows: `groups` workgroups' sums of every column, then their sum.
 // Workgroups of one wave are four times as many: 65,536 x 1,024 BF16 takes 116 us
-// with 512 of them, 88 with 2,048.
-constexpr int64_t kColumnGroups = 512;
+// with 512 of them, 88 with 2,048.  Each has kLeastEach rows (or the joining takes
+// longer than the rows: 300 x 4,096 BF16 13.5 us with one a group, 11.4 with four, 4,000
+// x 256 13.5 and 11.0), but where there are few at all.
+constexpr int64_t kColumnGroups = 512, kLeastEach = 4, kFewSums = 256;
 
 struct NormGradPlan {
     int32_t threads = kNormThreads;
     int32_t held = 0;
     int32_t columns = 1;   // of rows that are not held: workgroups over the columns
     int32_t groups = 1;    // over the rows
+    int32_t row_groups = 0;   // of rows that are held, without sums
     size_t workspace = 0;
 };
 
@@ -334,7 +337,11 @@ inline NormGradPlan plan_layernorm_grad(const ws_states& t) {
         p.groups = 0;
     } else if (p.held > 0) {
         const int64_t most = p.threads <= 64 ? 4 * kColumnGroups : kColumnGroups;
-        p.groups = (int32_t)(held.groups < most ? held.groups : most);
+        int64_t each = (t.rows + most - 1) / most;
+        if (each < kLeastEach && t.rows >= kFewSums) each = kLeastEach;
+        const int64_t groups = (t.rows + each - 1) / each;
+        p.groups = (int32_t)(groups < held.groups ? groups : held.groups);
+        p.row_groups = held.groups;
     } else {
         p.columns = (int32_t)((slots_in(t.width, t.dtype) + kNormThreads - 1) / kNormThreads);
         int64_t groups = kColumnGroups / p.columns;

@@ -292,6 +292,7 @@ static void test_plans() {
                 CHECK(f.held == 0 || (f.groups >= 1 && f.groups <= rows));
                 const ws::NormGradPlan n = ws::plan_layernorm_grad(t);
                 CHECK(n.groups >= 1 && n.groups <= rows);
+                CHECK(n.held == 0 || (n.row_groups >= n.groups && n.row_groups <= rows));
                 CHECK(n.workspace >= (size_t)n.groups * 2 * 4 * (size_t)width);
                 CHECK(n.held == 0 || (int64_t)n.threads * n.held >= ws::slots_in(t.width, t.dtype));
             }
