@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(kLookupThreads) embed_kernel(EmbedParams p) {
 //
 // Tokens are sorted by a stable radix sort, a digit of kDigitBits a pass: every
 // tile counts its digits, and from all tiles' counts puts its tokens where they
-// belong; up to kSortTile tokens are sorted by one workgroup in LDS.  (Counting a
+// belong (two tiles count all tokens for themselves, a launch less); up to kSortTile tokens are sorted by one workgroup in LDS.  (Counting a
 // pass's digits while the pass before places them saves a launch, but its atomics
 // wait behind the zeros: 16,384 tokens 27 us instead of 16.)  Then blocks of sorted
 // rows are added, each thread its columns: a token whose rows lie in one block is
@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(kLookupThreads) embed_kernel(EmbedParams p) {
 // rows 552 and 134).  The table's zeros are written by workgroups beside the sort's,
 // whose few workgroups wait on latency.
 //
-// Bytes bound it: 16,384 rows into 32,768 x 4,096 BF16, 112 us for 268 MB of zeros,
+// Bytes bound it: 16,384 rows into 32,768 x 4,096 BF16, 114 us for 268 MB of zeros,
 // 134 read and 47 of sums written (4.0 TB/s): the sort with the zeros 46, the sums 57
 // (while the zeros still drain), the join 9.  Leaving out the zeros of rows that are
 // named would save 45 MB but cost as much: every clearing workgroup would read all
@@ -267,7 +267,23 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortParams p) 
     }
     // Where the tile's tokens of a digit go.
     uint32_t at = 0, total = 0;
-    if (tid < kDigits && p.tiles > kScanTiles) {
+    if (p.tiles <= kOwnTiles) {   // counted here, all tiles
+        uint32_t* all = tile.next[0];
+        uint32_t* earlier = tile.next[1];
+        if (tid < kDigits) all[tid] = earlier[tid] = 0;
+        __syncthreads();
+        for (int i = tid; i < p.n; i += kSortThreads) {
+            const uint32_t d = digit_of(key_of(p, i), p.shift);
+            atomicAdd(&all[d], 1u);
+            if (i < (int)blockIdx.x * kSortTile) atomicAdd(&earlier[d], 1u);
+        }
+        __syncthreads();
+        if (tid < kDigits) {
+            total = all[tid];
+            at = earlier[tid];
+        }
+        __syncthreads();   // read before rank_tile clears them
+    } else if (tid < kDigits && p.tiles > kScanTiles) {
         at = p.counts[(int64_t)blockIdx.x * kDigits + tid];
         total = p.counts[(int64_t)p.tiles * kDigits + tid];
     } else if (tid < kDigits) {
@@ -496,7 +512,7 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(SumParams p) {
 // The sum of the token's partial sums of blocks from `b` on, kJoinAhead of them at a
 // time and `step` from one time to the next, until the token ends (true) or the
 // block `until`.
-constexpr int kJoinAhead = 8;
+constexpr int kJoinAhead = 16;
 
 template <typename L>
 __device__ __forceinline__ bool add_partials(const SumParams& p, uint32_t key, int64_t b,
@@ -528,7 +544,7 @@ __device__ __forceinline__ bool add_partials(const SumParams& p, uint32_t key, i
 // in order.  Of a token that goes on for more than kJoinShort blocks the rest is
 // added by all threads, the sums of blocks side by side taking turns, and theirs
 // joined in order.
-constexpr int kJoinShort = 4 * kJoinAhead;
+constexpr int kJoinShort = kJoinAhead;
 
 template <typename L>
 __global__ void __launch_bounds__(kSumThreads) embed_join_kernel(SumParams p) {
@@ -780,7 +796,8 @@ int sort_tokens(const ws_states& t, const ws_embed_grad_args& a, const EmbedGrad
     p.vocab = a.vocab;
     p.tiles = plan.tiles;
     p.passes = plan.passes;
-    const int64_t steps = plan.tiles == 1 ? 1 : 2 * plan.passes;
+    const bool counted = plan.tiles > kOwnTiles;
+    const int64_t steps = plan.tiles == 1 ? 1 : (counted ? 2 : 1) * plan.passes;
     int64_t clears = 0, step = 0;
     const auto share = [&] {
         if (!a.accumulate)
@@ -801,8 +818,10 @@ int sort_tokens(const ws_states& t, const ws_embed_grad_args& a, const EmbedGrad
         p.keys_out = keys[to];
         p.rows_out = rows[to];
         p.shift = pass * kDigitBits;
-        share();
-        v = launch(sort_count_kernel, plan.tiles + clears, kSortThreads, p, s);
+        if (counted) {
+            share();
+            v = launch(sort_count_kernel, plan.tiles + clears, kSortThreads, p, s);
+        }
         if (v == WS_OK && plan.tiles > kScanTiles)
             v = launch(sort_scan_kernel, kDigits / kScanDigits, kScanDigits * 64, p, s);
         share();
