@@ -70,8 +70,8 @@ __global__ void __launch_bounds__(kLookupThreads) embed_kernel(EmbedParams p) {
 // whose few workgroups wait on latency.
 //
 // Bytes bound it: 16,384 rows into 32,768 x 4,096 BF16, 114 us for 268 MB of zeros,
-// 134 read and 47 of sums written (4.0 TB/s): the sort with the zeros 46, the sums 57
-// (while the zeros still drain), the join 9.  Leaving out the zeros of rows that are
+// 134 read and 47 of sums written (4.0 TB/s): the sort with the zeros 45, the sums 58
+// (while the zeros still drain), the join 10.  Leaving out the zeros of rows that are
 // named would save 45 MB but cost as much: every clearing workgroup would read all
 // tokens first (129 us).  Sorted, 777 x 1,000 FP32 rows take 18 us: three launches, each
 // a chain of latencies (sort 7.8, sums 5.7, join 3.6); few rows go without
