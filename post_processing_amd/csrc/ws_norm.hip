@@ -52,6 +52,19 @@ __device__ __forceinline__ float rounded(float v) {
     return v;
 }
 
+// A row's statistics from its first mean and the sums of the deviations from it and of
+// their squares: `shift` takes back the first mean's rounding.  Comparisons keep what the
+// formulas carry: the variance of a row that holds a NaN or an infinity is NaN (where a
+// maximum with 0 would make it 0), and the mean of one whose infinities have one sign is
+// that infinity, not its sum with deviations' that are NaN.
+__device__ __forceinline__ ws_norm_stats row_stats(float mean, float left, float square,
+                                                   const NormParams& p, float& shift) {
+    shift = left * p.inv_width;
+    const float var = square * p.inv_width - shift * shift;
+    const float inverse = 1.0f / sqrtf((var < 0.0f ? 0.0f : var) + p.eps);
+    return {__builtin_isnan(shift) ? mean : mean + shift, inverse};
+}
+
 // Has the compiler unpack the slots again instead of keeping twice the registers
 // (4,096 x 32,768 BF16 142 us, 154 unpacked).
 template <int R>
@@ -112,11 +125,11 @@ __global__ void __launch_bounds__(group_threads(NT)) norm_kernel(NormParams p) {
         }
         far = group_sums<NT>(far, second);
         if constexpr (!kHold) stay_packed(own);
-        const float shift = far.x * p.inv_width;
-        const float var = fmaxf(far.y * p.inv_width - shift * shift, 0.0f);
-        const float inverse = 1.0f / sqrtf(var + p.eps);
+        float shift;
+        const ws_norm_stats stats = row_stats(mean, far.x, far.y, p, shift);
+        const float inverse = stats.inverse;
         if (kRows > 1 && row >= p.rows) continue;
-        if (p.stats && threadIdx.x % NT == 0) p.stats[row] = {mean + shift, inverse};
+        if (p.stats && threadIdx.x % NT == 0) p.stats[row] = stats;
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             if (!slots.any(i)) continue;
@@ -174,10 +187,12 @@ __global__ void __launch_bounds__(NT) norm_long_kernel(NormParams p) {
             square = fmaf(d, d, square);
         }
     }
-    const float shift = group_sum<NT>(left, waves[1]) * p.inv_width;
-    const float var = fmaxf(group_sum<NT>(square, waves[2]) * p.inv_width - shift * shift, 0.0f);
-    const float inverse = 1.0f / sqrtf(var + p.eps);
-    if (p.stats && threadIdx.x == 0) p.stats[row] = {mean + shift, inverse};
+    left = group_sum<NT>(left, waves[1]);
+    square = group_sum<NT>(square, waves[2]);
+    float shift;
+    const ws_norm_stats stats = row_stats(mean, left, square, p, shift);
+    const float inverse = stats.inverse;
+    if (p.stats && threadIdx.x == 0) p.stats[row] = stats;
     for (int c = first; c < p.width; c += NT * VEC) {
         float v[VEC], g[VEC], b[VEC];
         L::unpack(load_columns<L>(x, c, p.width), v);

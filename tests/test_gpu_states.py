@@ -447,6 +447,57 @@ def test_norm_keeps_nan_and_infinity_in_their_rows(gpu_lib):
         assert torch.equal(y[[0, 3]], y2)
 
 
+def _rows_with_nan_and_infinity(width, seed=9):
+    """Clean rows among ones that hold a NaN, an infinity of either sign, and both."""
+    x = np.random.default_rng(seed).normal(size=(7, width))
+    x[1, width // 2] = np.nan
+    x[2, width - 1] = np.inf
+    x[3, 0] = -np.inf
+    x[5, 0], x[5, width - 1] = np.inf, -np.inf
+    return x
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("width", [3, 8, 50, 600, 1500, 8200, 16384, 40000, 70001])
+def test_norm_statistics_of_nan_and_infinity(gpu_lib, dtype, width):
+    """The statistics are the formulas' as well: a deviation of NaN, and a mean that is
+    the infinity where the row's infinities have one sign."""
+    x = _rows_with_nan_and_infinity(width)
+    with np.errstate(invalid="ignore"):
+        mean, inverse = os_.norm_stats(x, 1e-5)
+        assert np.isnan(inverse[[1, 2, 3, 5]]).all() and np.isfinite(inverse[[0, 4, 6]]).all()
+        assert mean[2] == np.inf and mean[3] == -np.inf and np.isnan(mean[[1, 5]]).all()
+        check_norm(x, dtype, weight=dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("width", [3, 50, 1500, 40000])
+def test_norm_grad_of_nan_and_infinity(gpu_lib, dtype, width):
+    """A forward's statistics of such rows: their gradients are NaN, the other rows'
+    those of a call without them, the weight's NaN and the bias's finite."""
+    import torch
+    x = torch.from_numpy(_rows_with_nan_and_infinity(width)).to(_dev()).to(_type(dtype))
+    g = torch.from_numpy(np.random.default_rng(1).normal(size=(7, width))).to(_dev()).to(_type(dtype))
+    clean = [0, 4, 6]
+
+    def step(x, g):
+        rows = x.shape[0]
+        shape = st.make_states(rows=rows, width=width, dtype=CODE[dtype])
+        y, gx = torch.empty_like(x), torch.empty_like(x)
+        stats = torch.empty(rows, 2, device=_dev())
+        gw, gb = torch.empty(width, device=_dev()), torch.empty(width, device=_dev())
+        run(st.LayerNorm(shape, x, y, stats=stats))
+        run(st.LayerNormGrad(shape, x, stats, g, weight_dtype=ws.DTYPE_F32, grad_x=gx, grad_weight=gw,
+                             grad_bias=gb))
+        return gx, gw, gb
+
+    gx, gw, gb = step(x, g)
+    want, _, _ = step(x[clean].contiguous(), g[clean].contiguous())
+    assert torch.equal(gx[clean], want)
+    assert torch.isnan(gx[[1, 2, 3, 5]]).all()
+    assert torch.isnan(gw).all() and torch.isfinite(gb).all()
+
+
 def check_norm_grad(x, grad, dtype, weight="f32", pad=0, shift=0, in_place=None, eps=1e-5,
                     parts=("grad_x", "grad_weight", "grad_bias")):
     import torch
