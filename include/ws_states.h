@@ -18,7 +18,9 @@
  * thread's current device.  Arguments are read during the call and not
  * retained; the buffers must stay until the stream has passed the call.  No
  * output may overlap an input, the workspace or another output, but where said
- * so.  Calls share no state: two may run at once from any threads and streams
+ * so.  The elements between a matrix's rows are not its own: an array may lie
+ * there, and another matrix of the same stride in bytes (matrices of different
+ * strides must lie apart, one wholly behind the other).  Calls share no state: two may run at once from any threads and streams
  * as long as neither writes what the other uses, the workspace included (two
  * captured graphs that may run at once need a workspace each).  A workspace
  * needs no initialisation and its contents do not matter between calls.

@@ -41,18 +41,20 @@ struct Extent {
     bool aligned() const { return aligned_to(at, (uintptr_t)logit_bytes(dtype)); }
 };
 
-// Whether no byte belongs to both: apart, or between each other's rows (equal
-// steps: two rows then lie a fixed distance modulo the step apart, wherever the
-// two extents meet).
+// Whether no byte belongs to both: apart, or between each other's rows.  An array (one
+// row) may lie in a matrix's padding.  Two matrices whose rows interleave need equal
+// steps, where two rows lie a fixed distance modulo the step apart, wherever the two
+// extents meet; of other steps they have to lie apart.
 inline bool disjoint(const Extent& a, const Extent& b) {
     if (a.rows == 0 || b.rows == 0) return true;
-    const uintptr_t apart = a.begin() < b.begin() ? b.begin() - a.begin() : a.begin() - b.begin();
-    if (apart >= (a.begin() < b.begin() ? a.bytes() : b.bytes())) return true;
-    const uintptr_t step = (uintptr_t)(a.stride * logit_bytes(a.dtype));
-    if (step != (uintptr_t)(b.stride * logit_bytes(b.dtype))) return false;
-    // From the lower one's row to the next row of the upper one, and back.
     const Extent& low = a.begin() < b.begin() ? a : b;
     const Extent& high = a.begin() < b.begin() ? b : a;
+    const uintptr_t apart = high.begin() - low.begin();
+    if (apart >= low.bytes()) return true;
+    if (low.rows == 1) return false;   // reaches the other's first row
+    const uintptr_t step = (uintptr_t)(low.stride * logit_bytes(low.dtype));
+    if (high.rows > 1 && step != (uintptr_t)(high.stride * logit_bytes(high.dtype))) return false;
+    // From the lower one's row to the next row of the upper one, and back.
     const uintptr_t into = apart % step;
     return into >= (uintptr_t)(low.width * logit_bytes(low.dtype)) &&
            step - into >= (uintptr_t)(high.width * logit_bytes(high.dtype));

@@ -263,6 +263,38 @@ static void test_disjoint() {
                             }
 }
 
+// An array against a matrix's rows, exactly: between them, over them, and behind the
+// last one.
+static void test_array_and_matrix() {
+    for (int64_t rows : {1, 2, 3})
+        for (int64_t width : {1, 3, 5})
+            for (int64_t stride : {5, 8})
+                for (int64_t n : {1, 2, 3, 4, 9, 40})
+                    for (uintptr_t b = 4; b < 240; b += 2)
+                        for (int32_t dtype : {WS_DTYPE_BF16, WS_DTYPE_F32}) {
+                            const ws::Extent m = {at<void>(100), rows, width, stride, WS_DTYPE_BF16};
+                            const ws::Extent array = {at<void>(b), 1, n, n, dtype};
+                            const uintptr_t end = b + (uintptr_t)(n * ws::logit_bytes(dtype));
+                            bool met = false;
+                            for (int64_t r = 0; r < rows; ++r) {
+                                const uintptr_t from = 100 + (uintptr_t)(r * stride * 2);
+                                met |= b < from + (uintptr_t)(width * 2) && from < end;
+                            }
+                            CHECK(ws::disjoint(m, array) == !met);
+                            CHECK(ws::disjoint(array, m) == !met);
+                        }
+    // Through the calls: indices, statistics and weights in the rows' padding.
+    YES(validate_embed, embed, a.ids = at<int32_t>(0x10000 + 200));
+    NO(validate_embed, embed, a.ids = at<int32_t>(0x10000 + 196));
+    NO(validate_embed, embed, a.ids = at<int32_t>(0x10000 + 228));
+    YES(validate_layernorm, norm, t.row_stride = 400; t.rows = 3; a.y_stride = 400;
+        a.stats = at<ws_norm_stats>(0x20000 + 200); a.weight = at<void>(0x20000 + 224));
+    NO(validate_layernorm, norm, t.row_stride = 400; t.rows = 3; a.y_stride = 400;
+       a.weight = at<void>(0x20000 + 404));
+    YES(validate_layernorm_grad, norm_grad, t.row_stride = 400; a.grad_weight = at<void>(0x10000 + 200));
+    NO(validate_layernorm_grad, norm_grad, t.row_stride = 400; a.grad_weight = at<void>(0x10000 + 404));
+}
+
 static void test_plans() {
     for (int32_t dtype : {WS_DTYPE_F32, WS_DTYPE_F16, WS_DTYPE_BF16})
         for (int64_t rows : {1ll, 2ll, 31ll, 2048ll, 2049ll, 100000ll, 1ll << 22})
@@ -340,6 +372,7 @@ int main(int argc, char** argv) {
     test_norm();
     test_norm_grad();
     test_disjoint();
+    test_array_and_matrix();
     test_plans();
     std::printf("%d failures\n", failures);
     return failures != 0;
