@@ -894,7 +894,7 @@ extern "C" int ws_embed_grad(const ws_states* states, const ws_embed_grad_args* 
     int v = ws::validate_embed_grad(states, args);
     if (v != WS_OK) return v;
     const ws::EmbedGradPlan plan = ws::plan_embed_grad(*states, args->vocab);
-    v = ws::validate_workspace(args->workspace, args->workspace_bytes, plan.workspace);
+    v = ws::validate_embed_grad_workspace(*states, *args, plan.workspace);
     if (v != WS_OK) return v;
     if (states->rows == 0 && args->accumulate) return WS_OK;
     v = ws::device_ready(states->device);

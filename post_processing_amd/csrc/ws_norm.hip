@@ -608,7 +608,7 @@ extern "C" int ws_layernorm_grad(const ws_states* states, const ws_layernorm_gra
     if (v != WS_OK) return v;
     const ws::NormGradPlan plan = ws::plan_layernorm_grad(*states);
     const bool sums = args->grad_weight || args->grad_bias;
-    v = ws::validate_workspace(args->workspace, args->workspace_bytes, sums ? plan.workspace : 0);
+    v = ws::validate_layernorm_grad_workspace(*states, *args, sums ? plan.workspace : 0);
     if (v != WS_OK) return v;
     v = ws::device_ready(states->device);
     if (v != WS_OK) return v;

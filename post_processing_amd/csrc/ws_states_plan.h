@@ -8,6 +8,7 @@
 #include <cmath>
 #include <cstddef>
 #include <cstdint>
+#include <initializer_list>
 
 #include "ws_logits_plan.h"
 #include "ws_states.h"
@@ -103,6 +104,28 @@ inline int validate_embed_grad(const ws_states* t, const ws_embed_grad_args* a) 
     const Extent ids = {a->ids, 1, t->rows, t->rows, WS_DTYPE_F32};
     if (!a->grad_out || !a->ids || !rows.aligned() || !ids.aligned()) return WS_E_INVALID_ARG;
     return disjoint(grad, rows) && disjoint(grad, ids) ? WS_OK : WS_E_INVALID_ARG;
+}
+
+// The `needed` bytes of workspace that a call writes: they must be there, and belong to
+// none of its other buffers.
+inline int validate_apart(const void* workspace, size_t given, size_t needed,
+                          std::initializer_list<Extent> buffers) {
+    const int v = validate_workspace(workspace, given, needed);
+    if (v != WS_OK || needed == 0) return v;
+    const int64_t words = (int64_t)((needed + 3) / 4);
+    const Extent space = {workspace, 1, words, words, WS_DTYPE_F32};
+    for (const Extent& b : buffers)
+        if (!disjoint(space, b)) return WS_E_INVALID_ARG;
+    return WS_OK;
+}
+
+// (with arguments that validate_embed_grad has passed)
+inline int validate_embed_grad_workspace(const ws_states& t, const ws_embed_grad_args& a,
+                                         size_t needed) {
+    return validate_apart(a.workspace, a.workspace_bytes, needed,
+                          {extent_of(t, a.grad_out, t.row_stride),
+                           {a.ids, 1, t.rows, t.rows, WS_DTYPE_F32},
+                           {a.grad_table, a.vocab, t.width, a.grad_stride, a.grad_dtype}});
 }
 
 inline int64_t slots_in(int32_t width, int32_t dtype) {
@@ -267,6 +290,20 @@ inline int validate_layernorm_grad(const ws_states* t, const ws_layernorm_grad_a
             !disjoint(*out, weight) || !disjoint(*out, stats))
             return WS_E_INVALID_ARG;
     return WS_OK;
+}
+
+// (with arguments that validate_layernorm_grad has passed)
+inline int validate_layernorm_grad_workspace(const ws_states& t, const ws_layernorm_grad_args& a,
+                                             size_t needed) {
+    const auto vector = [&](const void* p) -> Extent {
+        return {p, p ? 1 : 0, t.width, t.width, a.weight_dtype};
+    };
+    Extent gx = extent_of(t, a.grad_x, a.grad_x_stride);
+    if (!a.grad_x) gx.rows = 0;
+    return validate_apart(a.workspace, a.workspace_bytes, needed,
+                          {extent_of(t, a.x, t.row_stride), extent_of(t, a.grad_y, a.grad_y_stride), gx,
+                           {a.stats, 1, 2ll * t.rows, 2ll * t.rows, WS_DTYPE_F32}, vector(a.weight),
+                           vector(a.grad_weight), vector(a.grad_bias)});
 }
 
 constexpr int kNormThreads = 256, kLongThreads = 1024, kLongGroups = 1 << 20;

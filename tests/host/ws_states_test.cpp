@@ -295,6 +295,61 @@ static void test_array_and_matrix() {
     NO(validate_layernorm_grad, norm_grad, t.row_stride = 400; a.grad_weight = at<void>(0x10000 + 404));
 }
 
+// A workspace over a call's buffers, byte by byte around each of them.
+static void test_workspaces_lie_apart() {
+    const ws_states t = states();
+    const auto around = [](uintptr_t from, uintptr_t bytes, size_t needed, auto validate) {
+        for (const uintptr_t b : {from - needed, from + (bytes + 15) / 16 * 16})
+            CHECK(validate(b) == WS_OK);
+        for (const uintptr_t b : {from - needed + 16, from, from + (bytes - 1) / 16 * 16})
+            CHECK(validate(b) == WS_E_INVALID_ARG);
+    };
+    const size_t needed = 0x1000;
+    const uintptr_t rows = (7 * 128 + 100) * 2;
+    const auto embed = [&](uintptr_t b) {
+        ws_embed_grad_args a = embed_grad();
+        a.workspace = at<void>(b);
+        a.workspace_bytes = needed;
+        return ws::validate_embed_grad_workspace(t, a, needed);
+    };
+    around(0x10000, rows, needed, embed);                  // grad_out
+    around(0x80000, 8 * 4, needed, embed);                 // ids
+    around(0x100000, 50 * 100 * 4, needed, embed);         // grad_table
+    ws_embed_grad_args none = embed_grad();
+    CHECK(ws::validate_embed_grad_workspace(t, none, needed) == WS_E_INVALID_ARG);
+    CHECK(ws::validate_embed_grad_workspace(t, none, 0) == WS_OK);
+    // In the rows' padding, and a workspace larger than needed, whose rest is not used.
+    ws_states wide = states();
+    wide.row_stride = 0x2000;
+    none.workspace = at<void>(0x10000 + 0x100);
+    none.workspace_bytes = 0x100000;
+    CHECK(ws::validate_embed_grad_workspace(wide, none, needed) == WS_OK);
+    CHECK(ws::validate_embed_grad_workspace(wide, none, 0x4000) == WS_E_INVALID_ARG);
+
+    const auto norm = [&](uintptr_t b) {
+        ws_layernorm_grad_args a = norm_grad();
+        a.grad_weight = at<void>(0x50000);                 // apart from each other by more
+        a.grad_bias = at<void>(0x60000);                   // than the workspace
+        a.stats = at<ws_norm_stats>(0x70000);
+        a.workspace = at<void>(b);
+        a.workspace_bytes = needed;
+        return ws::validate_layernorm_grad_workspace(t, a, needed);
+    };
+    around(0x10000, rows, needed, norm);                   // x
+    around(0x20000, (7 * 100 + 100) * 2, needed, norm);    // grad_y
+    around(0x30000, (7 * 100 + 100) * 2, needed, norm);    // grad_x
+    around(0x50000, 400, needed, norm);
+    around(0x60000, 400, needed, norm);
+    around(0x70000, 64, needed, norm);                     // stats
+    around(0x80000, 400, needed, norm);                    // weight
+    ws_layernorm_grad_args parts = norm_grad();            // what is left out is nowhere
+    parts.grad_x = parts.grad_bias = nullptr;
+    parts.weight = nullptr;
+    parts.workspace = at<void>(0x80000 - needed + 0x100);
+    parts.workspace_bytes = needed;
+    CHECK(ws::validate_layernorm_grad_workspace(t, parts, needed) == WS_OK);
+}
+
 static void test_plans() {
     for (int32_t dtype : {WS_DTYPE_F32, WS_DTYPE_F16, WS_DTYPE_BF16})
         for (int64_t rows : {1ll, 2ll, 31ll, 2048ll, 2049ll, 100000ll, 1ll << 22})
@@ -373,6 +428,7 @@ int main(int argc, char** argv) {
     test_norm_grad();
     test_disjoint();
     test_array_and_matrix();
+    test_workspaces_lie_apart();
     test_plans();
     std::printf("%d failures\n", failures);
     return failures != 0;

@@ -108,6 +108,25 @@ def test_workspaces_are_checked(lib):
     assert call.submit() == ws.WS_E_INVALID_ARG
 
 
+def test_workspaces_over_other_buffers_are_refused(lib):
+    """Few rows and many, through the built library: a workspace that begins in, or
+    reaches into, what the call reads or writes."""
+    for rows in (40, 5000):
+        t = st.make_states(rows=rows, width=100)
+        need = st.embed_grad_workspace(t, 1000)
+        out, ids, table = 1 << 28, 1 << 27, 1 << 29
+        for at in (out, out + 16, out - need + 16, ids, table, table - 16):
+            call = st.EmbedGrad(t, out, ids, table, vocab=1000, workspace=at)
+            assert call._args.workspace_bytes >= need
+            assert call.submit() == ws.WS_E_INVALID_ARG, (rows, at)
+        need = st.layernorm_grad_workspace(t)
+        x, stats, gy, gx, weight, gw, gb = (i << 26 for i in range(1, 8))
+        for at in (x, stats, gy, gx, gx - need + 16, weight, gw, gb):
+            call = st.LayerNormGrad(t, x, stats, gy, grad_x=gx, weight=weight, grad_weight=gw,
+                                    grad_bias=gb, workspace=at)
+            assert call.submit() == ws.WS_E_INVALID_ARG, (rows, at)
+
+
 def test_binding_checks_tensors(lib):
     """Type, device, size and layout of tensors are refused in Python, before an
     address is taken (CPU tensors stand for a wrong device)."""
