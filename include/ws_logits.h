@@ -46,7 +46,9 @@
  * probability or loss, and its whole gradient).
  *
  * Errors: as in ws.h.  Everything the host can see is checked before anything
- * is enqueued; a call with 0 rows checks its arguments and enqueues nothing.
+ * is enqueued (of buffers that overlap, a gradient over its logits, and any of
+ * ws_sample's over what it writes; the others are the caller's to keep apart);
+ * a call with 0 rows checks its arguments and enqueues nothing.
  */
 #ifndef WS_LOGITS_H
 #define WS_LOGITS_H

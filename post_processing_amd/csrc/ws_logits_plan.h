@@ -8,7 +8,6 @@
 #include <cmath>
 #include <cstddef>
 #include <cstdint>
-#include <initializer_list>
 
 #include "ws_logits.h"
 
@@ -17,6 +16,38 @@ namespace ws {
 inline int64_t logit_bytes(int32_t dtype) { return dtype == WS_DTYPE_F32 ? 4 : 2; }
 
 inline bool aligned_to(const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+
+// A matrix of `rows` rows in memory.
+struct Extent {
+    const void* at;
+    int64_t rows, width, stride;   // elements
+    int32_t dtype;
+
+    uintptr_t begin() const { return (uintptr_t)at; }
+    uintptr_t bytes() const {
+        return rows == 0 ? 0 : (uintptr_t)(((rows - 1) * stride + width) * logit_bytes(dtype));
+    }
+    bool aligned() const { return aligned_to(at, (uintptr_t)logit_bytes(dtype)); }
+};
+
+// Whether no byte belongs to both: apart, or between each other's rows.  An array (one
+// row) may lie in a matrix's padding.  Two matrices whose rows interleave need equal
+// steps, where two rows lie a fixed distance modulo the step apart, wherever the two
+// extents meet; of other steps they have to lie apart.
+inline bool disjoint(const Extent& a, const Extent& b) {
+    if (a.rows == 0 || b.rows == 0) return true;
+    const Extent& low = a.begin() < b.begin() ? a : b;
+    const Extent& high = a.begin() < b.begin() ? b : a;
+    const uintptr_t apart = high.begin() - low.begin();
+    if (apart >= low.bytes()) return true;
+    if (low.rows == 1) return false;   // reaches the other's first row
+    const uintptr_t step = (uintptr_t)(low.stride * logit_bytes(low.dtype));
+    if (high.rows > 1 && step != (uintptr_t)(high.stride * logit_bytes(high.dtype))) return false;
+    // From the lower one's row to the next row of the upper one, and back.
+    const uintptr_t into = apart % step;
+    return into >= (uintptr_t)(low.width * logit_bytes(low.dtype)) &&
+           step - into >= (uintptr_t)(high.width * logit_bytes(high.dtype));
+}
 
 inline int validate_rows(const ws_rows* r) {
     if (!r) return WS_E_INVALID_ARG;
@@ -140,6 +171,40 @@ inline int validate_distill_grad(const ws_rows* r, const ws_distill_grad_args* a
     return validate_gradient(*r, a->logits, a->grad_logits, a->grad_stride);
 }
 
+inline int validate_workspace(const void* workspace, size_t given, size_t needed) {
+    if (needed == 0) return WS_OK;
+    if (!workspace || !aligned_to(workspace, 16) || given < needed) return WS_E_INVALID_ARG;
+    return WS_OK;
+}
+
+// The `needed` bytes of workspace that a call writes: they must be there, and belong to
+// none of its other buffers.
+inline int validate_apart(const void* workspace, size_t given, size_t needed,
+                          const Extent* buffers, int count) {
+    const int v = validate_workspace(workspace, given, needed);
+    if (v != WS_OK || needed == 0) return v;
+    const int64_t words = (int64_t)((needed + 3) / 4);
+    const Extent space = {workspace, 1, words, words, WS_DTYPE_F32};
+    for (int i = 0; i < count; ++i)
+        if (!disjoint(space, buffers[i])) return WS_E_INVALID_ARG;
+    return WS_OK;
+}
+
+// The buffers of a sampling call, what is left out being nowhere; the first
+// kSampleOutputs are written.
+constexpr int kSampleOutputs = 2, kSampleBuffers = 8;
+
+struct SampleBuffers {
+    Extent at[kSampleBuffers];
+
+    SampleBuffers(const ws_rows& r, const ws_sample_args& a) {
+        const void* arrays[] = {a.token, a.logprob, a.uniform, a.temperature, a.top_k, a.top_p, a.min_p};
+        for (int i = 0; i < kSampleBuffers - 1; ++i)
+            at[i] = {arrays[i], arrays[i] ? 1 : 0, r.rows, r.rows, WS_DTYPE_F32};
+        at[kSampleBuffers - 1] = {a.logits, r.rows, r.vocab, r.row_stride, r.dtype};
+    }
+};
+
 inline int validate_sample(const ws_rows* r, const ws_sample_args* a) {
     const int v = validate_rows(r);
     if (v != WS_OK) return v;
@@ -147,17 +212,19 @@ inline int validate_sample(const ws_rows* r, const ws_sample_args* a) {
     if (r->rows == 0) return WS_OK;
     if (!logits_ok(*r, a->logits)) return WS_E_INVALID_ARG;
     if (!a->uniform || !a->token) return WS_E_INVALID_ARG;
-    for (const void* p : {(const void*)a->uniform, (const void*)a->temperature,
-                          (const void*)a->top_k, (const void*)a->top_p, (const void*)a->min_p,
-                          (const void*)a->token, (const void*)a->logprob})
-        if (!aligned_to(p, 4)) return WS_E_INVALID_ARG;
+    const SampleBuffers buffers(*r, *a);
+    for (const Extent& b : buffers.at)
+        if (!b.aligned()) return WS_E_INVALID_ARG;
+    for (int i = 0; i < kSampleOutputs; ++i)
+        for (int j = i + 1; j < kSampleBuffers; ++j)
+            if (!disjoint(buffers.at[i], buffers.at[j])) return WS_E_INVALID_ARG;
     return WS_OK;
 }
 
-inline int validate_workspace(const void* workspace, size_t given, size_t needed) {
-    if (needed == 0) return WS_OK;
-    if (!workspace || !aligned_to(workspace, 16) || given < needed) return WS_E_INVALID_ARG;
-    return WS_OK;
+// (with arguments that validate_sample has passed)
+inline int validate_sample_workspace(const ws_rows& r, const ws_sample_args& a, size_t needed) {
+    const SampleBuffers buffers(r, a);
+    return validate_apart(a.workspace, a.workspace_bytes, needed, buffers.at, kSampleBuffers);
 }
 
 // ---------------------------------------------------------------------------

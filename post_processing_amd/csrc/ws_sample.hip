@@ -1465,7 +1465,7 @@ extern "C" int ws_sample(const ws_rows* rows, const ws_sample_args* args, void* 
     const ws_rows& r = *rows;
     if (r.rows == 0) return WS_OK;
     const ws::SamplePlan plan = ws::plan_sample(r);
-    v = ws::validate_workspace(args->workspace, args->workspace_bytes, plan.workspace);
+    v = ws::validate_sample_workspace(r, *args, plan.workspace);
     if (v != WS_OK) return v;
     v = ws::device_ready(r.device);
     if (v != WS_OK) return v;

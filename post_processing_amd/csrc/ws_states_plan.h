@@ -29,38 +29,6 @@ inline int validate_states(const ws_states* t) {
     return stride_ok(t->row_stride, t->width) ? WS_OK : WS_E_INVALID_ARG;
 }
 
-// A matrix of `rows` rows in memory.
-struct Extent {
-    const void* at;
-    int64_t rows, width, stride;   // elements
-    int32_t dtype;
-
-    uintptr_t begin() const { return (uintptr_t)at; }
-    uintptr_t bytes() const {
-        return rows == 0 ? 0 : (uintptr_t)(((rows - 1) * stride + width) * logit_bytes(dtype));
-    }
-    bool aligned() const { return aligned_to(at, (uintptr_t)logit_bytes(dtype)); }
-};
-
-// Whether no byte belongs to both: apart, or between each other's rows.  An array (one
-// row) may lie in a matrix's padding.  Two matrices whose rows interleave need equal
-// steps, where two rows lie a fixed distance modulo the step apart, wherever the two
-// extents meet; of other steps they have to lie apart.
-inline bool disjoint(const Extent& a, const Extent& b) {
-    if (a.rows == 0 || b.rows == 0) return true;
-    const Extent& low = a.begin() < b.begin() ? a : b;
-    const Extent& high = a.begin() < b.begin() ? b : a;
-    const uintptr_t apart = high.begin() - low.begin();
-    if (apart >= low.bytes()) return true;
-    if (low.rows == 1) return false;   // reaches the other's first row
-    const uintptr_t step = (uintptr_t)(low.stride * logit_bytes(low.dtype));
-    if (high.rows > 1 && step != (uintptr_t)(high.stride * logit_bytes(high.dtype))) return false;
-    // From the lower one's row to the next row of the upper one, and back.
-    const uintptr_t into = apart % step;
-    return into >= (uintptr_t)(low.width * logit_bytes(low.dtype)) &&
-           step - into >= (uintptr_t)(high.width * logit_bytes(high.dtype));
-}
-
 // The same rows of the same elements.
 inline bool same_rows(const Extent& a, const Extent& b) {
     return a.at == b.at && a.dtype == b.dtype && (a.stride == b.stride || a.rows <= 1);
@@ -106,26 +74,13 @@ inline int validate_embed_grad(const ws_states* t, const ws_embed_grad_args* a) 
     return disjoint(grad, rows) && disjoint(grad, ids) ? WS_OK : WS_E_INVALID_ARG;
 }
 
-// The `needed` bytes of workspace that a call writes: they must be there, and belong to
-// none of its other buffers.
-inline int validate_apart(const void* workspace, size_t given, size_t needed,
-                          std::initializer_list<Extent> buffers) {
-    const int v = validate_workspace(workspace, given, needed);
-    if (v != WS_OK || needed == 0) return v;
-    const int64_t words = (int64_t)((needed + 3) / 4);
-    const Extent space = {workspace, 1, words, words, WS_DTYPE_F32};
-    for (const Extent& b : buffers)
-        if (!disjoint(space, b)) return WS_E_INVALID_ARG;
-    return WS_OK;
-}
-
 // (with arguments that validate_embed_grad has passed)
 inline int validate_embed_grad_workspace(const ws_states& t, const ws_embed_grad_args& a,
                                          size_t needed) {
-    return validate_apart(a.workspace, a.workspace_bytes, needed,
-                          {extent_of(t, a.grad_out, t.row_stride),
-                           {a.ids, 1, t.rows, t.rows, WS_DTYPE_F32},
-                           {a.grad_table, a.vocab, t.width, a.grad_stride, a.grad_dtype}});
+    const Extent buffers[] = {extent_of(t, a.grad_out, t.row_stride),
+                              {a.ids, 1, t.rows, t.rows, WS_DTYPE_F32},
+                              {a.grad_table, a.vocab, t.width, a.grad_stride, a.grad_dtype}};
+    return validate_apart(a.workspace, a.workspace_bytes, needed, buffers, 3);
 }
 
 inline int64_t slots_in(int32_t width, int32_t dtype) {
@@ -300,10 +255,14 @@ inline int validate_layernorm_grad_workspace(const ws_states& t, const ws_layern
     };
     Extent gx = extent_of(t, a.grad_x, a.grad_x_stride);
     if (!a.grad_x) gx.rows = 0;
-    return validate_apart(a.workspace, a.workspace_bytes, needed,
-                          {extent_of(t, a.x, t.row_stride), extent_of(t, a.grad_y, a.grad_y_stride), gx,
-                           {a.stats, 1, 2ll * t.rows, 2ll * t.rows, WS_DTYPE_F32}, vector(a.weight),
-                           vector(a.grad_weight), vector(a.grad_bias)});
+    const Extent buffers[] = {extent_of(t, a.x, t.row_stride),
+                              extent_of(t, a.grad_y, a.grad_y_stride),
+                              gx,
+                              {a.stats, 1, 2ll * t.rows, 2ll * t.rows, WS_DTYPE_F32},
+                              vector(a.weight),
+                              vector(a.grad_weight),
+                              vector(a.grad_bias)};
+    return validate_apart(a.workspace, a.workspace_bytes, needed, buffers, 7);
 }
 
 constexpr int kNormThreads = 256, kLongThreads = 1024, kLongGroups = 1 << 20;

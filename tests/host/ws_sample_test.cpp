@@ -88,6 +88,56 @@ static void test_arguments() {
     YES(r.rows = 0; std::memset(&a, 0, sizeof a));
 }
 
+// Outputs and the workspace over each other buffer of the call, and beside it.
+static void test_buffers_lie_apart() {
+    const uintptr_t inputs[][2] = {{0x10000, 7 * 2048 + 2000}, {0x80000, 32}, {0x81000, 32},
+                                   {0x82000, 32}, {0x83000, 32}, {0x84000, 32}};
+    for (const auto& in : inputs) {
+        const uintptr_t first = in[0], end = in[0] + in[1];
+        for (const uintptr_t b : {first - 28, first, end - 4}) {
+            CHECK(with([&](ws_rows&, ws_sample_args& a) { a.token = at<int32_t>(b); }) == WS_E_INVALID_ARG);
+            CHECK(with([&](ws_rows&, ws_sample_args& a) { a.logprob = at<float>(b); }) == WS_E_INVALID_ARG);
+        }
+        for (const uintptr_t b : {first - 32, end}) {
+            CHECK(with([&](ws_rows&, ws_sample_args& a) { a.token = at<int32_t>(b); }) == WS_OK);
+            CHECK(with([&](ws_rows&, ws_sample_args& a) { a.logprob = at<float>(b); }) == WS_OK);
+        }
+    }
+    NO(a.logprob = at<float>(0x85000));                    // the tokens
+    NO(a.logprob = at<float>(0x85000 + 28));
+    YES(a.logprob = at<float>(0x85000 + 32));
+    YES(a.temperature = a.top_p = a.min_p = a.uniform);    // inputs may be one array
+    YES(a.logits = at<void>(0x80000));                     // and lie in each other
+    YES(a.token = at<int32_t>(0x10000 + 2000));            // the last row ends before the
+    NO(a.token = at<int32_t>(0x10000 + 2020));             // padding's 48 bytes do
+    NO(r.rows = 100; r.row_stride = 1000; a.token = at<int32_t>(0x10000 + 2000));
+
+    const ws_rows r = rows();
+    const size_t needed = 0x400;
+    const auto workspace = [&](uintptr_t b) {
+        ws_sample_args a = sample();
+        a.workspace = at<void>(b);
+        a.workspace_bytes = needed;
+        return ws::validate_sample_workspace(r, a, needed);
+    };
+    for (const uintptr_t first : {0x10000, 0x80000, 0x81000, 0x82000, 0x83000, 0x84000, 0x85000, 0x86000}) {
+        CHECK(workspace(first) == WS_E_INVALID_ARG);
+        CHECK(workspace(first - needed + 16) == WS_E_INVALID_ARG);
+        CHECK(workspace(first - needed) == WS_OK);
+    }
+    CHECK(workspace(0x85000 + 32) == WS_OK);
+    CHECK(workspace(0x10000 + 7 * 2048 + 2000) == WS_OK);
+    ws_sample_args few = sample();
+    few.logprob = nullptr;
+    few.temperature = nullptr;
+    few.workspace = at<void>(0x86000 - needed + 16);
+    few.workspace_bytes = needed;
+    CHECK(ws::validate_sample_workspace(r, few, needed) == WS_OK);
+    few.workspace = nullptr;
+    CHECK(ws::validate_sample_workspace(r, few, needed) == WS_E_INVALID_ARG);
+    CHECK(ws::validate_sample_workspace(r, few, 0) == WS_OK);
+}
+
 static void test_plans() {
     for (int32_t dtype : {WS_DTYPE_F32, WS_DTYPE_F16, WS_DTYPE_BF16})
         for (int64_t count : {1ll, 2ll, 15ll, 16ll, 17ll, 64ll, 256ll, 257ll, 512ll, 513ll, 1ll << 22})
@@ -124,6 +174,7 @@ int main(int argc, char** argv) {
         return 0;
     }
     test_arguments();
+    test_buffers_lie_apart();
     test_plans();
     std::printf("%d failures\n", failures);
     return failures != 0;

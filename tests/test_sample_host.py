@@ -70,6 +70,20 @@ def test_c_abi_refuses_before_it_touches_a_device(lib):
     assert lib.ws_sample(byref(none), byref(lg.SampleArgs()), None) == ws.WS_OK
 
 
+def test_outputs_over_other_buffers_are_refused(lib):
+    """Through the built library, a workspace among them."""
+    r = lg.make_rows(rows=4, vocab=100)
+    assert lg.Sample(r, 1 << 20, 1 << 21, (1 << 20) + 400).submit() == ws.WS_E_INVALID_ARG
+    assert lg.Sample(r, 1 << 20, 1 << 21, 1 << 21).submit() == ws.WS_E_INVALID_ARG
+    assert lg.Sample(r, 1 << 20, 1 << 21, 1 << 22,
+                     logprob=(1 << 22) + 12).submit() == ws.WS_E_INVALID_ARG
+    one = lg.make_rows(rows=1, vocab=131072, dtype=ws.DTYPE_BF16)
+    assert lg.sample_workspace(one) > 0
+    for at in (1 << 20, (1 << 20) + 262144 - 16, 1 << 21, 1 << 22):
+        call = lg.Sample(one, 1 << 20, 1 << 21, 1 << 22, workspace=at)
+        assert call.submit() == ws.WS_E_INVALID_ARG, at
+
+
 def test_binding_checks_tensors(lib):
     r = lg.make_rows(rows=4, vocab=100)
     meta = {"device": "meta"}
