@@ -12,6 +12,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "ws_logits_rows.h"
 
@@ -21,32 +22,18 @@ typedef uint32_t Slot2 __attribute__((ext_vector_type(4), aligned(2)));
 typedef uint32_t Slot4 __attribute__((ext_vector_type(4), aligned(4)));
 
 template <typename L>
+using LooseSlot = std::conditional_t<sizeof(typename L::Elem) == 2, Slot2, Slot4>;
+
+template <typename L>
 __device__ __forceinline__ uint4 load_loose(const typename L::Elem* p) {
-    Slot16 v;
-    if constexpr (sizeof(typename L::Elem) == 2) {
-        const Slot2* q = reinterpret_cast<const Slot2*>(p);
-        if constexpr (L::kStream) v = __builtin_nontemporal_load(q);
-        else v = *q;
-    } else {
-        const Slot4* q = reinterpret_cast<const Slot4*>(p);
-        if constexpr (L::kStream) v = __builtin_nontemporal_load(q);
-        else v = *q;
-    }
+    const Slot16 v = *reinterpret_cast<const LooseSlot<L>*>(p);
     return make_uint4(v.x, v.y, v.z, v.w);
 }
 
 template <typename L>
 __device__ __forceinline__ void store_loose(typename L::Elem* p, uint4 w) {
     const Slot16 v = {w.x, w.y, w.z, w.w};
-    if constexpr (sizeof(typename L::Elem) == 2) {
-        Slot2* q = reinterpret_cast<Slot2*>(p);
-        if constexpr (L::kStream) __builtin_nontemporal_store((Slot2)v, q);
-        else *q = v;
-    } else {
-        Slot4* q = reinterpret_cast<Slot4*>(p);
-        if constexpr (L::kStream) __builtin_nontemporal_store((Slot4)v, q);
-        else *q = v;
-    }
+    *reinterpret_cast<LooseSlot<L>*>(p) = v;
 }
 
 // Elements c .. c + VEC - 1 of a row of `width`, 0 behind it.
