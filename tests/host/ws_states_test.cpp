@@ -385,6 +385,35 @@ static void test_plans() {
             }
 }
 
+// Which launches the GPU tests' sizes take, so that each path stays tested: how many
+// tiles sort, the rows of a block, and the workgroups over a row.
+static void test_paths() {
+    struct Path { int32_t rows, width, dtype; bool few; int32_t tiles, block, columns; };
+    const Path paths[] = {
+        {150, 5000, WS_DTYPE_BF16, true, 1, 0, 0},     {203, 67, WS_DTYPE_BF16, true, 1, 0, 0},
+        {700, 520, WS_DTYPE_BF16, true, 1, 0, 0},      {777, 1000, WS_DTYPE_F32, true, 1, 0, 0},
+        {1025, 5000, WS_DTYPE_BF16, false, 1, 8, 3},   {1025, 5000, WS_DTYPE_F32, false, 1, 10, 5},
+        {1025, 1, WS_DTYPE_BF16, false, 1, 8, 1},      {1100, 67, WS_DTYPE_F16, false, 1, 8, 1},
+        {2100, 67, WS_DTYPE_F32, false, 2, 8, 1},      {4500, 67, WS_DTYPE_BF16, false, 3, 8, 1},
+        {1100, 20, WS_DTYPE_F32, false, 1, 8, 1},      {3000, 20, WS_DTYPE_F32, false, 2, 8, 1},
+        {5000, 20, WS_DTYPE_F32, false, 3, 8, 1},      {1100, 300, WS_DTYPE_F32, false, 1, 8, 1},
+        {5000, 300, WS_DTYPE_F16, false, 3, 8, 1},     {2100, 2051, WS_DTYPE_F32, false, 2, 12, 3},
+        {5000, 2051, WS_DTYPE_F32, false, 3, 29, 3},   {16384, 2100, WS_DTYPE_BF16, false, 8, 32, 2},
+        {262200, 1032, WS_DTYPE_BF16, false, 129, 33, 1}, {1500, 520, WS_DTYPE_BF16, false, 1, 8, 1},
+        {2100, 520, WS_DTYPE_BF16, false, 2, 8, 1},    {5000, 520, WS_DTYPE_BF16, false, 3, 8, 1},
+        {140000, 40, WS_DTYPE_BF16, false, 69, 8, 1},
+    };
+    for (const Path& path : paths) {
+        ws_states t = states();
+        t.rows = path.rows;
+        t.width = t.row_stride = path.width;
+        t.dtype = path.dtype;
+        const ws::EmbedGradPlan p = ws::plan_embed_grad(t, 900);
+        CHECK(p.few == path.few && p.tiles == path.tiles);
+        if (!p.few) CHECK(p.block == path.block && p.columns == path.columns);
+    }
+}
+
 static void layout() {
 #define SIZE(T) std::printf(#T " sizeof %zu\n", sizeof(T))
 #define FIELD(T, f) std::printf(#T " " #f " %zu\n", offsetof(T, f))
@@ -430,6 +459,7 @@ int main(int argc, char** argv) {
     test_array_and_matrix();
     test_workspaces_lie_apart();
     test_plans();
+    test_paths();
     std::printf("%d failures\n", failures);
     return failures != 0;
 }

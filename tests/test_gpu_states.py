@@ -320,6 +320,77 @@ def test_embed_grad_many_rows(gpu_lib):
     assert_close(out.double().cpu().numpy(), want, (38 + 8192) * E * size)
 
 
+# Past the few rows that go without a sort: which launches each of these sizes takes,
+# and its block of sorted rows, is held by the host test of the launch rules.
+
+
+@pytest.mark.parametrize("width", [1, 3, 8, 9, 255, 2048, 2051, 5000])
+def test_embed_grad_sorted_widths(gpu_lib, width):
+    rng = np.random.default_rng(width)
+    check_embed_grad("bf16", rng.integers(-1, 20, 1025), width, 20, grad_dtype="f32")
+    check_embed_grad("f32", rng.integers(-1, 400, 1025), width, 400)
+
+
+@pytest.mark.parametrize("pad,shift", [(1, 0), (3, 5), (0, 1), (8, 8), (7, 3)])
+@pytest.mark.parametrize("dtype,grad_dtype", [("bf16", "bf16"), ("f16", "f32"), ("f32", "f32")])
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("rows", [1100, 2100, 4500])
+def test_embed_grad_sorted_strides_and_accumulation(gpu_lib, rows, pad, shift, dtype, grad_dtype,
+                                                    accumulate):
+    rng = np.random.default_rng(pad + rows)
+    check_embed_grad(dtype, rng.integers(-1, 900, rows), 67, 900, scale=0.5, grad_dtype=grad_dtype,
+                     accumulate=accumulate, pad=pad, shift=shift)
+
+
+# (rows, width, type, rows of a block)
+BLOCKS = [(1100, 20, "f32", 8), (3000, 20, "f32", 8), (5000, 20, "f32", 8), (1100, 300, "f32", 8),
+          (5000, 300, "f16", 8), (2100, 2051, "f32", 12), (5000, 2051, "f32", 29),
+          (16384, 2100, "bf16", 32)]
+
+
+@pytest.mark.parametrize("rows,width,dtype,block", BLOCKS)
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_embed_grad_sorted_runs(gpu_lib, rows, width, dtype, block, accumulate):
+    """Runs of one token that end on a border of the blocks of sorted rows, a row before
+    it and a row behind it, and go on for as many blocks as are joined at a time, one
+    less and one more, and twice as many; a token of most rows, and rows that name none."""
+    ends = [block, 2 * block, 4 * block]                      # on the border, one block or two
+    ends += [5 * block - 1, 5 * block, 6 * block + 1, 7 * block]
+    for blocks in (3, 15, 16, 17, 18, 33):                    # from a border to a border
+        ends.append(ends[-1] + blocks * block)
+    ends.append(ends[-1] + 16 * block + 1)                    # behind the border, and back on it
+    ends.append(ends[-1] + 2 * block - 1)
+    assert ends[-1] % block == 0 and ends[-1] < rows - 8
+    counts = np.diff([0] + ends + [rows - 5])
+    ids = np.repeat(2 * np.arange(len(counts)), counts)       # every other token has no row
+    ids = np.concatenate([ids, [-1, 999, -1, 2 ** 31 - 1, -2 ** 31]])
+    ids = np.random.default_rng(rows).permutation(ids)
+    check_embed_grad(dtype, ids, width, 2 * len(counts) + 3, scale=0.7, accumulate=accumulate,
+                     seed=width)
+
+
+def test_embed_grad_blocks_past_the_most_workgroups(gpu_lib):
+    """So many rows that the blocks grow past their usual size (33 rows here)."""
+    import torch
+    rows, width, vocab = 262200, 1032, 30
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    ids = torch.randint(-1, vocab, (rows,), device=_dev(), generator=gen, dtype=torch.int32)
+    ids[torch.rand(rows, device=_dev(), generator=gen) < 0.4] = 7
+    grad = torch.randn(rows, width, device=_dev(), generator=gen).bfloat16()
+    out = torch.empty(vocab, width, device=_dev())
+    shape = st.make_states(rows=rows, width=width, dtype=ws.DTYPE_BF16)
+    run(st.EmbedGrad(shape, grad, ids, out, vocab=vocab, grad_dtype=ws.DTYPE_F32))
+    named = ids >= 0
+    at, exact = ids[named].long(), grad[named].double()
+    sums = lambda v: torch.zeros(vocab, width, device=_dev(),  # noqa: E731
+                                 dtype=torch.float64).index_add_(0, at, v)
+    want = sums(exact).cpu().numpy()
+    size = sums(exact.abs_()).cpu().numpy()
+    count = torch.bincount(at, minlength=vocab)[:, None].cpu().numpy()
+    # (float64's own sums are off by 2^-29 of this)
+    assert_close(out.double().cpu().numpy(), want, (count + 2) * E * size + E * np.abs(want))
+
+
 # ---------------------------------------------------------------------------
 # Layer norm.
 
@@ -683,6 +754,66 @@ def test_states_captured_and_replayed(gpu_lib):
         _run_all(twin, torch.cuda.current_stream().cuda_stream)
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(outs, twin_outs)), k
+
+
+# Gradients of the lookup that take a sort: in one workgroup's LDS, by two tiles that
+# count for themselves, by three that are counted first, and by more than the tiles that
+# add the counts themselves.
+SORTED = [(1500, 520, 900), (2100, 520, 900), (5000, 520, 900), (140000, 40, 900)]
+
+
+@pytest.mark.parametrize("rows,width,vocab", SORTED)
+def test_sorted_states_on_two_streams_at_once(gpu_lib, rows, width, vocab):
+    import torch
+    sets = [_many_calls(s, rows, width, vocab) for s in (1, 2)]
+    torch.cuda.synchronize()
+    for calls, _, _ in sets:
+        _run_all(calls, None)
+    torch.cuda.synchronize()
+    want = [[o.clone() for o in outs] for _, outs, _ in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _, outs, _ in sets:
+        for o in outs:
+            o.fill_(float("nan"))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for (calls, _, _), s in zip(sets, streams):
+            _run_all(calls, s.cuda_stream)
+    torch.cuda.synchronize()
+    for (_, outs, _), w in zip(sets, want):
+        assert all(torch.equal(a, b) for a, b in zip(outs, w))
+
+
+@pytest.mark.parametrize("rows,width,vocab", SORTED)
+def test_sorted_states_captured_and_replayed(gpu_lib, rows, width, vocab):
+    import torch
+    calls, outs, (table, ids, gy) = _many_calls(3, rows, width, vocab)
+    twin, twin_outs, (table2, ids2, gy2) = _many_calls(3, rows, width, vocab)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        _run_all(calls, torch.cuda.current_stream().cuda_stream)
+    for k in range(4):
+        gen = torch.Generator(device="cuda").manual_seed(10 + k)
+        table.copy_(torch.randn(table.shape, device=_dev(), generator=gen))
+        gy.copy_(torch.randn(gy.shape, device=_dev(), generator=gen))
+        ids.copy_(torch.randint(-1, vocab, ids.shape, device=_dev(), generator=gen))
+        if k == 2:
+            ids[: rows // 2] = 5                              # one token of half the rows
+        for a, b in ((table2, table), (gy2, gy), (ids2, ids)):
+            a.copy_(b)
+        for o in outs + twin_outs:
+            o.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        _run_all(twin, torch.cuda.current_stream().cuda_stream)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, twin_outs)), k
+        want = os_.embed_grad(outs[3].double().cpu().numpy(), ids.cpu().numpy(), vocab, 3.0)
+        size = os_.embed_grad(outs[3].double().abs().cpu().numpy(), ids.cpu().numpy(), vocab, 3.0)
+        count = torch.bincount(ids[ids >= 0].long(), minlength=vocab)[:, None].cpu().numpy()
+        tol = (count + 3) * E * size + HALF["bf16"] * np.abs(want) * (1 + E) + SMALLEST["bf16"]
+        assert_close(outs[-1].double().cpu().numpy(), want, np.where(count > 0, tol, 0.0))
 
 
 def test_states_refuse_another_device(gpu_lib):
