@@ -104,9 +104,9 @@ struct SortParams {
     ClearParams clear;         // by the workgroups behind the tiles
 };
 
-// Zeros: rows of the table, kClearRows a workgroup.
+// Zeros: rows of the table, kClearRows a workgroup, but for those whose bits `skip` has.
 template <typename L, int NT>
-__device__ __forceinline__ void clear_rows(const ClearParams& p, int group) {
+__device__ __forceinline__ void clear_rows(const ClearParams& p, int group, uint32_t skip = 0) {
     using Elem = typename L::Elem;
     constexpr int VEC = L::VEC;
     const int lane = threadIdx.x & (p.lanes - 1), each = NT / p.lanes;
@@ -114,6 +114,7 @@ __device__ __forceinline__ void clear_rows(const ClearParams& p, int group) {
     const int end = first + kClearRows < p.to ? first + kClearRows : p.to;
     const float v[VEC] = {};
     for (int row = first + (int)(threadIdx.x / (uint32_t)p.lanes); row < end; row += each) {
+        if (skip >> (row - first) & 1u) continue;
         Elem* to = static_cast<Elem*>(p.table) + (int64_t)row * p.stride;
         for (int c = lane * VEC; c < p.width; c += p.lanes * VEC)
             store_columns<L>(to, c, p.width, v);
@@ -629,11 +630,8 @@ constexpr int kFewEach = kFewRows / kSumThreads;   // tokens a thread reads
 
 template <typename L>
 __device__ __forceinline__ void clear_unnamed(const FewParams& few, int group) {
-    using Elem = typename L::Elem;
-    constexpr int VEC = L::VEC;
-    const ClearParams& p = few.clear;
     __shared__ uint32_t named;
-    const int first = p.from + group * kClearRows;
+    const int first = few.clear.from + group * kClearRows;
     if (threadIdx.x == 0) named = 0;
     __syncthreads();
 #pragma unroll
@@ -643,16 +641,7 @@ __device__ __forceinline__ void clear_unnamed(const FewParams& few, int group) {
         if (at < (uint32_t)kClearRows) atomicOr(&named, 1u << at);
     }
     __syncthreads();
-    const uint32_t skip = named;
-    const int lane = threadIdx.x & (p.lanes - 1), each = kSumThreads / p.lanes;
-    const int end = first + kClearRows < p.to ? first + kClearRows : p.to;
-    const float v[VEC] = {};
-    for (int row = first + (int)(threadIdx.x / (uint32_t)p.lanes); row < end; row += each) {
-        if (skip >> (row - first) & 1u) continue;
-        Elem* to = static_cast<Elem*>(p.table) + (int64_t)row * p.stride;
-        for (int c = lane * VEC; c < p.width; c += p.lanes * VEC)
-            store_columns<L>(to, c, p.width, v);
-    }
+    clear_rows<L, kSumThreads>(few.clear, group, named);
 }
 
 template <typename L>
@@ -752,13 +741,6 @@ __global__ void __launch_bounds__(kSumThreads) embed_few_kernel(FewParams few) {
 }
 
 // ---------------------------------------------------------------------------
-
-#define WS_BY_DTYPE(dtype, CALL)                             \
-    do {                                                     \
-        if ((dtype) == WS_DTYPE_F32) { CALL(F32); }          \
-        else if ((dtype) == WS_DTYPE_F16) { CALL(F16); }     \
-        else { CALL(BF16); }                                 \
-    } while (0)
 
 // Rows [from, to) of the table as a kernel clears them; `groups` workgroups.
 ClearParams clear_of(const ws_states& t, const ws_embed_grad_args& a, int from, int to,

@@ -476,13 +476,6 @@ __global__ void __launch_bounds__(kJoinThreads) norm_join_kernel(NormGradParams 
 
 // ---------------------------------------------------------------------------
 
-#define WS_BY_DTYPE(dtype, CALL)                             \
-    do {                                                     \
-        if ((dtype) == WS_DTYPE_F32) { CALL(F32); }          \
-        else if ((dtype) == WS_DTYPE_F16) { CALL(F16); }     \
-        else { CALL(BF16); }                                 \
-    } while (0)
-
 // A workgroup a row.  A side of a grid has less than 2^32 threads, which 2^22 rows
 // of 1,024 would not be.
 dim3 long_grid(int64_t rows) {

@@ -16,6 +16,14 @@
 
 #include "ws_logits_rows.h"
 
+// CALL(type) for the rows' element type.
+#define WS_BY_DTYPE(dtype, CALL)                             \
+    do {                                                     \
+        if ((dtype) == WS_DTYPE_F32) { CALL(F32); }          \
+        else if ((dtype) == WS_DTYPE_F16) { CALL(F16); }     \
+        else { CALL(BF16); }                                 \
+    } while (0)
+
 namespace ws {
 
 typedef uint32_t Slot2 __attribute__((ext_vector_type(4), aligned(2)));
