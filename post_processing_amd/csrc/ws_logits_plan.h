@@ -403,19 +403,26 @@ inline DistillPlan plan_distill(const ws_rows& r, int32_t mode, bool gradient, b
 // few, or long (the longest row's nucleus is then waited for: 1,024 x 131,072 BF16
 // with mixed settings 131 us, 166 with two rows of 512 threads); two of 512 where
 // rows come in more than one round and are shorter (2,000 x 32,768 FP16 mixed 77 us
-// and 115 with one of 1,024; 600 x 50,001 BF16 with the best 50 30 and 38), and up to
-// 512 rows of any length (300 x 50,001 FP32 31 and 38); 256 threads for rows that
-// give more no whole slot.
+// and 115 with one of 1,024; 600 x 50,001 BF16 with the best 50 30 and 38); 256
+// threads for rows that give more no whole slot.
+//
+// Up to 512 rows, one turn of 512 threads for two of 1,024: what reads the row once
+// gains, an undecided row's nucleus, whose list is as long as the workgroup, loses, the
+// more the longer the row.  Microseconds with 512 and 1,024, for all kept, mixed
+// settings and the best 50: 300 x 70,001 BF16 43 and 50, 80 and 64, 18 and 28; 300 x
+// 50,001 FP32 32 and 39, 69 and 51, 20 and 29; 300 x 131,072 BF16 56 and 57, 112 and
+// 89, 27 and 36; but 300 x 131,072 FP32 60 and 67, 132 and 98, 48 and 54, and 300 x
+// 200,003 BF16 85 and 94, 263 and 135, 34 and 42: 512 up to kSampleWide slots.
 constexpr int kMaxSampleParts = 32;
 constexpr int64_t kSampleSlots = 1024;   // of a part, at least
-constexpr int64_t kSampleShort = 1024, kSampleLong = 8192;   // slots of a row
+constexpr int64_t kSampleShort = 1024, kSampleLong = 8192, kSampleWide = 16384;   // slots of a row
 constexpr int kSampleGroups = 256;       // workgroups of 1,024 threads at work at a time
 constexpr int kStretchBytes = 24 + 64 * 4;
 
 inline int32_t sample_threads(int64_t rows, int64_t slots) {
     if (slots <= kSampleShort) return 256;
     if (rows <= kSampleGroups) return 1024;
-    return rows <= 2 * kSampleGroups || slots <= kSampleLong ? 512 : 1024;
+    return slots <= (rows <= 2 * kSampleGroups ? kSampleWide : kSampleLong) ? 512 : 1024;
 }
 
 struct SamplePlan {

@@ -161,6 +161,28 @@ static void test_plans() {
             }
 }
 
+// The threads of a row's workgroup, on both sides of each border of the rule.
+static void test_threads() {
+    struct Rule { int32_t rows, vocab, dtype, threads; };
+    const Rule rules[] = {
+        {1, 8192, WS_DTYPE_BF16, 256},      {5000, 4096, WS_DTYPE_F32, 256},
+        {256, 8193, WS_DTYPE_BF16, 1024},   {256, 200003, WS_DTYPE_F16, 1024},
+        {257, 8193, WS_DTYPE_BF16, 512},    {300, 50001, WS_DTYPE_F32, 512},
+        {512, 131072, WS_DTYPE_BF16, 512},  {512, 65536, WS_DTYPE_F32, 512},
+        {512, 131073, WS_DTYPE_BF16, 1024}, {300, 65537, WS_DTYPE_F32, 1024},
+        {257, 200003, WS_DTYPE_F16, 1024},  {513, 65536, WS_DTYPE_BF16, 512},
+        {513, 65537, WS_DTYPE_BF16, 1024},  {1024, 131072, WS_DTYPE_BF16, 1024},
+    };
+    for (const Rule& rule : rules) {
+        ws_rows r = rows();
+        r.rows = rule.rows;
+        r.vocab = rule.vocab;
+        r.row_stride = rule.vocab;
+        r.dtype = rule.dtype;
+        CHECK(ws::plan_sample(r).threads == rule.threads);
+    }
+}
+
 static void layout() {
 #define FIELD(f) std::printf("ws_sample_args " #f " %zu\n", offsetof(ws_sample_args, f))
     std::printf("ws_sample_args sizeof %zu\n", sizeof(ws_sample_args));
@@ -176,6 +198,7 @@ int main(int argc, char** argv) {
     test_arguments();
     test_buffers_lie_apart();
     test_plans();
+    test_threads();
     std::printf("%d failures\n", failures);
     return failures != 0;
 }

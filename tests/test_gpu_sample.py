@@ -252,6 +252,18 @@ def test_sample_batches(gpu_lib, rows, V):
               min_p=rng.choice([0, 0, 0.05, 0.1], rows))
 
 
+@pytest.mark.parametrize("rows,V,dtype", [(257, 131072, "bf16"), (257, 131073, "bf16"), (300, 65537, "f32")])
+def test_sample_rows_in_two_turns(gpu_lib, rows, V, dtype):
+    """More rows than CUs on both sides of the border between 512 and 1,024 threads a
+    row, undecided ones among them."""
+    rng = np.random.default_rng(V)
+    z = logits(rng, rows, V)
+    kinds = np.arange(rows) % 4
+    given = dict(temperature=0.9, top_k=np.choose(kinds, [0, 50, 0, 700]),
+                 top_p=np.choose(kinds, [1.0, 0.9, 0.8, 0.95]), min_p=np.choose(kinds, [0.0, 0.0, 0.0, 1e-3]))
+    check(z, rng.random(rows), dtype, **given)
+
+
 @pytest.mark.parametrize("rows", [257, 512, 513, 1023, 1024, 1025, 2600])
 def test_sample_rows_in_any_order(gpu_lib, rows):
     """More rows than workgroups at work at a time, which take them in an order of
