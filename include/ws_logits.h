@@ -242,9 +242,10 @@ int ws_distill_grad(const ws_rows *rows, const ws_distill_grad_args *args, void 
  * for every row.
  *
  * w and its sums are FP64 (a token is a whole number: with sums in FP32 one draw
- * in a hundred from a large vocabulary would be another token), or, where tokens
- * are counted by their values, in whole steps of V 2^-62; a w below e^-200 counts
- * as 0.
+ * in a hundred from a large vocabulary would be another token), each w to 2e-13 of
+ * itself, or, where tokens are counted by their values, in whole steps of V 2^-62; a
+ * w below e^-200 counts as 0.  So a token may differ from the formulas' where u, or
+ * the cut by p, lies that near a border between two tokens.
  *
  * A row that holds a NaN or +inf has token -1 and logprob NaN, and so has one
  * whose settings lie outside their ranges (tau 0 or WS_MIN_TEMPERATURE..

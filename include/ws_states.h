@@ -20,10 +20,11 @@
  * output may overlap an input, the workspace or another output, but where said
  * so.  The elements between a matrix's rows are not its own: an array may lie
  * there, and another matrix of the same stride in bytes (matrices of different
- * strides must lie apart, one wholly behind the other).  Calls share no state: two may run at once from any threads and streams
- * as long as neither writes what the other uses, the workspace included (two
- * captured graphs that may run at once need a workspace each).  A workspace
- * needs no initialisation and its contents do not matter between calls.
+ * strides must lie apart, one wholly behind the other).  Calls share no state:
+ * two may run at once from any threads and streams as long as neither writes
+ * what the other uses, the workspace included (two captured graphs that may run
+ * at once need a workspace each).  A workspace needs no initialisation and its
+ * contents do not matter between calls.
  *
  * Numbers: rows are FP32, FP16 or BF16.  Sums, means and deviations are FP32;
  * every output is rounded once to its type.  The same call on the same inputs
@@ -96,7 +97,9 @@ typedef struct ws_embed_grad_args {
     float          scale;         /* finite                                   */
 } ws_embed_grad_args;
 
-/* Workspace bytes of ws_embed_grad for these rows and this vocabulary. */
+/* Workspace bytes of ws_embed_grad for these rows and this vocabulary.  (Few rows
+ * are added without a sort and leave it untouched, but it is asked for all the
+ * same.) */
 int ws_embed_grad_workspace(const ws_states *states, int32_t vocab, size_t *bytes);
 
 int ws_embed_grad(const ws_states *states, const ws_embed_grad_args *args, void *stream);
@@ -109,7 +112,9 @@ int ws_embed_grad(const ws_states *states, const ws_embed_grad_args *args, void 
  * with equal strides in one buffer, each row of one in the other's padding.
  * `states` describes x. */
 typedef struct ws_norm_stats {
-    float mean;
+    float mean;      /* rounded to FP32, which ws_layernorm itself does not see:
+                        of a row whose mean is n times its deviation the
+                        gradient's u is off by up to n 2^-24                  */
     float inverse;
 } ws_norm_stats;
 

@@ -56,9 +56,10 @@ __global__ void __launch_bounds__(kLookupThreads) embed_kernel(EmbedParams p) {
 //
 // Tokens are sorted by a stable radix sort, a digit of kDigitBits a pass: every
 // tile counts its digits, and from all tiles' counts puts its tokens where they
-// belong (two tiles count all tokens for themselves, a launch less); up to kSortTile tokens are sorted by one workgroup in LDS.  (Counting a
-// pass's digits while the pass before places them saves a launch, but its atomics
-// wait behind the zeros: 16,384 tokens 27 us instead of 16.)  Then blocks of sorted
+// belong (two tiles count all tokens for themselves, a launch less); up to kSortTile
+// tokens are sorted by one workgroup in LDS.  (Counting a pass's digits while the pass
+// before places them saves a launch, but its atomics wait behind the zeros: 16,384
+// tokens 27 us instead of 16.)  Then blocks of sorted
 // rows are added, each thread its columns: a token whose rows lie in one block is
 // written at once; of a token that goes over a border each block leaves a partial
 // sum, and the block where the token begins has them added in order.  So no sum
@@ -70,12 +71,13 @@ __global__ void __launch_bounds__(kLookupThreads) embed_kernel(EmbedParams p) {
 // whose few workgroups wait on latency.
 //
 // Bytes bound it: 16,384 rows into 32,768 x 4,096 BF16, 114 us for 268 MB of zeros,
-// 134 read and 47 of sums written (4.0 TB/s): the sort with the zeros 45, the sums 58
-// (while the zeros still drain), the join 10.  Leaving out the zeros of rows that are
-// named would save 45 MB but cost as much: every clearing workgroup would read all
-// tokens first (129 us).  Sorted, 777 x 1,000 FP32 rows take 18 us: three launches, each
-// a chain of latencies (sort 7.8, sums 5.7, join 3.6); few rows go without
-// (embed_few_kernel).
+// 134 of rows and 47 of sums written (4.0 TB/s): the sort with the zeros 46, the sums 58
+// (while the zeros still drain), the join 10; added to what the table holds, without
+// zeros, 68; into FP32 183.  Leaving out the zeros of rows that are named would save
+// 45 MB; clearing workgroups that read all tokens for it cost as much (129 us), ones
+// behind the sort that search its tokens have not been tried.  Sorted, 777 x 1,000 FP32
+// rows take 18 us: three launches, each a chain of latencies (sort 7.8, sums 5.7, join
+// 3.6); few rows go without (embed_few_kernel).
 
 struct ClearParams {
     void* table;
@@ -617,7 +619,7 @@ __global__ void __launch_bounds__(kSumThreads) embed_join_kernel(SumParams p) {
 // lie side by side joined in order.  Further workgroups write zeros into the rows that
 // no token names, and read all tokens for that.  Two latencies one after the other
 // (tokens, rows) and the workgroups' turns bound it (777 x 1,000 FP32 into 5,003 rows
-// 9.7 us; with 1,024 threads a workgroup 8.8, but 13.2 instead of 7.6 for 1,000 x 64
+// 9.4 us; with 1,024 threads a workgroup 8.8, but 13.2 instead of 7.6 for 1,000 x 64
 // into 50,000, whose many clearing workgroups then wait for room).
 struct FewParams {
     SumParams sum;

@@ -36,10 +36,12 @@ struct NormParams {
 // weights stay in registers but for 1,024 threads' four 16-bit slots (8,200 BF16
 // elements: 80 us for 8,183 rows with them read again, 57 with 512 threads' three
 // slots and theirs; 32,768 elements: 105 us for 2,048 with 512 threads, 74), and each
-// element is read and written once (counted: 134.5 MB read, 134.8 written for 16,384
-// x 4,096 BF16).  HBM bounds it: 52.5 us for that, 5.1 TB/s, the rate of a large copy; three
-// passes over the row in a workgroup a row took 75.7.  64 rows take 3.9 us: a
-// launch, one row's latency and two sums over four waves.
+// element is read and written once (counted: 134.6 MB read, 134.8 written for 16,384
+// x 4,096 BF16).  HBM bounds it: 52.6 us for that, 5.1 TB/s, where a large copy runs at
+// 4.9; three passes over the row in a workgroup a row took 75.7.  (Slots read and
+// written past the caches, which carry the gradient of rows of logits to 6 TB/s, have
+// not been tried here.)  64 rows take 3.9 us: a launch, one row's latency and two sums
+// over four waves.
 // NT threads to a row; rows of less than a wave's slots lie side by side in one,
 // whose lanes would else be idle (200,000 x 256 BF16 68 us with a wave a row, 40 with
 // two rows a wave).

@@ -38,11 +38,12 @@ namespace {
 // 1,024 threads; without the mass HBM bounds it.  The rest is a chain of latencies,
 // for a best 50 of 131,072: bound 1.3 us, the few logits 2.5, sorting and drawing
 // 2.5; a nucleus of thousands takes 13 us for the histogram and 38 for the exact
-// pass.  Whole calls: 1 x 131,072 BF16 with the best 50 12.9 us (3.6 and 9.6 in the
-// two kernels), 64 x 32,768 FP16 with mixed settings 24-34 (the one undecided row's
-// nucleus), 300 x 50,001 FP32 all kept 30.7, 1,024 x 131,072 BF16 mixed 116-131 and
-// best 50 81 (3.3 TB/s).  A sort of the whole row in elementary operations takes 350
-// us for the first and 16.8 ms for the last.
+// pass.  Whole calls: 1 x 131,072 BF16 with the best 50 12.8 us (3.6 and 9.5 in the
+// two kernels), greedy 8.5, an undecided row's nucleus of 0.9 69; 64 x 32,768 FP16 with
+// mixed settings 25-35, as the inputs have an undecided row or none; 300 x 50,001 FP32
+// all kept 30.7; 1,024 x 131,072 BF16 mixed 104-136 by the inputs, best 50 78 (3.4
+// TB/s), greedy 58, all undecided nuclei 354.  A sort of the whole row in elementary
+// operations takes 350 us for the first and 16.8 ms for the mixed 1,024.
 
 struct SampleParams {
     const void* logits;
@@ -105,11 +106,14 @@ __device__ __forceinline__ void fill_table(double* table, int threads) {
 
 constexpr double kScale = 369.3299304675746;     // 256 / log 2
 
-// e^(t / kScale) for t between -700 and 130 times kScale, to 2e-13 relative: t = n +
-// r, 2 to the n / 256 from a table (LDS) and a shift of its exponent, and the series
-// of what is left (at most 1.4e-3) to the third power.  Sixteen instructions with
-// the sum, half of the exponential the library has in FP64; the draw's borders
-// between tokens lie 1e-6 apart and more.
+// e^(t / kScale) for t between -700 and 130 times kScale: t = n + r, 2 to the n / 256
+// from a table (LDS) and a shift of its exponent, and the series of what is left (at
+// most 1.4e-3) to the third power, whose next term leaves the result up to 1.4e-13
+// too small, 1.6e-13 with the rounding of t down to e^-200.  Sums of such weights and
+// their borders between tokens, as shares of the whole, are off by less than 2e-13, so
+// a draw differs from the exact one only where the uniform number is that near a
+// border: for at most V x 4e-13 of the numbers, 5e-8 at V = 131,072.  Sixteen
+// instructions with the sum, half of the exponential the library has in FP64.
 __device__ __forceinline__ double table_exp_scaled(double t, const double* table) {
     constexpr double kMagic = 6755399441055744.0;    // 1.5 x 2^52: adds to an integer
     constexpr double a1 = 0.0027076061740622863;     // log 2 / 256

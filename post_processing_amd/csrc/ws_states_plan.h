@@ -121,11 +121,14 @@ constexpr int kMostRows = kBlockRows * kSumThreads / kLeastLanes;   // of a work
 static_assert(kMostRows >= WS_MAX_ROWS / kMostGroups, "a workgroup's rows");
 constexpr int kClearRows = 16;     // of the table, by one workgroup
 // Few rows go without a sort, a workgroup a row and kSumThreads slots at most: 777 x
-// 1,000 FP32 into 5,003 rows 9.7 us, sorted 17.8; 64 x 4,096 BF16 9.7 and 18.5.  Not
-// where that makes more than kFewGroups workgroups, each of which reads all tokens
-// (512 x 16,384 BF16 27 us, sorted 23), nor where one token's rows could be more than
-// kFewBytes for one workgroup to add (1,024 x 4,096 BF16 of one token 98 us, sorted 32;
-// 777 x 1,000 FP32 34 and 25; 512 x 4,096 BF16 23 and 22).
+// 1,000 FP32 into 5,003 rows 9.5 us, sorted 17.8; 1,000 x 64 BF16 into 50,000 7.9 and
+// 17.4; 512 x 4,096 BF16 into 1,000 10.7 and 18.5, into 32,768, whose zeros are most of
+// it, 41 and 42.  Not where that makes more than kFewGroups workgroups, each of which
+// reads all tokens (512 x 16,384 BF16 27 us, sorted 23), nor where one token's rows
+// could be more than kFewBytes for one workgroup to add (1,024 x 4,096 BF16 of one token
+// 98 us, sorted 32).  Below that one token of all rows costs up to half as much again:
+// 777 x 1,000 FP32 into 5,003 36 us, sorted 26; 512 x 4,096 BF16 into 1,000 23 and 23,
+// into 32,768 66 and 50.
 constexpr int kFewRows = 1024, kFewGroups = 2048;
 constexpr int64_t kFewBytes = 2 << 20;
 

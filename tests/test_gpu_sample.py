@@ -1,12 +1,16 @@
 """Tokens drawn from rows of logits against the float64 oracle.
 
-Tokens are equal: weights and sums are FP64 on both sides, good to 1e-14 or so,
-and a draw differs only where u lies that near a border between two tokens (1e-9
-a row at the largest vocabulary here).  Where a test puts u on a border on
-purpose, the weights are whole powers of two and every sum is exact.
+Tokens are equal: weights and sums are FP64 on both sides.  The kernels' weights are
+up to 1.6e-13 too small (an exponential of a table and a cubic), so the borders
+between tokens, as shares of the whole, are off by less than 2e-13, and a draw differs
+only where u lies that near one: a chance of at most V 4e-13 a row, 8e-8 at the 200,003
+tokens of the longest drawn ones here (the row of 2^30 has its numbers chosen, and
+weights of 1 but for two).  Where a test puts u on a border on purpose, the weights are
+equal, and every sum is exact.
 
-The log probability x_t - log K: x_t and log K are FP64 (their errors below
-1e-13), rounded once to FP32: half a step, E = 2^-24 relative, and 1e-12.
+The log probability is log(w_t / K): both good to 2e-13, so their ratio's log to 4e-13
+and the logarithm's own 2e-16, rounded once to FP32: half a step, E = 2^-24 relative,
+and 1e-12.
 """
 import numpy as np
 import pytest
