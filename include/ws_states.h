@@ -30,7 +30,9 @@
  * every output is rounded once to its type.  The same call on the same inputs
  * gives the same bits (no sum's order depends on timing); another shape,
  * alignment or order of tokens may change the order of a sum.  NaN and
- * infinities go where the formulas carry them.
+ * infinities go where the formulas carry them, and so do sums that pass FP32's
+ * range: a row whose sum does (its mean need not) has a norm of NaN, one whose
+ * deviations' squares do an inverse of 0.
  *
  * Errors: as in ws.h.  Everything the host can see is checked before anything
  * is enqueued; a call with 0 rows checks its arguments and does what the

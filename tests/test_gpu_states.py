@@ -541,6 +541,25 @@ def test_norm_statistics_of_nan_and_infinity(gpu_lib, dtype, width):
         check_norm(x, dtype, weight=dtype)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("width", [4, 50, 1500, 40000])
+def test_norm_of_sums_past_the_range(gpu_lib, dtype, width):
+    """A sum that overflows makes its row NaN, squares that do an inverse of 0; the rows
+    between them are as they are alone."""
+    import torch
+    x = torch.from_numpy(np.random.default_rng(2).normal(size=(4, width))).to(_dev()).to(_type(dtype))
+    x[1] = 3e38
+    x[3] = 0.0
+    x[3, 0], x[3, 1] = 1e25, -1e25                 # a mean of 0, squares of 1e50
+    y, stats = torch.empty_like(x), torch.empty(4, 2, device=_dev())
+    run(st.LayerNorm(st.make_states(rows=4, width=width, dtype=CODE[dtype]), x, y, stats=stats))
+    assert torch.isnan(y[1]).all() and torch.isnan(stats[1, 1])
+    assert stats[3, 1] == 0 and (y[3] == 0).all()
+    clean, alone = x[[0, 2]].contiguous(), torch.empty(2, width, device=_dev(), dtype=x.dtype)
+    run(st.LayerNorm(st.make_states(rows=2, width=width, dtype=CODE[dtype]), clean, alone))
+    assert torch.equal(y[[0, 2]], alone) and torch.isfinite(stats[[0, 2]]).all()
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("width", [3, 50, 1500, 40000])
 def test_norm_grad_of_nan_and_infinity(gpu_lib, dtype, width):
